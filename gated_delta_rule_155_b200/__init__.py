@@ -7,7 +7,8 @@ load the library; the first use of an entry point does, and fails loudly when th
 library is missing — there is no CPU fallback.
 """
 
-__all__ = ["forward_chunked", "decode_step", "layer_forward", "KdaError"]
+__all__ = ["forward_chunked", "decode_step", "layer_forward", "gdr_forward", "gdr_backward", "gdr_decode",
+           "pages_fork", "pages_copy", "pages_free", "pages_compact", "KdaError"]
 
 
 def __getattr__(name):

@@ -13,6 +13,7 @@
 
 #include "../../include/kda.h"
 #include "common.cuh"
+#include "gdr.h"
 #include "internal.h"
 
 namespace {
@@ -146,6 +147,8 @@ kda_status_t layer_core(const void *q_raw, const void *k_raw, const void *v_raw,
 
 }  // namespace
 
+int *kda::device_error_word() { return error_word(); }
+
 extern "C" {
 
 const char *kda_status_string(kda_status_t s)
@@ -158,6 +161,7 @@ const char *kda_status_string(kda_status_t s)
     case KDA_ERR_CUDA: return "a CUDA runtime call failed";
     case KDA_ERR_TIMEOUT: return "a kernel's bounded wait gave up (device error word set)";
     case KDA_ERR_WORKSPACE: return "workspace missing or too small";
+    case KDA_ERR_INDEX: return "a page index is out of range, not live, or named twice (device error word set)";
     }
     return "unknown status";
 }
@@ -348,7 +352,7 @@ kda_status_t kda_check_device_error(kda_stream_t stream)
     if (word != 0) {
         const int zero = 0;
         if (cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return KDA_ERR_CUDA;
-        return KDA_ERR_TIMEOUT;
+        return word == kda::kErrPageIndex ? KDA_ERR_INDEX : KDA_ERR_TIMEOUT;
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -20,7 +20,7 @@ KDA_OK = 0
 KDA_F32, KDA_BF16 = 0, 1
 STATUS_NAMES = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED",
                 3: "KDA_ERR_MISALIGNED", 4: "KDA_ERR_CUDA", 5: "KDA_ERR_TIMEOUT",
-                6: "KDA_ERR_WORKSPACE"}
+                6: "KDA_ERR_WORKSPACE", 7: "KDA_ERR_INDEX"}
 
 
 class KdaError(RuntimeError):
@@ -62,6 +62,24 @@ def _load():
     lib.kda_layer_decode_step.argtypes = [vp] * 12 + [f] + [vp] * 3 + [f] + [vp] * 2 + [i] * 4 + [i, vp]
     lib.kda_layer_decode_step.restype = i
     lib.kda_check_device_error.argtypes = [vp]
+    lib.kda_gdr_workspace_size.restype = i
+    lib.kda_gdr_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(sz)]
+    lib.kda_gdr_forward.restype = i
+    lib.kda_gdr_forward.argtypes = [vp] * 10 + [i] + [vp] * 2 + [sz] + [i] * 6 + [i, vp]
+    lib.kda_gdr_backward.restype = i
+    lib.kda_gdr_backward.argtypes = [vp] * 16 + [sz] + [i] * 6 + [i, vp]
+    lib.kda_gdr_decode.restype = i
+    lib.kda_gdr_decode.argtypes = [vp] * 7 + [i, vp] + [i] * 6 + [i, vp]
+    lib.kda_pages_fork.restype = i
+    lib.kda_pages_fork.argtypes = [vp, sz, i, i, vp, vp, vp, i, vp]
+    lib.kda_pages_copy.restype = i
+    lib.kda_pages_copy.argtypes = [vp, sz, i, i, vp, vp, i, vp]
+    lib.kda_pages_free.restype = i
+    lib.kda_pages_free.argtypes = [vp, i, vp, i, vp]
+    lib.kda_pages_workspace_size.restype = i
+    lib.kda_pages_workspace_size.argtypes = [i, ctypes.POINTER(sz)]
+    lib.kda_pages_compact.restype = i
+    lib.kda_pages_compact.argtypes = [vp, sz, i, i, vp, vp, i, vp, vp, sz, vp]
     lib.kda_set_wait_test_hooks.restype = i
     lib.kda_set_wait_test_hooks.argtypes = [ctypes.c_ulonglong, i]
     return lib
@@ -73,7 +91,9 @@ EXPORTED_SYMBOLS = ("kda_status_string", "kda_abi_version", "kda_forward_chunked
                     "kda_decode_step", "kda_layer_workspace_size", "kda_layer_forward",
                     "kda_layer_forward_noalloc", "kda_layer_decode_step", "kda_forward_chunked_varlen",
                     "kda_backward_workspace_size", "kda_backward_chunked", "kda_layer_forward_varlen",
-                    "kda_check_device_error", "kda_set_wait_test_hooks")
+                    "kda_gdr_workspace_size", "kda_gdr_forward", "kda_gdr_backward", "kda_gdr_decode",
+                    "kda_pages_fork", "kda_pages_copy", "kda_pages_free", "kda_pages_workspace_size",
+                    "kda_pages_compact", "kda_check_device_error", "kda_set_wait_test_hooks")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 
@@ -386,8 +406,214 @@ def kda_layer_forward_noalloc(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, g_raw
     return out, final_state
 
 
+def _gdr_shapes(q, k, v, g, beta, cu_seqlens):
+    """(N, T_total, Hk, Hv, dk, dv, leading shape) of the head-gated delta rule's inputs: packed
+    [T_total, ...] with cu_seqlens, [B, T, ...] without."""
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
+        N = cu_seqlens.numel() - 1
+        _need(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens")
+        if q.dim() != 3 or v.dim() != 3:
+            raise ValueError("with cu_seqlens, q and v are [T_total, H, d]")
+        lead = (q.shape[0],)
+        Tt = q.shape[0]
+    else:
+        if q.dim() != 4 or v.dim() != 4:
+            raise ValueError("without cu_seqlens, q and v are [B, T, H, d]")
+        lead = (q.shape[0], q.shape[1])
+        N, Tt = q.shape[0], q.shape[0] * q.shape[1]
+    Hk, dk = q.shape[-2:]
+    Hv, dv = v.shape[-2:]
+    for t, s, n in ((q, lead + (Hk, dk), "q"), (k, lead + (Hk, dk), "k"), (v, lead + (Hv, dv), "v"),
+                    (g, lead + (Hv,), "g"), (beta, lead + (Hv,), "beta")):
+        _need(t, s, q.dtype, n)
+    return N, Tt, Hk, Hv, dk, dv, lead
+
+
+def _workspace(need, device):
+    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+
+
+def _ws_bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _paged_state(state, index, N, tail, name):
+    """Checks a state buffer: [N, *tail], or [pages, *tail] where an index is given.  Its pages."""
+    if state is None:
+        if index is not None:
+            raise ValueError(f"{name}_index needs {name}_state")
+        return 0
+    if index is None:
+        _need(state, (N,) + tail, torch.float32, f"{name}_state")
+        return 0
+    _need(index, (N,), torch.int32, f"{name}_index")
+    _need(state, (state.shape[0],) + tail, torch.float32, f"{name}_state")
+    return state.shape[0]
+
+
+def kda_gdr_workspace_size(N, T_total, Hk, Hv, dk, dv, dtype, *, backward=False):
+    n = ctypes.c_size_t(0)
+    _check(_lib.kda_gdr_workspace_size(N, T_total, Hk, Hv, dk, dv, _io_code(dtype), int(backward), ctypes.byref(n)),
+           "kda_gdr_workspace_size")
+    return int(n.value)
+
+
+def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=None, final_state=None, *,
+                    initial_index=None, final_index=None, workspace=None, stream=None):
+    """The gated delta rule with one gate per value head, chunked.  q, k: [T_total, Hk, dk]; v:
+    [T_total, Hv, dv]; g, beta: [T_total, Hv] (io dtype) for the sequences of cu_seqlens, or [B, T, ...]
+    without it; value head h uses key head h // (Hv // Hk).  States are fp32 [N, Hv, dk, dv], or pages
+    [P, Hv, dk, dv] with an int32 index [N] (initial: -1 starts from zeros; final: -1 is not kept; the
+    two buffers have the same number of pages).  ``workspace`` (a uint8 CUDA tensor of
+    kda_gdr_workspace_size bytes) is allocated with torch when not given.  Returns (out, final_state)."""
+    N, Tt, Hk, Hv, dk, dv, lead = _gdr_shapes(q, k, v, g, beta, cu_seqlens)
+    p0 = _paged_state(initial_state, initial_index, N, (Hv, dk, dv), "initial")
+    p1 = _paged_state(final_state, final_index, N, (Hv, dk, dv), "final")
+    if p0 and p1 and p0 != p1:
+        raise ValueError(f"initial_state has {p0} pages, final_state {p1}")
+    if out is None:
+        out = torch.empty(lead + (Hv, dv), dtype=q.dtype, device=q.device)
+    _need(out, lead + (Hv, dv), q.dtype, "out")
+    if workspace is None:
+        workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype), q.device)
+    _check(_lib.kda_gdr_forward(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(initial_index), _ptr(out),
+        _ptr(final_state), _ptr(final_index), max(p0, p1), _ptr(cu_seqlens), _ptr(workspace), _ws_bytes(workspace),
+        N, Tt, Hk, Hv, dk, dv, _io_code(q.dtype), _stream(stream)), "kda_gdr_forward")
+    return out, final_state
+
+
+def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=None, d_final_state=None, *,
+                     grads=None, d_initial_state=None, workspace=None, stream=None):
+    """Gradients of kda_gdr_forward (dense states).  Returns a dict dq, dk, dv, dg, dbeta (io dtype,
+    shaped as the inputs) and d_initial_state (fp32, None unless a buffer is passed).  ``grads`` may
+    hold preallocated outputs; ``workspace`` is allocated with torch when not given."""
+    N, Tt, Hk, Hv, dk, dv, lead = _gdr_shapes(q, k, v, g, beta, cu_seqlens)
+    _need(d_out, lead + (Hv, dv), q.dtype, "d_out")
+    for t, n in ((initial_state, "initial_state"), (d_final_state, "d_final_state"),
+                 (d_initial_state, "d_initial_state")):
+        _need(t, (N, Hv, dk, dv), torch.float32, n, allow_none=True)
+    gr = dict(grads or {})
+    for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
+        if gr.get(n) is None:
+            gr[n] = torch.empty_like(t)
+        _need(gr[n], t.shape, q.dtype, n)
+    if workspace is None:
+        workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype, backward=True), q.device)
+    _check(_lib.kda_gdr_backward(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out),
+        _ptr(d_final_state), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]), _ptr(gr["dg"]), _ptr(gr["dbeta"]),
+        _ptr(d_initial_state), _ptr(workspace), _ws_bytes(workspace), N, Tt, Hk, Hv, dk, dv, _io_code(q.dtype),
+        _stream(stream)), "kda_gdr_backward")
+    gr["d_initial_state"] = d_initial_state
+    return gr
+
+
+def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None):
+    """One or a few tokens per sequence, states updated in place.  q, k: [N, T, Hk, dk]; v: [N, T, Hv, dv];
+    g, beta: [N, T, Hv], or all without T for one token; state: fp32 [N, Hv, dk, dv], or pages
+    [P, Hv, dk, dv] with ``index`` int32 [N] (-1: an idle row, whose out is left alone).  Returns out."""
+    one = q.dim() == 3
+    if q.dim() not in (3, 4) or v.dim() != q.dim():
+        raise ValueError("q and v are [N, T, H, d], or [N, H, d] for one token")
+    lead = tuple(q.shape[:-2])
+    N, T = (lead[0], 1) if one else lead
+    Hk, dk = q.shape[-2:]
+    Hv, dv = v.shape[-2:]
+    io = q.dtype
+    for t, s, n in ((q, lead + (Hk, dk), "q"), (k, lead + (Hk, dk), "k"), (v, lead + (Hv, dv), "v"),
+                    (g, lead + (Hv,), "g"), (beta, lead + (Hv,), "beta")):
+        _need(t, s, io, n)
+    if index is None:
+        _need(state, (N, Hv, dk, dv), torch.float32, "state")
+    else:
+        _need(index, (N,), torch.int32, "index")
+        _need(state, (state.shape[0], Hv, dk, dv), torch.float32, "state")
+    if out is None:
+        out = torch.empty(lead + (Hv, dv), dtype=io, device=q.device)
+    _need(out, lead + (Hv, dv), io, "out")
+    _check(_lib.kda_gdr_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(index),
+                               state.shape[0], _ptr(out), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream)),
+           "kda_gdr_decode")
+    return out
+
+
+def _cache(cache):
+    """(layers, pages, bytes of a page) of a cache [layers, pages, ...] of any dtype."""
+    if cache.dim() < 3:
+        raise ValueError("cache must be [layers, pages, ...]")
+    _need(cache, cache.shape, cache.dtype, "cache")
+    L, P = cache.shape[:2]
+    return L, P, (cache.numel() // max(1, L * P)) * cache.element_size()
+
+
+def _ids(t, name):
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D tensor of page numbers")
+    _need(t, t.shape, torch.int32, name)
+    return t.numel()
+
+
+def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
+    """A free page for each of ``parents`` (int32 [n]), lowest first, with the parent's contents in every
+    layer of ``cache`` [L, P, ...] (zeros for -1); ``refs`` (int32 [P]) of the new pages become 1.
+    Returns their numbers, int32 [n]: -1 where no page is left or the parent is not live."""
+    L, P, nbytes = _cache(cache)
+    n = _ids(parents, "parents")
+    _need(refs, (P,), torch.int32, "refs")
+    if children is None:
+        children = torch.empty_like(parents)
+    _need(children, (n,), torch.int32, "children")
+    _check(_lib.kda_pages_fork(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(parents), _ptr(children), n, _stream(stream)),
+           "kda_pages_fork")
+    return children
+
+
+def kda_pages_copy(cache, src, dst, *, stream=None):
+    """Page dst[i] <- page src[i] in every layer of ``cache`` [L, P, ...] (src -1: zeros; dst -1: nothing)."""
+    L, P, nbytes = _cache(cache)
+    n = _ids(src, "src")
+    _need(dst, (n,), torch.int32, "dst")
+    _check(_lib.kda_pages_copy(_ptr(cache), nbytes, L, P, _ptr(src), _ptr(dst), n, _stream(stream)), "kda_pages_copy")
+
+
+def kda_pages_free(refs, ids, *, stream=None):
+    """One holder less for each page of ``ids`` (int32 [n], -1: nothing); a page is free at refs 0."""
+    n = _ids(ids, "ids")
+    P = _ids(refs, "refs")
+    _check(_lib.kda_pages_free(_ptr(refs), P, _ptr(ids), n, _stream(stream)), "kda_pages_free")
+
+
+def kda_pages_workspace_size(pages):
+    n = ctypes.c_size_t(0)
+    _check(_lib.kda_pages_workspace_size(pages, ctypes.byref(n)), "kda_pages_workspace_size")
+    return int(n.value)
+
+
+def kda_pages_compact(cache, refs, table=None, live=None, *, workspace=None, stream=None):
+    """Moves the live pages of ``cache`` [L, P, ...] to the lowest numbers, ``refs`` (int32 [P]) with them,
+    and renumbers ``table`` (int32, any page numbers, -1 stays) in place.  Returns their count, int32 [1]."""
+    L, P, nbytes = _cache(cache)
+    _need(refs, (P,), torch.int32, "refs")
+    n = 0
+    if table is not None:
+        _need(table, table.shape, torch.int32, "table")
+        n = table.numel()
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=cache.device)
+    _need(live, (1,), torch.int32, "live")
+    if workspace is None:
+        workspace = _workspace(kda_pages_workspace_size(P), cache.device)
+    _check(_lib.kda_pages_compact(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(table), n, _ptr(live), _ptr(workspace),
+                                  _ws_bytes(workspace), _stream(stream)), "kda_pages_compact")
+    return live
+
+
 def kda_check_device_error(stream=None):
-    """Synchronise the stream and raise if a kernel flagged a bounded-wait timeout or CUDA error."""
+    """Synchronise the stream and raise if a kernel flagged a bounded-wait timeout, a bad page index or a
+    CUDA error."""
     _check(_lib.kda_check_device_error(_stream(stream)), "kda_check_device_error")
 
 
@@ -403,5 +629,12 @@ forward_chunked_varlen = kda_forward_chunked_varlen
 backward_chunked = kda_backward_chunked
 decode_step = kda_decode_step
 layer_forward = kda_layer_forward
+gdr_forward = kda_gdr_forward
+gdr_backward = kda_gdr_backward
+gdr_decode = kda_gdr_decode
+pages_fork = kda_pages_fork
+pages_copy = kda_pages_copy
+pages_free = kda_pages_free
+pages_compact = kda_pages_compact
 layer_workspace_size = kda_layer_workspace_size
 check_device_error = kda_check_device_error

@@ -21,6 +21,11 @@
  *                                _varlen variants
  *   kda_layer_decode_step        one decode step of the layer core with a conv cache
  *   kda_backward_chunked         gradients of the recurrence's inputs
+ *   kda_gdr_forward              the recurrence with one gate per value head and value heads
+ *                                that share key heads; states dense or in cache pages
+ *   kda_gdr_backward             its gradients
+ *   kda_gdr_decode               the same for one or a few tokens a sequence, on cache pages
+ *   kda_pages_fork, _copy, _free, _compact   pages of a state cache
  *   kda_*_workspace_size, kda_check_device_error, kda_status_string, kda_abi_version
  *   kda_set_wait_test_hooks      wait limit and failure injection for the failure path
  *
@@ -59,7 +64,8 @@ typedef enum {
     KDA_ERR_MISALIGNED = 3,   /* a tensor pointer is not 16-byte aligned              */
     KDA_ERR_CUDA = 4,         /* a CUDA runtime call failed (launch, attribute, ...)  */
     KDA_ERR_TIMEOUT = 5,      /* a kernel's bounded wait gave up (device error word)  */
-    KDA_ERR_WORKSPACE = 6     /* workspace missing or smaller than required           */
+    KDA_ERR_WORKSPACE = 6,    /* workspace missing or smaller than required           */
+    KDA_ERR_INDEX = 7         /* a page index out of range, not live, or named twice  */
 } kda_status_t;
 
 typedef enum {
@@ -292,6 +298,129 @@ kda_status_t kda_layer_decode_step(const void *q_raw, const void *k_raw, const v
                                    kda_dtype_t io, kda_stream_t stream);
 
 /*
+ * ---- The gated delta rule with one gate per value head and grouped heads ("gdr") ----
+ *
+ * Hv value heads share Hk key heads (Hv a multiple of Hk): value head h reads q and k of key
+ * head h / (Hv / Hk).  Per value head, with a dk x dv fp32 state S and, per token, a
+ * log-decay g (one number, expected <= 0) and a strength beta in [0, 1]:
+ *     S' = exp(g) S;   u = beta (v - S'^T k);   S <- S' + k u^T;   o = S^T q
+ *   q, k       [T_total, Hk, dk]  io dtype     v, out  [T_total, Hv, dv]  io dtype
+ *   g, beta    [T_total, Hv]      io dtype     states  [.., Hv, dk, dv]   fp32
+ *   cu_seqlens [N + 1] int32 device offsets of N packed sequences, as
+ *              kda_forward_chunked_varlen; or NULL for N sequences of T_total / N tokens each
+ *              (T_total a multiple of N).
+ * Any head counts, dk and dv in {64, 128} (all four pairs), both io dtypes.  bf16 at
+ * dk = dv = 128 runs on tcgen05 kernels (KDA_ERR_UNSUPPORTED where they cannot run); its
+ * products read the state, its corrections and their gradients as bf16 hi + lo pairs with
+ * fp32 sums, so states and out carry about 2^-16 relative error before out's own rounding.
+ * The other shapes run exact fp32 CUDA-core kernels.  A g below -128 (-inf among them) acts as
+ * a full reset, which exp(g) = 0 is; NaN inputs reach their own head's values and no other's.
+ */
+
+/*
+ * Bytes of device workspace of kda_gdr_forward (backward = 0) or kda_gdr_backward
+ * (backward = 1): per 64-token chunk and value head, the chunk's matrices M and P M (32 KiB),
+ * and for the backward pass also the chunk's states, corrections and their gradients.  A call
+ * needs it only while it runs; calls that overlap on the GPU need one each (two captured
+ * graphs that may run at once among them).
+ */
+kda_status_t kda_gdr_workspace_size(int N, int T_total, int Hk, int Hv, int dk, int dv, kda_dtype_t io,
+                                    int backward, size_t *bytes);
+
+/*
+ * kda_gdr_forward — outputs and final states of N sequences.
+ *   initial_state  [N, Hv, dk, dv] fp32, or with initial_index [pages, Hv, dk, dv]; NULL: zeros
+ *   initial_index  [N] int32 device: the page each sequence starts from, -1 for zeros; several
+ *                  sequences may start from one page.  NULL: sequence n starts from page n.
+ *   final_state    as initial_state (may be the same buffer), NULL: not kept
+ *   final_index    [N] int32 device: the page each final state goes to, -1: not kept; NULL: n.
+ *                  Pages that no sequence names are left as they were.
+ *   pages          pages of the two buffers, where an index is given (else ignored)
+ *   out            written at every token of the N sequences; rows behind the last are left alone
+ *   workspace      kda_gdr_workspace_size(.., 0) bytes, 256-byte aligned
+ * Index values are checked on the device: an index out of range counts as -1; of sequences with
+ * the same final page the first keeps its state there, and a final page that another sequence
+ * starts from (in the same buffer) is not written.  Each sets the device error word
+ * (KDA_ERR_INDEX from kda_check_device_error).  A sequence of length 0 passes its state through.
+ */
+kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                             const float *initial_state, const int *initial_index, void *out, float *final_state,
+                             const int *final_index, int pages, const int *cu_seqlens, void *workspace,
+                             size_t workspace_bytes, int N, int T_total, int Hk, int Hv, int dk, int dv,
+                             kda_dtype_t io, kda_stream_t stream);
+
+/*
+ * kda_gdr_backward — gradients of kda_gdr_forward's inputs, given d_out = dL/d out and
+ * d_final_state = dL/d final_state (dense [N, Hv, dk, dv] fp32, or NULL for zeros).  The
+ * forward pass is recomputed from the inputs; nothing of it need be kept.
+ *   initial_state   [N, Hv, dk, dv] fp32 or NULL (zeros)
+ *   d_q, d_k        [T_total, Hk, dk] io dtype (written; summed over the value heads of the group)
+ *   d_v             [T_total, Hv, dv] io dtype (written)     d_g, d_beta  [T_total, Hv] io dtype (written)
+ *   d_initial_state [N, Hv, dk, dv] fp32 (written) or NULL; may be d_final_state
+ *   workspace       kda_gdr_workspace_size(.., 1) bytes, 256-byte aligned
+ * No atomics: the same inputs give the same bits.
+ */
+kda_status_t kda_gdr_backward(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                              const float *initial_state, const int *cu_seqlens, const void *d_out,
+                              const float *d_final_state, void *d_q, void *d_k, void *d_v, void *d_g, void *d_beta,
+                              float *d_initial_state, void *workspace, size_t workspace_bytes, int N, int T_total,
+                              int Hk, int Hv, int dk, int dv, kda_dtype_t io, kda_stream_t stream);
+
+/*
+ * kda_gdr_decode — T >= 1 tokens of N sequences, token by token, states updated in place (read
+ * and written once per call, whatever T).
+ *   q, k [N, T, Hk, dk]; v, out [N, T, Hv, dv]; g, beta [N, T, Hv], io dtype
+ *   state [N, Hv, dk, dv] fp32, or with index [pages, Hv, dk, dv]
+ *   index [N] int32 device: each sequence's page; -1: an idle row, whose out is left alone.  A
+ *         page out of range, or one that an earlier row names, makes its row idle and sets the
+ *         device error word (KDA_ERR_INDEX).  NULL: sequence n's state is n.
+ * Exact fp32 arithmetic in every dtype.  dk, dv in {64, 128}.
+ */
+kda_status_t kda_gdr_decode(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                            float *state, const int *index, int pages, void *out, int N, int T, int Hk, int Hv,
+                            int dk, int dv, kda_dtype_t io, kda_stream_t stream);
+
+/*
+ * ---- Pages of a state cache ----
+ *
+ * cache is [layers, pages, page_bytes] of any contents (the states of kda_gdr_decode, or of
+ * kda_decode_step with one page a sequence), page_bytes a multiple of 16; refs [pages] int32
+ * (device) counts the holders of each page, 0 for a free one.  Everything is decided on the
+ * device, so every call can be captured in a graph; bad indices are left out and set the
+ * device error word (KDA_ERR_INDEX).
+ *
+ * kda_pages_fork: for each i < n a free page, lowest first, with the contents of page
+ * parents[i] in every layer (zeros for parents[i] = -1); children[i] receives its number and its
+ * refs becomes 1.  children[i] = -1 where parents[i] is not a live page (its free page stays
+ * free), and, without an error, where no free page is left.
+ */
+kda_status_t kda_pages_fork(void *cache, size_t page_bytes, int layers, int pages, int *refs, const int *parents,
+                            int *children, int n, kda_stream_t stream);
+
+/*
+ * kda_pages_copy: page dst[i] <- page src[i] in every layer (zeros for src[i] = -1; dst[i] = -1:
+ * nothing).  A pair is left out, with the error word set, where an index is out of range, where
+ * an earlier pair has the same destination, or where its source is another pair's destination.
+ */
+kda_status_t kda_pages_copy(void *cache, size_t page_bytes, int layers, int pages, const int *src, const int *dst,
+                            int n, kda_stream_t stream);
+
+/* kda_pages_free: refs[ids[i]] -= 1 (-1: nothing).  A page that nobody holds is left at 0. */
+kda_status_t kda_pages_free(int *refs, int pages, const int *ids, int n, kda_stream_t stream);
+
+/* Bytes of device workspace of kda_pages_compact (at most 8 (pages + 1)). */
+kda_status_t kda_pages_workspace_size(int pages, size_t *bytes);
+
+/*
+ * kda_pages_compact: moves the m live pages to pages 0 .. m - 1.  Live pages below m stay; the
+ * k-th live page at or above m moves to the k-th free page below it, its refs with it.  table
+ * [n] int32 (NULL with n = 0) holds page numbers and is renumbered in place (-1 stays; a number
+ * of no live page becomes -1 and sets the error word).  live [1] int32 or NULL receives m.
+ */
+kda_status_t kda_pages_compact(void *cache, size_t page_bytes, int layers, int pages, int *refs, int *table, int n,
+                               int *live, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
  * kda_set_wait_test_hooks — the failure path of the tensor-core kernels, made testable
  * without a GPU fault.  Those kernels wait on their own mbarriers (tile loads, MMA
  * completion) with a time limit; a wait that runs out sets the device error word, makes
@@ -312,7 +441,7 @@ kda_status_t kda_set_wait_test_hooks(unsigned long long wait_limit_ns, int skip_
 /*
  * Synchronises `stream`, then reports and clears the library's device error word
  * (set by a kernel whose bounded wait gave up) and any sticky CUDA error.
- * Returns KDA_OK, KDA_ERR_TIMEOUT or KDA_ERR_CUDA.
+ * Returns KDA_OK, KDA_ERR_TIMEOUT, KDA_ERR_INDEX or KDA_ERR_CUDA.
  */
 kda_status_t kda_check_device_error(kda_stream_t stream);
 

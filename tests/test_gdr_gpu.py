@@ -1,0 +1,583 @@
+"""The head-gated delta rule and the state cache's pages on the GPU, against the 64-bit reference.
+
+Tolerances (e = the reference, in 64 bits, from the values that the GPU reads):
+  * a value stored in bf16 is off by at most half a step, 2^-8 |e|, by that rounding alone.
+  * fp32 kernels: sums of at most 128 products, each step at most 2^-24 relative to the sum of its terms'
+    absolute values, through three products a chunk: about 3 * 128 * 2^-24 = 2^-15.4 of the largest value
+    in the worst case.  Bound: 2^-14 of the largest |e| of the tensor.
+  * bf16 at dk = dv = 128: every operand that is not exact in bf16 is a hi + lo pair, off by at most 2^-17
+    relative (hi by 2^-8, lo by 2^-9 of that), and the product of the lo parts is left out (2^-16); three
+    products a chunk: about 3 * 2^-15 of the largest value at worst.  Bound: 2^-13 of the largest |e| for
+    states and, on top of the bf16 rounding, for outputs and dv.  The gradients of q, k, g and beta read
+    states and corrections rounded once to bf16: four roundings of 2^-8 relative to their terms, which are
+    independent, so their 2-norm is at most 2^-8 of the gradient's beside the output's own; bound 2^-7 of
+    the 2-norm, and 2^-4 of the rms on top of 2^-8 |e| for one element (the largest of 10^5 such errors is
+    within 5 of their rms of 2^-8 rms sqrt(4), times two for terms that cancel).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdr
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def kda():
+    from gated_delta_rule_155_b200 import build
+
+    build.build()
+    from gated_delta_rule_155_b200 import kda as k
+
+    return k
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(T, Hk, Hv, dk, dv, io, seed, N=1, gate=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True).clamp_min(1e-6)  # noqa: E731
+    silu = torch.nn.functional.silu
+    d = dict(q=unit(silu(rn(T, Hk, dk))), k=unit(silu(rn(T, Hk, dk))), v=silu(rn(T, Hv, dv)),
+             g=-gate * torch.nn.functional.softplus(rn(T, Hv) - 2.0), beta=torch.sigmoid(rn(T, Hv)))
+    d = {n: x.to(DT[io]) for n, x in d.items()}
+    d["s0"] = 0.3 * rn(N, Hv, dk, dv)
+    d["dS"] = 0.3 * rn(N, Hv, dk, dv)
+    d["dO"] = rn(T, Hv, dv).to(DT[io])
+    return d
+
+
+def cu_of(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def to(d, *names):
+    return [d[n].cuda() for n in names]
+
+
+NAMES = ("q", "k", "v", "g", "beta")
+
+
+def tc(io, dk, dv):
+    return io == "bf16" and dk == dv == 128
+
+
+def near(got, ref, io, exact_path, what, stored=True):
+    got, ref = (f64(got) if isinstance(got, torch.Tensor) else got), np.asarray(ref)
+    assert np.isfinite(got).all(), what
+    if not ref.size:
+        return
+    bound = (2.0 ** -14 if exact_path else 2.0 ** -13) * max(np.abs(ref).max(), 1e-30)
+    if stored and io == "bf16":
+        bound = bound + 2.0 ** -8 * np.abs(ref)
+    off = np.abs(got - ref)
+    assert (off <= bound).all(), f"{what}: off by {off.max():.3g}, {np.max(off / bound):.2f} of the bound"
+
+
+def near_grad(got, ref, io, exact_path, what):
+    if exact_path:
+        return near(got, ref, io, True, what)
+    got, ref = f64(got), np.asarray(ref)
+    assert np.isfinite(got).all(), what
+    norm = np.linalg.norm(ref)
+    assert np.linalg.norm(got - ref) <= 2.0 ** -7 * norm + 1e-30, f"{what}: {np.linalg.norm(got - ref) / norm:.3g} of the norm"
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -4 * np.sqrt(np.mean(ref * ref)) + 1e-30
+    assert (np.abs(got - ref) <= bound).all(), f"{what}: {np.max(np.abs(got - ref) / bound):.2f} of the bound"
+
+
+SHAPES = [  # lens, Hk, Hv, dk, dv
+    ([1], 1, 1, 128, 128),
+    ([64], 2, 4, 128, 128),
+    ([130, 0, 1, 63, 65], 2, 6, 128, 128),
+    ([257], 3, 3, 128, 128),
+    ([17, 100], 1, 4, 64, 64),
+    ([70, 1], 2, 2, 64, 128),
+    ([70, 66], 2, 4, 128, 64),
+]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("state", [False, True])
+def test_forward(kda, io, shape, state):
+    lens, Hk, Hv, dk, dv = shape
+    N, cu = len(lens), cu_of(lens)
+    d = make(cu[-1], Hk, Hv, dk, dv, io, 3, N)
+    s0 = d["s0"] if state else None
+    sT = torch.empty(N, Hv, dk, dv, device="cuda")
+    out, _ = kda.kda_gdr_forward(*to(d, *NAMES), torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                 None if s0 is None else s0.cuda(), final_state=sT)
+    kda.kda_check_device_error()
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), cu, None if s0 is None else f64(s0))
+    ex = not tc(io, dk, dv)
+    near(out, ro, io, ex, "out")
+    near(sT, rs, io, ex, "final state", stored=False)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("state", [False, True])
+def test_backward(kda, io, shape, state):
+    lens, Hk, Hv, dk, dv = shape
+    N, cu = len(lens), cu_of(lens)
+    d = make(cu[-1], Hk, Hv, dk, dv, io, 4, N)
+    s0, dS = (d["s0"], d["dS"]) if state else (None, None)
+    d0 = torch.empty(N, Hv, dk, dv, device="cuda")
+    cug = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    args = (*to(d, *NAMES, "dO"), cug, None if s0 is None else s0.cuda(), None if dS is None else dS.cuda())
+    gr = kda.kda_gdr_backward(*args, d_initial_state=d0)
+    kda.kda_check_device_error()
+    ref = gdr.backward(*(f64(d[n]) for n in NAMES), cu, f64(d["dO"]), None if s0 is None else f64(s0),
+                       None if dS is None else f64(dS))
+    ex = not tc(io, dk, dv)
+    near(gr["d_initial_state"], ref["d_initial_state"], io, ex, "d_initial_state", stored=False)
+    near(gr["dv"], ref["dv"], io, ex, "dv")
+    for n in ("dq", "dk", "dg", "dbeta"):
+        near_grad(gr[n], ref[n], io, ex, n)
+    again = kda.kda_gdr_backward(*args, d_initial_state=torch.empty_like(d0))
+    for n in gr:
+        assert torch.equal(gr[n], again[n]), f"{n} differs between two runs"
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_long_memory(kda, io, dk):
+    """Slow decays over many chunks: errors add up, sums of gates reach far."""
+    d = make(1500, 1, 2, dk, dk, io, 5, gate=0.02)
+    sT = torch.empty(1, 2, dk, dk, device="cuda")
+    out, _ = kda.kda_gdr_forward(*(x[None] for x in to(d, *NAMES)), None, d["s0"].cuda(), final_state=sT)
+    kda.kda_check_device_error()
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), [0, 1500], f64(d["s0"]))
+    near(out[0], ro, io, io == "f32", "out")
+    near(sT, rs, io, io == "f32", "final state", stored=False)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("case", ["reset", "frozen", "no write", "same key", "strong"])
+def test_edges(kda, io, dk, case):
+    T, Hk, Hv = 150, 1, 2
+    d = make(T, Hk, Hv, dk, dk, io, 6)
+    if case == "reset":
+        d["g"][[0, 5, 63, 64, 100]] = -float("inf")
+        d["g"][7] = -1e30
+    elif case == "frozen":
+        d["g"].zero_()
+        d["beta"].fill_(1.0)
+    elif case == "no write":
+        d["beta"][10:90] = 0.0
+    elif case == "same key":
+        d["k"][:] = d["k"][:1].clone()
+        d["beta"].fill_(1.0)
+    else:
+        d["g"].fill_(-60.0)
+    sT = torch.empty(1, Hv, dk, dk, device="cuda")
+    x = [t[None] for t in to(d, *NAMES)]
+    out, _ = kda.kda_gdr_forward(*x, None, d["s0"].cuda(), final_state=sT)
+    gr = kda.kda_gdr_backward(*x, d["dO"].cuda()[None], None, d["s0"].cuda(), d["dS"].cuda(),
+                              d_initial_state=torch.empty_like(sT))
+    kda.kda_check_device_error()
+    a = [f64(d[n]) for n in NAMES]
+    ro, rs = gdr.forward(*a, [0, T], f64(d["s0"]))
+    ex = io == "f32"
+    near(out[0], ro, io, ex, "out")
+    near(sT, rs, io, ex, "final state", stored=False)
+    ref = gdr.backward(*a, [0, T], f64(d["dO"]), f64(d["s0"]), f64(d["dS"]))
+    near(gr["d_initial_state"], ref["d_initial_state"], io, ex, "d_initial_state", stored=False)
+    near(gr["dv"][0], ref["dv"], io, ex, "dv")
+    for n in ("dq", "dk", "dbeta"):
+        near_grad(gr[n][0], ref[n], io, ex, n)
+    near_grad(gr["dg"][0], ref["dg"], io, ex, "dg")
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_neighbours_and_rows_behind(kda, io, dk):
+    """NaN and infinities of one sequence reach no other; tokens behind the last sequence are left alone."""
+    lens, Hk, Hv = [70, 40, 100], 1, 2
+    cu = cu_of(lens)
+    T = cu[-1] + 30
+    d = make(T, Hk, Hv, dk, dk, io, 7, 3)
+    clean = {n: f64(d[n]) for n in NAMES + ("dO",)}
+    for n in NAMES + ("dO",):
+        d[n][70:110] = float("nan")
+        d[n][cu[-1]:] = float("inf")
+    cug = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out = torch.full((T, Hv, dk), 7.0, dtype=DT[io], device="cuda")
+    sT = torch.empty(3, Hv, dk, dk, device="cuda")
+    kda.kda_gdr_forward(*to(d, *NAMES), cug, d["s0"].cuda(), out, sT)
+    grads = {n: torch.full_like(d[m], 7.0).cuda() for n, m in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"),
+                                                               ("dbeta", "beta"))}
+    kda.kda_gdr_backward(*to(d, *NAMES, "dO"), cug, d["s0"].cuda(), d["dS"].cuda(), grads=grads)
+    kda.kda_check_device_error()
+    ro, rs = gdr.forward(*(clean[n] for n in NAMES), cu, f64(d["s0"]))
+    ref = gdr.backward(*(clean[n] for n in NAMES), cu, clean["dO"], f64(d["s0"]), f64(d["dS"]))
+    ex = io == "f32"
+    for lo, hi in ((0, 70), (110, 210)):
+        near(out[lo:hi], ro[lo:hi], io, ex, "out")
+        for n in grads:
+            near_grad(grads[n][lo:hi], ref[n][lo:hi], io, ex, n)
+    near(sT[[0, 2]], rs[[0, 2]], io, ex, "final state", stored=False)
+    for t in (out, *grads.values()):
+        assert bool((t[cu[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_pages_of_states(kda, io, dk):
+    """Initial and final states on pages: shared starts, a new sequence, a state that is not kept."""
+    lens, Hk, Hv, P = [70, 5, 64, 0, 33], 1, 2, 9
+    cu = cu_of(lens)
+    d = make(cu[-1], Hk, Hv, dk, dk, io, 8, P)
+    start, end = [3, 3, -1, 7, 8], [1, 0, 5, 2, -1]
+    pages = d["s0"].cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, _ = kda.kda_gdr_forward(*to(d, *NAMES), i32(cu), pages, final_state=pages, initial_index=i32(start),
+                                 final_index=i32(end))
+    kda.kda_check_device_error()
+    s0 = np.stack([f64(d["s0"])[p] if p >= 0 else np.zeros((Hv, dk, dk)) for p in start])
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), cu, s0)
+    want = f64(d["s0"]).copy()
+    for n, p in enumerate(end):
+        if p >= 0:
+            want[p] = rs[n]
+    ex = io == "f32"
+    near(out, ro, io, ex, "out")
+    near(pages, want, io, ex, "pages", stored=False)
+    untouched = [3, 4, 6, 7, 8]
+    assert torch.equal(pages[untouched].cpu(), d["s0"][untouched])
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_bad_state_pages_are_refused(kda, io, dk):
+    lens, Hk, Hv, P = [20, 20, 20, 20], 1, 1, 5
+    cu = cu_of(lens)
+    d = make(cu[-1], Hk, Hv, dk, dk, io, 9, P)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def call(start, end):
+        pages = d["s0"].cuda()
+        kda.kda_gdr_forward(*to(d, *NAMES), i32(cu), pages, final_state=pages, initial_index=i32(start), final_index=i32(end))
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_check_device_error()
+        assert e.value.status == 7
+        kda.kda_check_device_error()      # the word was cleared
+        return pages.cpu()
+
+    pages = call([0, 1, 2, 3], [0, 0, 5, -1])      # named twice; out of range
+    assert torch.equal(pages[1:], d["s0"][1:]) and not torch.equal(pages[0], d["s0"][0])
+    pages = call([0, 1, 2, 3], [1, -1, 4, -1])     # page 1 is where sequence 1 starts
+    assert torch.equal(pages[:4], d["s0"][:4]) and not torch.equal(pages[4], d["s0"][4])
+    pages = call([9, -1, -1, -1], [0, -1, -1, -1])  # a start out of range counts as zeros
+    _, rs = gdr.forward(*(f64(d[n]) for n in NAMES), cu)
+    near(pages[0], rs[0], io, io == "f32", "state", stored=False)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("N,T,Hk,Hv,dk,dv", [(1, 1, 1, 1, 128, 128), (3, 1, 2, 4, 128, 128), (5, 3, 1, 3, 128, 128),
+                                             (4, 1, 2, 2, 64, 64), (2, 4, 1, 2, 64, 128), (2, 2, 1, 2, 128, 64),
+                                             (90, 1, 2, 8, 128, 128)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_decode(kda, io, N, T, Hk, Hv, dk, dv, paged):
+    P = N + 3 if paged else N
+    d = make(N * T, Hk, Hv, dk, dv, io, 10, P)
+    x = {n: d[n].view(N, T, *d[n].shape[1:]) for n in NAMES}
+    index = None
+    if paged:
+        index = torch.randperm(P, generator=torch.Generator().manual_seed(1))[:N].to(torch.int32)
+        if N > 2:
+            index[1] = -1
+    state = d["s0"].cuda()
+    out = torch.full((N, T, Hv, dv), 7.0, dtype=DT[io], device="cuda")
+    kda.kda_gdr_decode(*(x[n].cuda() for n in NAMES), state, None if index is None else index.cuda(), out)
+    kda.kda_check_device_error()
+    ro, rs = gdr.decode(*(f64(x[n]) for n in NAMES), f64(d["s0"]), None if index is None else index.tolist())
+    rows = [n for n in range(N) if index is None or index[n] >= 0]
+    near(out[rows], ro[rows], io, True, "out")
+    near(state, rs, io, True, "state", stored=False)
+    if paged:
+        rest = [p for p in range(P) if p not in index.tolist()]
+        assert torch.equal(state[rest].cpu(), d["s0"][rest])
+        assert all(bool((out[n] == 7.0).all()) for n in range(N) if n not in rows)
+
+
+def test_decode_without_a_token_axis_and_bad_pages(kda):
+    N, Hv, dk = 4, 2, 128
+    d = make(N, 1, Hv, dk, dk, "bf16", 11, 4)
+    state = d["s0"].cuda()
+    out = torch.full((N, Hv, dk), 7.0, dtype=torch.bfloat16, device="cuda")
+    index = torch.tensor([2, 2, 4, 0], dtype=torch.int32)     # named twice; out of range
+    kda.kda_gdr_decode(*to(d, *NAMES), state, index.cuda(), out)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_check_device_error()
+    assert e.value.status == 7
+    ro, rs = gdr.decode(*(f64(d[n])[:, None] for n in NAMES), f64(d["s0"]), index.tolist())
+    near(out[[0, 3]], ro[[0, 3], 0], "bf16", True, "out")
+    near(state, rs, "bf16", True, "state", stored=False)
+    assert bool((out[1:3] == 7.0).all())
+
+
+@pytest.mark.parametrize("L,P,E,dtype", [(1, 5, 4, torch.float32), (3, 40, 2052, torch.float32), (2, 9, 8192, torch.bfloat16),
+                                         (1, 3000, 8, torch.int16)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_pages_against_a_plain_model(kda, L, P, E, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    cache = torch.randint(-1000, 1000, (L, P, E), generator=gen).to(dtype)
+    refs = (torch.rand(P, generator=gen) < 0.5).to(torch.int32)
+    refs[0] = 2
+    live = refs.nonzero()[:, 0]
+    n = int((refs == 0).sum()) + (2 if seed else 0)       # with seed 1: more than there are free pages
+    parents = live[torch.randint(0, len(live), (n,), generator=gen)].to(torch.int32)
+    parents[torch.rand(n, generator=gen) < 0.3] = -1
+    c, r = cache.cuda(), refs.cuda()
+    children = kda.kda_pages_fork(c, r, parents.cuda())
+    kda.kda_check_device_error()
+    wc, wr, wch = gdr.fork(cache.float().numpy(), refs.numpy(), parents.tolist())
+    assert children.cpu().tolist() == wch.tolist() and r.cpu().tolist() == wr.tolist()
+    assert np.array_equal(c.cpu().float().numpy(), wc)
+
+    ended = torch.randperm(P, generator=gen)[: P // 2].to(torch.int32)
+    ended = torch.cat([ended[torch.from_numpy(wr)[ended.long()] > 0], torch.tensor([-1], dtype=torch.int32)])
+    kda.kda_pages_free(r, ended.cuda())
+    for p in ended.tolist():
+        if p >= 0:
+            wr[p] -= 1
+    assert r.cpu().tolist() == wr.tolist()
+
+    table = torch.from_numpy(np.flatnonzero(wr > 0).astype(np.int32))
+    table = torch.cat([table.flip(0), torch.tensor([-1], dtype=torch.int32)]).cuda()
+    before = table.cpu().numpy()
+    count = kda.kda_pages_compact(c, r, table)
+    kda.kda_check_device_error()
+    wc, wr, wt, m = gdr.compact(wc, wr, before)
+    assert int(count) == m and r.cpu().tolist() == wr.tolist() and table.cpu().tolist() == wt.tolist()
+    assert np.array_equal(c.cpu().float().numpy(), wc)
+
+    k = min(P // 2, 300)
+    perm = torch.randperm(P, generator=gen).to(torch.int32)
+    src, dst = perm[:k].clone(), perm[k:2 * k].clone()
+    if k > 2:
+        src[1] = src[0]       # one source twice
+        src[2] = -1           # zeros
+        dst[0] = -1           # nothing
+    kda.kda_pages_copy(c, src.cuda(), dst.cuda())
+    kda.kda_check_device_error()
+    wc = gdr.copy(wc, src.tolist(), dst.tolist())
+    assert np.array_equal(c.cpu().float().numpy(), wc)
+
+
+def test_bad_pages_are_left_out(kda):
+    cache = torch.arange(2 * 6 * 4, dtype=torch.float32).view(2, 6, 4)
+    refs = torch.tensor([1, 0, 1, 0, 0, 0], dtype=torch.int32)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def refused():
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_check_device_error()
+        assert e.value.status == 7
+
+    c, r = cache.cuda(), refs.cuda()
+    parents = (2, 3, -2, 6, 0, -1)                        # 3 is free, -2 and 6 are no pages
+    children = kda.kda_pages_fork(c, r, i32(*parents))
+    refused()
+    wc, wr, wch = gdr.fork(cache.numpy(), refs.numpy(), parents)
+    assert children.cpu().tolist() == wch.tolist() and r.cpu().tolist() == wr.tolist()
+    assert np.array_equal(c.cpu().numpy(), wc)
+
+    for src, dst in (((0, 1), (4, 4)), ((0, 4), (4, 5)), ((0, 1), (1, 0)), ((0, 7), (5, 1)), ((0, 2), (-3, 5))):
+        c = cache.cuda()
+        kda.kda_pages_copy(c, i32(*src), i32(*dst))
+        refused()
+        assert np.array_equal(c.cpu().numpy(), gdr.copy(cache.numpy(), src, dst)), (src, dst)
+    c = cache.cuda()
+    kda.kda_pages_copy(c, i32(3, 3), i32(3, 1))           # onto itself is nothing, and no conflict
+    kda.kda_check_device_error()
+    assert np.array_equal(c.cpu().numpy(), gdr.copy(cache.numpy(), (3, 3), (3, 1)))
+
+    r = refs.cuda()
+    kda.kda_pages_free(r, i32(0, 0, 3, 9))                # 0 twice, 3 is free, 9 is no page
+    refused()
+    assert r.cpu().tolist() == [0, 0, 1, 0, 0, 0]
+
+    c, r, table = cache.cuda(), refs.cuda(), i32(2, 5, 17, -1)
+    live = kda.kda_pages_compact(c, r, table)
+    refused()
+    assert table.cpu().tolist() == [1, -1, -1, -1] and int(live) == 2 and r.cpu().tolist() == [1, 1, 0, 0, 0, 0]
+    assert torch.equal(c[:, 1].cpu(), cache[:, 2])
+
+
+def _serve(kda, d, dec, pages, refs, io, dk, cu, draws):
+    """Prompts prefilled into new pages, forked into samples, decoded, some ended, the cache packed, decoded on."""
+    P, Hv = pages.shape[0], pages.shape[1]
+    cache = pages.view(1, P, Hv, dk, dk)
+    new = torch.full((len(cu) - 1,), -1, dtype=torch.int32, device="cuda")
+    prompt = kda.kda_pages_fork(cache, refs, new)
+    out0, _ = kda.kda_gdr_forward(*d, torch.tensor(cu, dtype=torch.int32).cuda(), pages, final_state=pages,
+                                  initial_index=new, final_index=prompt)
+    samples = kda.kda_pages_fork(cache, refs, prompt.repeat_interleave(draws))
+    out1 = kda.kda_gdr_decode(*dec[0], pages, samples)
+    ended = samples[::2].contiguous()
+    kda.kda_pages_free(refs, ended)
+    kda.kda_pages_free(refs, prompt)
+    table = samples.clone()
+    table[::2] = -1
+    live = kda.kda_pages_compact(cache, refs, table)
+    out2 = kda.kda_gdr_decode(*dec[1], pages, table, torch.zeros_like(out1[:, :1]))
+    return out0, out1, out2, table, live
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_a_serving_run(kda, io, dk):
+    lens, Hk, Hv, draws, P = [70, 1, 129], 1, 2, 3, 16
+    cu, N = cu_of(lens), len(lens) * draws
+    d = make(cu[-1], Hk, Hv, dk, dk, io, 12)
+    dec = [make(N * T, Hk, Hv, dk, dk, io, 13 + T) for T in (2, 1)]
+    dev = [[x[n].view(N, T, *x[n].shape[1:]).cuda() for n in NAMES] for x, T in zip(dec, (2, 1))]
+    pages, refs = torch.randn(P, Hv, dk, dk, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
+    refs[[1, 4]] = 1         # pages of someone else
+    other = pages[[1, 4]].clone()
+    out0, out1, out2, table, live = _serve(kda, to(d, *NAMES), dev, pages, refs, io, dk, cu, draws)
+    kda.kda_check_device_error()
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), cu)
+    ex = io == "f32"
+    near(out0, ro, io, ex, "prefill")
+    st = np.repeat(rs, draws, 0)
+    r1, st = gdr.decode(*(f64(t) for t in dev[0]), st)
+    near(out1, r1, io, ex, "decode")
+    r2, st = gdr.decode(*(f64(t) for t in dev[1]), st)
+    near(out2[1::2], r2[1::2], io, ex, "decode after packing")
+    assert bool((out2[::2] == 0).all())
+    rows = table.cpu().tolist()
+    assert int(live) == 2 + N // 2 and max(rows) < int(live) and rows[::2] == [-1] * ((N + 1) // 2)
+    near(pages[rows[1::2]], st[1::2], io, ex, "states", stored=False)
+    mine = set(rows)
+    kept = [p for p in range(int(live)) if p not in mine]
+    assert torch.equal(pages[kept], other)
+
+
+def test_a_captured_run_replays(kda):
+    """The same run captured in a graph, replayed on new inputs, beside an eager run on another stream."""
+    io, dk, lens, Hk, Hv, draws, P = "bf16", 128, [70, 1, 129], 1, 2, 3, 16
+    cu, N = cu_of(lens), len(lens) * draws
+    sets = []
+    for seed in (20, 30):
+        d = make(cu[-1], Hk, Hv, dk, dk, io, seed)
+        dec = [make(N * T, Hk, Hv, dk, dk, io, seed + T) for T in (2, 1)]
+        sets.append((to(d, *NAMES), [[x[n].view(N, T, *x[n].shape[1:]).cuda() for n in NAMES]
+                                     for x, T in zip(dec, (2, 1))]))
+    eager = []
+    for d, dec in sets:
+        pages, refs = torch.zeros(P, Hv, dk, dk, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            eager.append([t.clone() for t in _serve(kda, d, dec, pages, refs, io, dk, cu, draws)] + [pages])
+        torch.cuda.current_stream().wait_stream(s)
+    d, dec = [x.clone() for x in sets[0][0]], [[x.clone() for x in y] for y in sets[0][1]]
+    pages, refs = torch.zeros(P, Hv, dk, dk, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
+    cug = torch.tensor(cu, dtype=torch.int32).cuda()
+    new = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+
+    def body():
+        cache = pages.view(1, P, Hv, dk, dk)
+        prompt = kda.kda_pages_fork(cache, refs, new)
+        out0, _ = kda.kda_gdr_forward(*d, cug, pages, final_state=pages, initial_index=new, final_index=prompt)
+        samples = kda.kda_pages_fork(cache, refs, prompt.repeat_interleave(draws, output_size=N))
+        out1 = kda.kda_gdr_decode(*dec[0], pages, samples)
+        kda.kda_pages_free(refs, samples[::2].contiguous())
+        kda.kda_pages_free(refs, prompt)
+        table = samples.clone()
+        table[::2] = -1
+        live = kda.kda_pages_compact(cache, refs, table)
+        out2 = kda.kda_gdr_decode(*dec[1], pages, table, torch.zeros_like(out1[:, :1]))
+        return out0, out1, out2, table, live
+
+    body()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = body()
+    for i in (0, 1, 0):
+        for a, b in zip(d, sets[i][0]):
+            a.copy_(b)
+        for x, y in zip(dec, sets[i][1]):
+            for a, b in zip(x, y):
+                a.copy_(b)
+        pages.zero_()
+        refs.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*got, pages), eager[i]):
+            assert torch.equal(a, b)
+    kda.kda_check_device_error()
+
+
+def test_backward_captured_beside_an_eager_one(kda):
+    d = make(150, 2, 4, 128, 128, "bf16", 40)
+    x = [t[None].contiguous() for t in to(d, *NAMES, "dO")]
+    eager = kda.kda_gdr_backward(*x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kda.kda_gdr_backward(*x)
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(got[n], eager[n])
+
+
+def test_gradients_agree_with_differences(kda):
+    """A directional difference of the fp32 forward pass: the loss is a sum of 10^4 products of rounding 2^-24
+    each, so with a step of 2^-6 the quotient is off by about 2^-24 * 10^2 / 2^-6 = 4e-4 of the products' size
+    and by the step's square (2^-12) of the third derivative; the bound is 2^-6 of the gradient's norm."""
+    d = make(100, 1, 2, 64, 64, "f32", 41)
+    x = {n: d[n][None].cuda() for n in NAMES}
+    do, s0 = d["dO"][None].cuda(), d["s0"].cuda()
+    gr = kda.kda_gdr_backward(*x.values(), do, None, s0)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def loss(y):
+        return float((kda.kda_gdr_forward(*y.values(), None, s0)[0].double() * do.double()).sum())
+
+    for n in NAMES:
+        v = torch.randn(x[n].shape, generator=gen, device="cuda")
+        v = v / v.norm()
+        step = 2.0 ** -6
+        lo, hi = ({**x, n: x[n] + s * step * v} for s in (-1, 1))
+        num, ana = (loss(hi) - loss(lo)) / (2 * step), float((gr["d" + n].double() * v.double()).sum())
+        assert abs(num - ana) <= 2.0 ** -6 * float(gr["d" + n].double().norm()), (n, num, ana)
+
+
+def test_binding_checks(kda):
+    d = make(10, 1, 2, 64, 64, "f32", 42)
+    x = to(d, *NAMES)
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        kda.kda_gdr_forward(*x)                                   # packed inputs without cu_seqlens
+    with pytest.raises(ValueError):
+        kda.kda_gdr_forward(x[0], x[1], x[2], x[3].bfloat16(), x[4], cu)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_forward(x[0].transpose(0, 2).contiguous().transpose(0, 2), *x[1:], cu)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_forward(*x, cu, initial_index=cu[:1])         # an index without its pages
+    with pytest.raises(ValueError):
+        kda.kda_gdr_decode(*x, d["s0"].cuda(), cu)                # index of another length
+    with pytest.raises(ValueError):
+        kda.kda_pages_fork(torch.zeros(2, 3, 4, device="cuda"), cu, cu)   # refs of another length
+    with pytest.raises(kda.KdaError):
+        kda.kda_pages_fork(torch.zeros(2, 2, 3, device="cuda"), cu, cu)   # 12-byte pages
+
+
+def test_no_tokens_pass_the_state_through(kda):
+    s0 = torch.randn(2, 2, 64, 128, device="cuda")
+    z = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    x = (z(2, 0, 1, 64), z(2, 0, 1, 64), z(2, 0, 2, 128), z(2, 0, 2), z(2, 0, 2))
+    sT, d0 = torch.empty_like(s0), torch.empty_like(s0)
+    out, _ = kda.kda_gdr_forward(*x, None, s0, final_state=sT)
+    kda.kda_gdr_backward(*x, z(2, 0, 2, 128), None, s0, s0, d_initial_state=d0)
+    kda.kda_check_device_error()
+    assert out.shape == (2, 0, 2, 128) and torch.equal(sT, s0) and torch.equal(d0, s0)
