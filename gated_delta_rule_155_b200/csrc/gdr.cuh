@@ -104,8 +104,9 @@ KDA_DEVICE bool page_is_free(const int *sT_index, const int *s0_index, bool same
 
 // M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats, by 16 x 16 blocks:
 // the diagonal blocks by forward substitution (one column a thread), then block row by block row
-// M_IJ = -M_II sum_{J <= K < I} A_IK M_KJ, every product in fp32.  `tmp`: 48 rows of LD floats.
-// 256 threads; M's upper triangle is written as zeros.  Ends with a barrier.
+// M_IJ = -M_II sum_{J <= K < I} A_IK M_KJ, every product in fp32, four columns of one row a thread
+// (one 16-byte load of A feeds four of M, 16 FMAs).  `tmp`: 48 rows of LD floats.  256 threads; M's
+// upper triangle is written as zeros.  Ends with a barrier.
 template <int LD>
 KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid)
 {
@@ -113,36 +114,63 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
         const int b = tid >> 4, c = tid & 15;
         float x[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = r == c ? 1.0f : 0.0f;
+        for (int r = 0; r < 16; ++r) {
+            float s[4] = {r == c ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < 15; ++m)
+            for (int m = 0; m < r; m += 4) {
+                float a[4];
+                ld4(A + (16 * b + r) * LD + 16 * b + m, a);
 #pragma unroll
-            for (int r = m + 1; r < 16; ++r) x[r] -= A[(16 * b + r) * LD + 16 * b + m] * x[m];
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < r) s[e] -= a[e] * x[m + e];
+            }
+            x[r] = (s[0] + s[1]) + (s[2] + s[3]);
+        }
 #pragma unroll
         for (int r = 0; r < 16; ++r) M[(16 * b + r) * LD + 16 * b + c] = x[r];
     }
-    const int r = tid >> 4, c = tid & 15;
+    {
+        const int r = tid >> 4, c = tid & 15;
 #pragma unroll
-    for (int I = 0; I < 4; ++I)
+        for (int I = 0; I < 4; ++I)
 #pragma unroll
-        for (int J = I + 1; J < 4; ++J) M[(16 * I + r) * LD + 16 * J + c] = 0.0f;
+            for (int J = I + 1; J < 4; ++J) M[(16 * I + r) * LD + 16 * J + c] = 0.0f;
+    }
     __syncthreads();
+    const int J = tid >> 6, r = (tid & 63) >> 2, c = 4 * (tid & 3);
 #pragma unroll
     for (int I = 1; I < 4; ++I) {
+        if (J < I) {
+            float s[4] = {};
+            for (int m = 16 * J; m < 16 * I; m += 4) {
+                float a[4];
+                ld4(A + (16 * I + r) * LD + m, a);
 #pragma unroll
-        for (int J = 0; J < I; ++J) {
-            float s = 0.0f;
-#pragma unroll 16
-            for (int m = 16 * J; m < 16 * I; ++m) s += A[(16 * I + r) * LD + m] * M[m * LD + 16 * J + c];
-            tmp[(16 * J + r) * LD + c] = s;
+                for (int e = 0; e < 4; ++e) {
+                    float b[4];
+                    ld4(M + (m + e) * LD + 16 * J + c, b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] += a[e] * b[j];
+                }
+            }
+            st4(tmp + (16 * J + r) * LD + c, s);
         }
         __syncthreads();
+        if (J < I) {
+            float s[4] = {};
 #pragma unroll
-        for (int J = 0; J < I; ++J) {
-            float s = 0.0f;
+            for (int m = 0; m < 16; m += 4) {
+                float a[4];
+                ld4(M + (16 * I + r) * LD + 16 * I + m, a);
 #pragma unroll
-            for (int m = 0; m < 16; ++m) s += M[(16 * I + r) * LD + 16 * I + m] * tmp[(16 * J + m) * LD + c];
-            M[(16 * I + r) * LD + 16 * J + c] = -s;
+                for (int e = 0; e < 4; ++e) {
+                    float b[4];
+                    ld4(tmp + (16 * J + m + e) * LD + c, b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] -= a[e] * b[j];
+                }
+            }
+            st4(M + (16 * I + r) * LD + 16 * J + c, s);
         }
         __syncthreads();
     }

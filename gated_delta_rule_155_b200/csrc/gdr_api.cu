@@ -35,9 +35,14 @@ kda_status_t check_dims(int N, int T, int Hk, int Hv, int dk, int dv, kda_dtype_
     return KDA_OK;
 }
 
-size_t workspace_bytes_of(int N, int T, int Hk, int Hv, int dk, int dv, bool backward)
+// bf16 at dk = dv = 128 runs on the tensor cores and nowhere else
+bool on_tensor_cores(int dk, int dv, kda_dtype_t io, bool backward) { return !backward && kda::gdr_tc_shape(dk, dv, io_of(io)); }
+
+size_t workspace_bytes_of(int N, int T, int Hk, int Hv, int dk, int dv, kda_dtype_t io, bool backward)
 {
-    return T == 0 ? 0 : kda::gdr_simt_workspace(N, T, Hk, Hv, dk, dv, backward);
+    if (T == 0) return 0;
+    return on_tensor_cores(dk, dv, io, backward) ? kda::gdr_tc_workspace(N, T, Hk, Hv, backward)
+                                                 : kda::gdr_simt_workspace(N, T, Hk, Hv, dk, dv, backward);
 }
 
 kda_status_t check_workspace(const void *ws, size_t have, size_t need)
@@ -71,7 +76,7 @@ kda_status_t kda_gdr_workspace_size(int N, int T_total, int Hk, int Hv, int dk, 
     if (!bytes) return KDA_ERR_INVALID_ARG;
     const kda_status_t st = check_dims(N, T_total, Hk, Hv, dk, dv, io);
     if (st != KDA_OK) return st;
-    *bytes = workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, backward != 0);
+    *bytes = workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, backward != 0);
     return KDA_OK;
 }
 
@@ -90,10 +95,14 @@ kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const 
     if (misaligned({q, k, v, g, beta, initial_state, out, final_state}) ||
         misaligned4({initial_index, final_index, cu_seqlens}))
         return KDA_ERR_MISALIGNED;
-    st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, false));
+    st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, false));
     if (st != KDA_OK) return st;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, initial_index, out, final_state, final_index, pages, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word()};
+    if (on_tensor_cores(dk, dv, io, false)) {
+        if (!kda::gdr_tc_available()) return KDA_ERR_UNSUPPORTED;
+        return cuda_status(kda::launch_gdr_forward_tc(a, (cudaStream_t)stream));
+    }
     return cuda_status(kda::launch_gdr_forward_simt(a, (cudaStream_t)stream));
 }
 
@@ -110,7 +119,7 @@ kda_status_t kda_gdr_backward(const void *q, const void *k, const void *v, const
     if (misaligned({q, k, v, g, beta, initial_state, d_out, d_final_state, d_q, d_k, d_v, d_g, d_beta, d_initial_state}) ||
         misaligned4({cu_seqlens}))
         return KDA_ERR_MISALIGNED;
-    st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, true));
+    st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, true));
     if (st != KDA_OK) return st;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, nullptr, nullptr, nullptr, nullptr, 0, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word(),
