@@ -30,7 +30,7 @@ kda_status_t check_dims(int N, int T, int Hk, int Hv, int dk, int dv, kda_dtype_
     if (io != KDA_F32 && io != KDA_BF16) return KDA_ERR_INVALID_ARG;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KDA_ERR_UNSUPPORTED;
     // grids have the value heads in y; token, chunk and block counts are 32-bit, element offsets 64-bit
-    if (Hv > 65535 || (long long)T * Hv > INT_MAX / 2 || (long long)N * Hv > INT_MAX / 2) return KDA_ERR_UNSUPPORTED;
+    if (Hv > 65534 || (long long)T * Hv > INT_MAX / 2 || (long long)N * Hv > INT_MAX / 2) return KDA_ERR_UNSUPPORTED;
     if ((long long)N * 8 > INT_MAX / 2 || (long long)T + 64ll * N > INT_MAX / 2) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

@@ -1,70 +1,28 @@
 // gdr_tc.cu — the head-gated delta rule in chunks of 64 tokens on tcgen05 tensor cores (bf16,
-// dk = dv = 128).  The formulas are those of gdr_simt.cu.
+// dk = dv = 128): the forward pass.  The formulas are those of gdr_simt.cu.
 //
 // prep, a block per chunk and value head: [K; Q] K^T in one M = 128 MMA (exact bf16 operands, fp32
 //   sums), the decays, M = (I + A)^-1 and P M in fp32 on CUDA cores; M and P M go to the workspace as
 //   one 128 x 64 operand [M; P M], split into bf16 hi + lo, in the 128-byte swizzle of the MMA's
 //   operand tiles, so the walk brings it in with one bulk copy.
-// walk, a block per sequence, value head and 64 or 128 state columns: three products a chunk, each
-//   an M = 128 MMA with the 64 columns of a warpgroup as N:
-//     D1 = [K; Q] S         rows 0..63: X = K S, rows 64..127: Q S
-//     D2 = [M; P M] R       rows 0..63: U, rows 64..127: P U        (R = beta (V - gamma X))
-//     D3 = K^T (lam U)      S <- gamma_C S + D3
-//   K, Q enter as they are.  S, R, U and [M; P M] enter as bf16 hi + lo pairs (lo x lo left out), so
-//   what one chunk hands to the next is good to about 2^-16.  S stays in fp32 registers (a thread has
-//   one row of it); TMEM holds only the three products.  The B operands (S, R, U: k rows x 64 columns,
-//   MN-major) share one 32 KB buffer, since each is written after the MMA that read the one before.
-// A chunk is a chain: three MMAs, each between a read of TMEM, a few operations a value and a
-// write of shared memory; what it costs is that chain's latency, so two warpgroups with 64 columns
-// each work on the same tiles of K, Q and [M; P M] and fill each other's waits.
-#include <cuda.h>
-
-#include "gdr.cuh"
-#include "tc_common.cuh"
+// walk, a block per sequence and value head, everything transposed: the lanes of tensor memory are the
+//   128 value columns, so what a chunk computes from the state is the A operand of the next product and
+//   never leaves tensor memory, and K, Q and [M; P M] are B operands as the copies brought them:
+//     X^T  = S^T K^T       R^T = beta (V^T - gamma X^T)
+//     U^T  = R^T M^T       S^T <- gamma_C S^T + (lam U)^T K
+//     QS^T = S^T Q^T       O^T = gamma QS^T + R^T (P M)^T
+//   K, Q enter as they are.  S, R, lam U and [M; P M] enter as bf16 hi + lo pairs (lo x lo left out),
+//   so what one chunk hands to the next is good to about 2^-16; S itself stays in fp32.
+// The chain S -> X -> R -> U -> S bounds a sequence: three products, three reads of tensor memory with a
+// few operations a value, three writes.  Eight warps do that, half the columns each; one thread issues
+// the MMAs (the products of the outputs run in the shadow of the chain's vector phases), one the copies
+// of the chunks to come, and four warps write the outputs.
+#include "gdr_tc.cuh"
 
 namespace kda {
 namespace {
 
 using namespace gdr;
-using namespace tc;
-
-constexpr int D = 128;               // dk = dv
-constexpr int N = 64;                // state columns of a warpgroup
-constexpr int TILE = 128 * 128;      // bytes of 128 rows x 64 bf16
-
-// workspace item of a chunk and value head
-constexpr int IT_LO = TILE;          // [M; P M] hi at 0, lo here
-constexpr int IT_GATES = 2 * TILE;   // floats: gamma, lam, beta, then G hi, G lo (64 each)
-constexpr int IT_BYTES = IT_GATES + 2048;
-constexpr int IT_WALK = IT_GATES + 768;   // what the walk reads
-
-KDA_DEVICE void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-// x -> bf16 hi and lo, two values a word
-KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
-{
-    hi = pack_bf16x2(x0, x1);
-    const float2 h = unpack_bf16x2(hi);
-    lo = pack_bf16x2(x0 - h.x, x1 - h.y);
-}
-
-struct TcP {
-    GdrArgs a;
-    uint8_t *items;
-    __nv_bfloat16 *S, *U;    // kept for the gradients: [items, 128, 128], [items, 64, 128]
-    unsigned long long wait_ns;
-    int skip_load_chunk;
-};
-
-// What a block has in flight when a bounded wait has given up: every MMA of the issuing threads
-// (one commit each on `drain`) and the loads that were issued but not waited for are let finish
-// before shared and tensor memory are released.
-constexpr unsigned long long DRAIN_NS = 2000000000ull;
 
 // ---------------------------------------------------------------- prep
 constexpr int LM = 68;
@@ -73,10 +31,30 @@ constexpr int PR_A = 2 * TILE, PR_P = PR_A + 64 * LM * 4, PR_G = PR_P + 64 * LM 
 constexpr int PR_BYTES = PR_G + 6 * 256 + 64 + 1024;
 static_assert(PR_TMP + 48 * LM * 4 <= 2 * TILE, "M and its scratch take K's and Q's place");
 
+// order[r] <- the sequence whose length is the r-th longest: the walks start with the longest.  A warp a sequence.
+KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
+{
+    const GdrArgs &a = p.a;
+    for (int n = first; n < a.N; n += step) {
+        const int len = span_of(a.cu, n, a.N, a.T).len;
+        int before = 0;
+        for (int j = lane; j < a.N; j += 32) {
+            const int l = span_of(a.cu, j, a.N, a.T).len;
+            before += l > len || (l == len && j < n);
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) p.order[before] = n;
+    }
+}
+
 __global__ void __launch_bounds__(256, 3)
 gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
 {
     const GdrArgs &a = p.a;
+    if (p.order && blockIdx.y == gridDim.y - 1) {       // the blocks behind the heads: the sequences' order
+        order_sequences(p, blockIdx.x * (256 / 32) + (threadIdx.x >> 5), gridDim.x * (256 / 32), threadIdx.x & 31);
+        return;
+    }
     int n, c;
     SeqSpan span;
     if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
@@ -115,7 +93,6 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    bool ok = true;
     if (tid == 0) {
         if (mbar_wait_bounded(&bars[0], 0, abort_flag, a.err, p.wait_ns)) {
             const uint32_t kq = smem_u32(sm + PR_KQ);
@@ -127,23 +104,24 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit(&bars[1]);
         }
     }
-    float *gates = nullptr;
     uint8_t *item = p.items + ((size_t)blockIdx.x * a.Hv + hv) * IT_BYTES;
-    gates = (float *)(item + IT_GATES);
+    float *gates = (float *)(item + IT_GATES);
     if (warp == 1) {
         gate_sums(graw, ghi, glo, lane);
         __syncwarp();
         for (int t = lane; t < CH; t += 32) {
-            gates[t] = __expf(ghi[t]);
-            gates[64 + t] = __expf((ghi[63] - ghi[t]) + (glo[63] - glo[t]));
-            gates[128 + t] = beta[t];
-            gates[192 + t] = ghi[t];
-            gates[256 + t] = glo[t];
+            const float gm = __expf(ghi[t]);
+            gates[GA_GAM + t] = gm;
+            gates[GA_LAM + t] = __expf((ghi[63] - ghi[t]) + (glo[63] - glo[t]));
+            gates[GA_BETA + t] = beta[t];
+            gates[GA_BG + t] = beta[t] * gm;
+            gates[GA_HI + t] = ghi[t];
+            gates[GA_LO + t] = glo[t];
         }
     }
     if (tid == 0 && !*abort_flag) mbar_wait_bounded(&bars[1], 0, abort_flag, a.err, p.wait_ns);
     __syncthreads();
-    ok = !*abort_flag;
+    const bool ok = !*abort_flag;
     if (ok) {
         tc_fence_after();
         // thread: row r of [K; Q] K^T, 32 of its columns
@@ -223,56 +201,47 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------- the walk
-// shared memory: two stages of {K; Q tiles 32 KB, [M; P M] hi + lo 32 KB, gates}, then a B operand
-// buffer a warpgroup
-constexpr int ST_KQ = 0, ST_MM = 2 * TILE, ST_BYTES = ST_MM + IT_GATES + 1024;
+// shared memory: stages of {K; Q tiles 32 KB, V tiles 16 KB, [M; P M] hi + lo 32 KB, gates 1 KB}
+constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT_GATES, ST_BYTES = ST_G + 1024;
 constexpr int STAGES = 2;
-constexpr int OFF_B = STAGES * ST_BYTES, B_BYTES = 2 * TILE;   // 128 rows x 64 columns, hi then lo
-template <int NWG> constexpr int walk_bar() { return OFF_B + NWG * B_BYTES; }
-template <int NWG> constexpr int walk_bytes() { return walk_bar<NWG>() + 128 + 1024; }
-static_assert(walk_bytes<2>() <= 232448, "shared memory per block");
+constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
+static_assert(W_BYTES <= 232448, "shared memory per block");
+// tensor memory columns: S (fp32), S as an operand (hi, lo), X then R, U, Q S, P U
+constexpr int TM_S = 0, TM_SHL = 128, TM_X = 256, TM_U = 320, TM_QS = 384, TM_PU = 448;
+// warps: 0..3 and 4..7 the chain (tokens, or state rows, of the first and second half), 8..11 the
+// outputs, 12 the copies, 13 the MMAs
+constexpr int W_THREADS = 448;
 
-// 8 values of a row -> the row's 16-byte pieces of a hi and a lo tile
-KDA_DEVICE void put_split(uint8_t *hi, uint8_t *lo, int row, int j, const float (&x)[8])
+// 32 values a lane -> 16 words hi, 16 words lo
+KDA_DEVICE void put_hl(uint32_t hi_at, uint32_t lo_at, const float (&x)[32], uint32_t (&h)[16])
 {
-    uint4 h, l;
-    split2(x[0], x[1], h.x, l.x);
-    split2(x[2], x[3], h.y, l.y);
-    split2(x[4], x[5], h.z, l.z);
-    split2(x[6], x[7], h.w, l.w);
-    const uint32_t off = swz(row, j);
-    *(uint4 *)(hi + off) = h;
-    *(uint4 *)(lo + off) = l;
+    uint32_t l[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
+    tmem_st16(hi_at, h);
+    tmem_st16(lo_at, l);
 }
-KDA_DEVICE uint4 pack8(const float (&x)[8])
-{
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
+// A operand of token step kk (16 tokens) in a 64-column region: [tokens 0..31: hi, lo][32..63: hi, lo]
+KDA_DEVICE uint32_t tok_step(uint32_t region, int kk, int lo) { return region + 32 * (kk >> 1) + 16 * lo + 8 * (kk & 1); }
 
-// K and Q rows behind a sequence's end (the next sequence's, or NaN) are zeroed before they meet the
-// zeros of the other operand: the product of a zero and a NaN is not zero.
-KDA_DEVICE void zero_tail(uint8_t *kq, int valid, int tid, int nthreads)
-{
-    for (int u = tid; u < (CH - valid) * 32; u += nthreads) {
-        const int t = valid + (u >> 5), b = (u >> 3) & 3;   // b: channel block, then K or Q
-        *(uint4 *)(kq + (b >> 1) * TILE + (b & 1) * (TILE / 2) + swz(t, u & 7)) = make_uint4(0u, 0u, 0u, 0u);
-    }
-}
-
-template <int NWG, bool KEEP>
-__global__ void __launch_bounds__(128 * NWG + 32, 1)
-gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
+// KEEP: leaves each chunk's start state and U for the gradients, and writes no output and no final state
+template <bool KEEP>
+__global__ void __launch_bounds__(W_THREADS, 1)
+gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, TcP p)
 {
     const GdrArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint64_t *bars = (uint64_t *)(sm + walk_bar<NWG>());
-    uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES, *drain = done + 3 * NWG;
+    uint64_t *full = (uint64_t *)(sm + W_BAR), *empty = full + STAGES;
+    uint64_t *b_s = empty + STAGES, *b_r = b_s + 1, *b_u = b_s + 2, *b_free = b_s + 3;   // vector phases done
+    uint64_t *m_x = b_s + 4, *m_u = b_s + 5, *m_o = b_s + 6, *m_s = b_s + 7;             // products done
+    uint64_t *drain = b_s + 8;
     uint32_t *tslot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int GROUPS = 2 / NWG;      // blocks of a head
-    const int n = blockIdx.x / GROUPS, hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
+    const int hv = blockIdx.x % a.Hv, hk = hv / (a.Hv / a.Hk);
+    const int n = p.order ? p.order[blockIdx.x / a.Hv] : blockIdx.x / a.Hv;
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
     const size_t item0 = (size_t)slot_base(span.row0, n);
@@ -280,230 +249,306 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], NWG + 4 * NWG);   // a commit a warpgroup, and its warps' reads of the gates
+            mbar_init(&empty[i], 1 + 8 + (KEEP ? 0 : 4));
         }
-        for (int i = 0; i < 3 * NWG; ++i) mbar_init(&done[i], 1);
-        mbar_init(drain, NWG);
+        mbar_init(b_s, 8);
+        mbar_init(b_r, 8);
+        mbar_init(b_u, 8);
+        mbar_init(b_free, 4);
+        mbar_init(m_x, 1);
+        mbar_init(m_u, 1);
+        mbar_init(m_o, 1);
+        mbar_init(m_s, 1);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if (nchunks > 0) {
-            prefetch_tmap(&tm_q);
-            prefetch_tmap(&tm_k);
-        }
     }
     if (warp == 0) {
-        tmem_alloc(tslot, NWG == 2 ? 512 : 256);
+        tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    auto wait = [&](uint64_t *bar, int i) { return mbar_wait_bounded(bar, (uint32_t)(i & 1), abort_flag, a.err, p.wait_ns); };
+    // by a whole warp: one answer for all its lanes
+    auto wait_all = [&](uint64_t *bar, int i) { return __all_sync(0xffffffffu, wait(bar, i)) != 0; };
+    auto wait_full = [&](int ch) { return wait_all(&full[ch % STAGES], ch / STAGES); };
 
-    if (warp == 4 * NWG) {
+    if (warp == 12) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            int issued = 0, seen = 0;
+            int issued = 0;
+            if (nchunks > 0) {
+                prefetch_tmap(&tm_q);
+                prefetch_tmap(&tm_k);
+                prefetch_tmap(&tm_v);
+            }
             for (int ch = 0; ch < nchunks && !*abort_flag; ++ch) {
                 const int st = ch % STAGES;
-                if (ch >= STAGES && !mbar_wait_bounded(&empty[st], (uint32_t)((ch / STAGES - 1) & 1), abort_flag, a.err, p.wait_ns))
-                    break;
+                if (ch >= STAGES && !wait(&empty[st], ch / STAGES - 1)) break;
                 if (ch == p.skip_load_chunk) continue;   // injected failure: the wait for it runs out
                 uint8_t *s = sm + st * ST_BYTES;
-                mbar_arrive_expect_tx(&full[st], 2 * TILE + IT_WALK);
+                mbar_arrive_expect_tx(&full[st], 3 * TILE + IT_WALK);
                 const int row = span.row0 + ch * CH;
                 for (int cb = 0; cb < 2; ++cb) {
                     tma_load_4d(s + ST_KQ + cb * TILE, &tm_k, cb * 64, hk, row, 0, &full[st]);
                     tma_load_4d(s + ST_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row, 0, &full[st]);
+                    tma_load_4d(s + ST_V + cb * (TILE / 2), &tm_v, cb * 64, hv, row, 0, &full[st]);
                 }
                 bulk_load(s + ST_MM, p.items + ((item0 + ch) * a.Hv + hv) * IT_BYTES, IT_WALK, &full[st]);
                 issued = ch + 1;
             }
             // after an abort the loads of the last stages may still be on their way
-            for (seen = issued > STAGES ? issued - STAGES : 0; seen < issued && *abort_flag; ++seen)
+            for (int seen = issued > STAGES ? issued - STAGES : 0; seen < issued && *abort_flag; ++seen)
                 if (seen != p.skip_load_chunk)
                     mbar_wait_timed(&full[seen % STAGES], (uint32_t)((seen / STAGES) & 1), DRAIN_NS);
         }
-    } else {
-        // ------------------------------------------------------------ a warpgroup and its 64 columns
-        const int wg = warp >> 2, wt = tid & 127, lq = warp & 3;
-        const int col0 = (NWG == 2 ? wg : (int)blockIdx.x % GROUPS) * N;
-        const uint32_t lane_q = (uint32_t)(32 * lq) << 16;
-        const uint32_t d1 = tmem + 192 * wg, d2 = d1 + 64, d3 = d1 + 128;
-        uint8_t *B = sm + OFF_B + wg * B_BYTES;
-        // one barrier a product: a warp that comes late must not find the phase it waits for gone by
-        uint64_t *bar = &done[3 * wg];
-        const bool leader = wt == 0;
-        auto wait_mma = [&](int i, int ch) {
-            mbar_wait_bounded(bar + i, (uint32_t)(ch & 1), abort_flag, a.err, p.wait_ns);
-            tc_fence_after();
-        };
-        constexpr uint32_t id_b = idesc_bf16(128, N, false, true), id_tb = idesc_bf16(128, N, true, true);
-
-        float S[N];                       // row wt of the state, this warpgroup's columns
-        {
-            const int page = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
-            if (page >= 0) {
-                const float *src = a.s0 + (((size_t)page * a.Hv + hv) * D + wt) * D + col0;
-#pragma unroll
-                for (int e = 0; e < N; e += 4) ld4(src + e, *(float(*)[4])(S + e));
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) S[e] = 0.0f;
-            }
-        }
-        auto put_state = [&](int ch) {    // S -> hi + lo operand (and the copy kept for the gradients)
-#pragma unroll
-            for (int j = 0; j < N / 8; ++j) {
-                const float(&x)[8] = *(const float(*)[8])(S + 8 * j);
-                put_split(B, B + TILE, wt, j, x);
-                if (KEEP && ch < nchunks)
-                    *(uint4 *)(p.S + (((item0 + ch) * a.Hv + hv) * D + wt) * D + col0 + 8 * j) = pack8(x);
-            }
-            fence_proxy_async();
-            tc_fence_before();
-            named_bar_sync(1 + wg, 128);
-        };
-        if (nchunks > 0) put_state(0);
-
-        for (int ch = 0; ch < nchunks; ++ch) {
-            const int st = ch % STAGES;
-            uint8_t *s = sm + st * ST_BYTES;
+    } else if (warp == 13) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t id_k = idesc_bf16(128, 64, false, false), id_s = idesc_bf16(128, 128, false, true);
+        bool ok = true;
+        for (int ch = 0; ch < nchunks && ok; ++ch) {
+            uint8_t *s = sm + (ch % STAGES) * ST_BYTES;
+            ok = wait_full(ch);
             const int valid = min(CH, span.len - ch * CH);
-            const int t = wt & 63;        // rows 0..63 (warps 0, 1): X and U; 64..127 (warps 2, 3): the outputs
-            const size_t tok = (size_t)span.row0 + ch * CH + t;
-            mbar_wait_bounded(&full[st], (uint32_t)((ch / STAGES) & 1), abort_flag, a.err, p.wait_ns);
-            const float *gates = (const float *)(s + ST_MM + IT_GATES);
-            const float gam = gates[t], lam = gates[64 + t], bet = gates[128 + t], gC = gates[63];
-            __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty[st])) : "memory");
-            if (valid < CH) {             // uniform for the block
-                zero_tail(s + ST_KQ, valid, tid, 128 * NWG);
+            if (valid < CH) {     // K rows behind the end (the next sequence's, or NaN) meet the zeros of U: zero
+                for (int u = lane; u < (CH - valid) * 16; u += 32)
+                    *(uint4 *)(s + ST_KQ + ((u >> 3) & 1) * TILE + swz(valid + (u >> 4), u & 7)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async();
-                named_bar_sync(3, 128 * NWG);
+                __syncwarp();
             }
-            const uint32_t kq = smem_u32(s + ST_KQ), mm = smem_u32(s + ST_MM), b = smem_u32(B);
-            if (leader && !*abort_flag) {
-                tc_fence_after();
-#pragma unroll
-                for (int hl = 0; hl < 2; ++hl)
+            if (lane == 0) {
+                const uint32_t kq = smem_u32(s + ST_KQ), mm = smem_u32(s + ST_MM);
+                auto from_state = [&](int out, int rows) {       // S^T [K or Q]^T
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ss(d1, sdesc(kq + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024),
-                               sdesc(b + hl * TILE + kk * 2048, 8192, 1024), id_b, hl | kk);
-                mma_commit(bar + 0);
-            }
-            uint4 v[8];                   // V row, under the MMA
-            if (lq < 2) {
-                const uint4 *src = (const uint4 *)((const __nv_bfloat16 *)a.v + (tok * a.Hv + hv) * D + col0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = t < valid ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-            }
-            wait_mma(0, ch);
-            if (lq < 2) {                 // R = beta (V - gamma X), zero behind the end
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32];
-                    tmem_ld32(d1 + lane_q + 32 * hf, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w[4] = {v[4 * hf + j].x, v[4 * hf + j].y, v[4 * hf + j].z, v[4 * hf + j].w};
-                        float r[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = unpack_bf16x2(w[e]);
-                            r[2 * e] = t < valid ? bet * (f.x - gam * __uint_as_float(x[8 * j + 2 * e])) : 0.0f;
-                            r[2 * e + 1] = t < valid ? bet * (f.y - gam * __uint_as_float(x[8 * j + 2 * e + 1])) : 0.0f;
-                        }
-                        put_split(B, B + TILE / 2, t, 4 * hf + j, r);
-                    }
-                }
-                fence_proxy_async();
-                tc_fence_before();
-                named_bar_sync(4 + wg, 64);
-                if (leader && !*abort_flag) {
-                    tc_fence_after();
+                        for (int hl = 0; hl < 2; ++hl)
+                            mma_ts(tmem + out, tmem + TM_SHL + 64 * hl + 8 * kk,
+                                   sdesc(kq + rows + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024), id_k, kk | hl);
+                };
+                auto from_r = [&](int out, int rows) {           // R^T [M or P M]^T
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ah = sdesc(mm + kk * 32, 16, 1024), al = sdesc(mm + IT_LO + kk * 32, 16, 1024);
-                        const uint64_t bh = sdesc(b + kk * 2048, 8192, 1024), bl = sdesc(b + TILE / 2 + kk * 2048, 8192, 1024);
-                        mma_ss(d2, ah, bh, id_b, kk);
-                        mma_ss(d2, ah, bl, id_b, 1);
-                        mma_ss(d2, al, bh, id_b, 1);
+                        const uint32_t rh = tok_step(tmem + TM_X, kk, 0), rl = tok_step(tmem + TM_X, kk, 1);
+                        const uint64_t bh = sdesc(mm + rows + kk * 32, 16, 1024), bl = sdesc(mm + rows + IT_LO + kk * 32, 16, 1024);
+                        mma_ts(tmem + out, rh, bh, id_k, kk);
+                        mma_ts(tmem + out, rl, bh, id_k, 1);
+                        mma_ts(tmem + out, rh, bl, id_k, 1);
                     }
-                    mma_commit(bar + 1);
+                };
+                if (ok && (ok = wait(b_s, ch))) {
+                    tc_fence_after();
+                    from_state(TM_X, 0);
+                    mma_commit(m_x);
+                    if (ch > 0) ok = wait(b_free, ch - 1);       // the outputs' warps have read the chunk before
+                    tc_fence_after();
+                    if (!KEEP && ok) from_state(TM_QS, TILE / 2);
                 }
-            }
-            wait_mma(1, ch);
-            if (lq < 2) {                 // lam U -> operand
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32];
-                    tmem_ld32(d2 + lane_q + 32 * hf, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float r[8];
-                        if (KEEP) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) r[e] = __uint_as_float(x[8 * j + e]);
-                            *(uint4 *)(p.U + (((item0 + ch) * a.Hv + hv) * CH + t) * D + col0 + 32 * hf + 8 * j) = pack8(r);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) r[e] = lam * __uint_as_float(x[8 * j + e]);
-                        put_split(B, B + TILE / 2, t, 4 * hf + j, r);
+                if (ok && (ok = wait(b_r, ch))) {
+                    tc_fence_after();
+                    from_r(TM_U, 0);
+                    mma_commit(m_u);
+                    if (!KEEP) {
+                        from_r(TM_PU, TILE / 2);
+                        mma_commit(m_o);
                     }
                 }
-                fence_proxy_async();
-                tc_fence_before();
-                named_bar_sync(4 + wg, 64);
-                if (leader && !*abort_flag) {
+                if (ok && (ok = wait(b_u, ch))) {
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
-                            mma_ss(d3, sdesc(kq + kk * 2048, TILE, 1024), sdesc(b + hl * (TILE / 2) + kk * 2048, 8192, 1024),
-                                   id_tb, kk | hl);
-                    mma_commit(bar + 2);
-                    mma_commit(&empty[st]);
+                            mma_ts(tmem + TM_S, tok_step(tmem + (KEEP ? TM_X : TM_U), kk, hl), sdesc(kq + kk * 2048, TILE, 1024),
+                                   id_s, 1);
+                    mma_commit(m_s);
+                    mma_commit(&empty[ch % STAGES]);
                 }
-            } else if (!KEEP) {           // outputs: gamma (Q S) + P U
-                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + (tok * a.Hv + hv) * D + col0;
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        }
+        if (lane == 0 && *abort_flag) {
+            mma_commit(drain);
+            mbar_wait_timed(drain, 0u, DRAIN_NS);
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ outputs (KEEP: U)
+        const int dv = 32 * (warp & 3) + lane;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        for (int ch = 0; ch < nchunks; ++ch) {
+            const int st = ch % STAGES, valid = min(CH, span.len - ch * CH);
+            if (KEEP) {
+                if (!wait_all(m_u, ch)) break;
+                tc_fence_after();
+                uint8_t *dst = p.U + ((item0 + ch) * a.Hv + hv) * TILE;   // [dv][64 tokens]
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t x[32];
+                    tmem_ld32(at + TM_U + 32 * hf, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
+                        *(uint4 *)(dst + swz(dv, 4 * hf + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_free);
+            } else {
+                if (!wait_full(ch) || !wait_all(m_o, ch)) break;
+                tc_fence_after();
+                const float *gam = (const float *)(sm + st * ST_BYTES + ST_G) + GA_GAM;
+                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + (((size_t)span.row0 + ch * CH) * a.Hv + hv) * D + dv;
+                const size_t step = (size_t)a.Hv * D;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t x[32], y[32];
-                    tmem_ld32(d1 + lane_q + 32 * hf, y);
-                    tmem_ld32(d2 + lane_q + 32 * hf, x);
+                    tmem_ld32(at + TM_QS + 32 * hf, x);
+                    tmem_ld32(at + TM_PU + 32 * hf, y);
                     tmem_wait_ld();
-                    if (t < valid) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float r[8];
+                    for (int e = 0; e < 32; e += 4) {
+                        float g4[4];
+                        ld4(gam + 32 * hf + e, g4);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                r[e] = gam * __uint_as_float(y[8 * j + e]) + __uint_as_float(x[8 * j + e]);
-                            *(uint4 *)(dst + 32 * hf + 8 * j) = pack8(r);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (32 * hf + e + i < valid)
+                                dst[(32 * hf + e + i) * step] =
+                                    __float2bfloat16_rn(g4[i] * __uint_as_float(x[e + i]) + __uint_as_float(y[e + i]));
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(b_free);
+                    mbar_arrive(&empty[st]);
+                }
             }
-            wait_mma(2, ch);
+        }
+    } else {
+        // ------------------------------------------------------------ the chain
+        const int grp = warp >> 2, lq = warp & 3, dv = 32 * lq + lane;
+        const uint32_t at = tmem + ((uint32_t)(32 * lq) << 16);
+        const int r0 = 64 * grp;                     // state rows of the thread: r0 .. r0 + 63 of column dv
+        auto arrive = [&](uint64_t *bar) {           // after the writes to tensor memory
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        {
+            const int page = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
+            const float *src = a.s0 + (((size_t)max(page, 0) * a.Hv + hv) * D + r0) * D + dv;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t x[32];
-                tmem_ld32(d3 + lane_q + 32 * hf, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = page >= 0 ? __float_as_uint(src[(size_t)(32 * hf + e) * D]) : 0u;
+                tmem_st32(at + TM_S + r0 + 32 * hf, x);
+            }
+            tmem_wait_st();                          // each thread reads back what it wrote itself
+        }
+        bool ok = true;
+        for (int ch = 0; ch < nchunks; ++ch) {
+            const int st = ch % STAGES, valid = min(CH, span.len - ch * CH);
+            uint8_t *s = sm + st * ST_BYTES;
+            const float *gates = (const float *)(s + ST_G);
+            if (ch > 0) {
+                if (!(ok = wait_all(m_s, ch - 1))) break;
+                tc_fence_after();
+            }
+            {
+                uint32_t x[2][32], h[16];
+                tmem_ld32(at + TM_S + r0, x[0]);
+                tmem_wait_ld();
+                tmem_ld32(at + TM_S + r0 + 32, x[1]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (hf) tmem_wait_ld();
+                    float y[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[hf][e]);
+                    put_hl(at + TM_SHL + (r0 >> 1) + 16 * hf, at + TM_SHL + 64 + (r0 >> 1) + 16 * hf, y, h);
+                    if (KEEP) {                      // [dv][state row]
+                        uint8_t *dst = p.S + (((item0 + ch) * a.Hv + hv) * 2 + grp) * TILE;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *(uint4 *)(dst + swz(dv, 4 * hf + j)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                    }
+                }
+            }
+            arrive(b_s);
+            if (!(ok = wait_full(ch))) break;
+            const float gC = gates[GA_GAM + CH - 1];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {         // the state decayed, in the shadow of the product
+                uint32_t x[32];
+                tmem_ld32(at + TM_S + r0 + 32 * hf, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[32 * hf + e] = gC * S[32 * hf + e] + __uint_as_float(x[e]);
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(gC * __uint_as_float(x[e]));
+                tmem_st32(at + TM_S + r0 + 32 * hf, x);
             }
-            if (ch + 1 < nchunks) put_state(ch + 1);
+            // V^T: column dv of the group's 32 tokens
+            float r[32];
+            {
+                const uint8_t *vt = s + ST_V + (dv >> 6) * (TILE / 2) + grp * 32 * 128 + 2 * (dv & 7);
+                const int j = (dv & 63) >> 3;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float f = __bfloat162float(*(const __nv_bfloat16 *)(vt + e * 128 + ((j ^ (e & 7)) << 4)));
+                    r[e] = 32 * grp + e < valid ? f : 0.0f;
+                }
+            }
+            if (!(ok = wait_all(m_x, ch))) break;
+            tc_fence_after();
+            {
+                uint32_t x[32], h[16];
+                tmem_ld32(at + TM_X + 32 * grp, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float b4[4], c4[4];
+                    ld4(gates + GA_BETA + 32 * grp + e, b4);
+                    ld4(gates + GA_BG + 32 * grp + e, c4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[e + i] = b4[i] * r[e + i] - c4[i] * __uint_as_float(x[e + i]);
+                }
+                put_hl(at + TM_X + 32 * grp, at + TM_X + 32 * grp + 16, r, h);
+            }
+            arrive(b_r);
+            if (!(ok = wait_all(m_u, ch))) break;
+            tc_fence_after();
+            {
+                uint32_t x[32], h[16];
+                tmem_ld32(at + TM_U + 32 * grp, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float l4[4];
+                    ld4(gates + GA_LAM + 32 * grp + e, l4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[e + i] = l4[i] * __uint_as_float(x[e + i]);
+                }
+                const uint32_t to = at + (KEEP ? TM_X : TM_U) + 32 * grp;
+                put_hl(to, to + 16, r, h);
+            }
+            arrive(b_u);
+            if (lane == 0) mbar_arrive(&empty[st]);
         }
-
         if (!KEEP && a.sT) {
+            if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) {
+                tc_fence_after();
+            }
             const int page = page_of(a.sT_index, n, a.pages, a.err);
-            bool keep = page >= 0 && !*abort_flag;
+            bool keep = page >= 0 && ok && !*abort_flag;
             if (page >= 0 && (a.sT_index || (a.s0_index && a.sT == a.s0))) {
                 bool clash = false;       // as page_is_free, a warp at a time
                 for (int j = lane; j < a.N; j += 32) {
@@ -516,21 +561,23 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             if (keep) {
-                float *dst = a.sT + (((size_t)page * a.Hv + hv) * D + wt) * D + col0;
+                float *dst = a.sT + (((size_t)page * a.Hv + hv) * D + r0) * D + dv;
 #pragma unroll
-                for (int e = 0; e < N; e += 4) st4(dst + e, *(const float(*)[4])(S + e));
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t x[32];
+                    tmem_ld32(at + TM_S + r0 + 32 * hf, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) dst[(size_t)(32 * hf + e) * D] = __uint_as_float(x[e]);
+                }
             }
-        }
-        if (leader && *abort_flag) {
-            mma_commit(drain);
-            mbar_wait_timed(drain, 0u, DRAIN_NS);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, NWG == 2 ? 512 : 256);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -539,33 +586,35 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 bool gdr_tc_shape(int dk, int dv, IoType io) { return io == IO_BF16 && dk == D && dv == D; }
 bool gdr_tc_available() { return device_is_sm100() && tensor_maps_available(); }
 
-size_t gdr_tc_workspace(int N_, int T, int Hk, int Hv, bool backward)
+size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
 {
     (void)Hk;
-    const size_t items = (size_t)gdr_slots(N_, T) * Hv;
-    return backward ? 0 : items * IT_BYTES;
+    const size_t items = (size_t)gdr_slots(N, T) * Hv;
+    return backward ? 0 : items * IT_BYTES + 4 * (size_t)N;
 }
 
 cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
 {
-    struct TagP; struct Tag1; struct Tag2;
+    struct TagP; struct TagW;
     const WaitHooks hk = wait_hooks();
-    TcP p{a, (uint8_t *)a.ws, nullptr, nullptr, hk.wait_ns, hk.skip_load_chunk};
-    CUtensorMap mq{}, mk{};
+    TcP p{};
+    p.a = a;
+    p.items = (uint8_t *)a.ws;
+    p.wait_ns = hk.wait_ns;
+    p.skip_load_chunk = hk.skip_load_chunk;
+    CUtensorMap mq{}, mk{}, mv{};
     cudaError_t e;
     if (a.T > 0) {
-        if (!make_tile_map(&mq, a.q, 1, a.T, a.Hk, CH) || !make_tile_map(&mk, a.k, 1, a.T, a.Hk, CH)) return cudaErrorInvalidValue;
+        if (!make_tile_map(&mq, a.q, 1, a.T, a.Hk, CH) || !make_tile_map(&mk, a.k, 1, a.T, a.Hk, CH) ||
+            !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
+            return cudaErrorInvalidValue;
+        const size_t slots = (size_t)gdr_slots(a.N, a.T);
+        if (a.cu && a.N > 1) p.order = (int *)(p.items + slots * a.Hv * IT_BYTES);
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        gdr_prep_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hv), 256, PR_BYTES, s>>>(mq, mk, p);
+        gdr_prep_tc_kernel<<<dim3((unsigned)slots, a.Hv + (p.order ? 1 : 0)), 256, PR_BYTES, s>>>(mq, mk, p);
     }
-    // few heads: a block per 64 columns, so that twice as many SMs work
-    if ((long long)a.N * a.Hv <= 74) {
-        if ((e = smem_opt_in<Tag1>((const void *)gdr_walk_tc_kernel<1, false>, walk_bytes<1>())) != cudaSuccess) return e;
-        gdr_walk_tc_kernel<1, false><<<dim3((unsigned)a.N * 2, a.Hv), 160, walk_bytes<1>(), s>>>(mq, mk, p);
-    } else {
-        if ((e = smem_opt_in<Tag2>((const void *)gdr_walk_tc_kernel<2, false>, walk_bytes<2>())) != cudaSuccess) return e;
-        gdr_walk_tc_kernel<2, false><<<dim3((unsigned)a.N, a.Hv), 288, walk_bytes<2>(), s>>>(mq, mk, p);
-    }
+    if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel<false>, W_BYTES)) != cudaSuccess) return e;
+    gdr_walk_tc_kernel<false><<<(unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 

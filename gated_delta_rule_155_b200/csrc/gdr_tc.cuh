@@ -1,0 +1,58 @@
+// gdr_tc.cuh — layouts and helpers shared by the tensor-core kernels of the head-gated delta rule.
+#pragma once
+
+#include <cuda.h>
+
+#include "gdr.cuh"
+#include "tc_common.cuh"
+
+namespace kda {
+namespace gdr {
+
+using namespace tc;
+
+constexpr int D = 128;               // dk = dv
+constexpr int TILE = 128 * 128;      // bytes of 128 rows x 64 bf16
+
+// workspace item of a chunk and value head: [M; P M] as a 128-row operand tile, hi at 0, lo at IT_LO,
+// then gates, 64 floats each: gamma, lam, beta, beta gamma, G hi, G lo
+constexpr int IT_LO = TILE;
+constexpr int IT_GATES = 2 * TILE;
+constexpr int IT_BYTES = IT_GATES + 2048;
+constexpr int IT_WALK = IT_GATES + 1024;   // what the walks read
+enum { GA_GAM = 0, GA_LAM = 64, GA_BETA = 128, GA_BG = 192, GA_HI = 256, GA_LO = 320 };
+
+struct TcP {
+    GdrArgs a;
+    uint8_t *items;
+    int *order;              // sequences by length, longest first (null: as they are)
+    uint8_t *S, *U, *dS, *H; // kept for the gradients, operand tiles of 2, 1, 2 and 1 TILE bytes an item
+    unsigned long long wait_ns;
+    int skip_load_chunk;
+};
+
+KDA_DEVICE void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+KDA_DEVICE void mbar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// x -> bf16 hi and lo, two values a word
+KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x0, x1);
+    const float2 h = unpack_bf16x2(hi);
+    lo = pack_bf16x2(x0 - h.x, x1 - h.y);
+}
+
+// What a block has in flight when a bounded wait has given up (MMAs, by one commit of the thread that
+// issues them; loads that were issued but not waited for) is let finish before its memory is released.
+constexpr unsigned long long DRAIN_NS = 2000000000ull;
+
+}  // namespace gdr
+}  // namespace kda
