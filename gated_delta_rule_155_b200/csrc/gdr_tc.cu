@@ -14,9 +14,10 @@
 //   K, Q enter as they are.  S, R, lam U and [M; P M] enter as bf16 hi + lo pairs (lo x lo left out),
 //   so what one chunk hands to the next is good to about 2^-16; S itself stays in fp32.
 // The chain S -> X -> R -> U -> S bounds a sequence: three products, three reads of tensor memory with a
-// few operations a value, three writes.  Eight warps do that, half the columns each; one thread issues
-// the MMAs (the products of the outputs run in the shadow of the chain's vector phases), one the copies
-// of the chunks to come, and four warps write the outputs.
+// few operations a value, three writes.  Sixteen warps do that, a quarter of the columns each, and write
+// the outputs under the state's product; one thread issues the MMAs, one the copies of the chunks to
+// come.  An M = 128 MMA takes about max(54, N / 2) cycles, so X and Q S, and U and P U, are one product
+// of N = 128 each: 36 MMAs a chunk.
 #include "gdr_tc.cuh"
 
 namespace kda {
@@ -206,23 +207,10 @@ constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT
 constexpr int STAGES = 2;
 constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
 static_assert(W_BYTES <= 232448, "shared memory per block");
-// tensor memory columns: S (fp32), S as an operand (hi, lo), X then R, U, Q S, P U
-constexpr int TM_S = 0, TM_SHL = 128, TM_X = 256, TM_U = 320, TM_QS = 384, TM_PU = 448;
-// warps: 0..3 and 4..7 the chain (tokens, or state rows, of the first and second half), 8..11 the
-// outputs, 12 the copies, 13 the MMAs
-constexpr int W_THREADS = 448;
-
-// 32 values a lane -> 16 words hi, 16 words lo
-KDA_DEVICE void put_hl(uint32_t hi_at, uint32_t lo_at, const float (&x)[32], uint32_t (&h)[16])
-{
-    uint32_t l[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
-    tmem_st16(hi_at, h);
-    tmem_st16(lo_at, l);
-}
-// A operand of token step kk (16 tokens) in a 64-column region: [tokens 0..31: hi, lo][32..63: hi, lo]
-KDA_DEVICE uint32_t tok_step(uint32_t region, int kk, int lo) { return region + 32 * (kk >> 1) + 16 * lo + 8 * (kk & 1); }
+// tensor memory columns: S (fp32), S as an operand (hi, lo), X then R, Q S, U, P U
+constexpr int TM_S = 0, TM_SHL = 128, TM_X = 256, TM_QS = 320, TM_U = 384, TM_PU = 448;
+// warps: 4 g .. 4 g + 3, g < 4: tokens 16 g .. and state rows 32 g .. of the chain; 16 the copies, 17 the MMAs
+constexpr int W_THREADS = 576;
 
 // KEEP: leaves each chunk's start state and U for the gradients, and writes no output and no final state
 template <bool KEEP>
@@ -234,9 +222,9 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *full = (uint64_t *)(sm + W_BAR), *empty = full + STAGES;
-    uint64_t *b_s = empty + STAGES, *b_r = b_s + 1, *b_u = b_s + 2, *b_free = b_s + 3;   // vector phases done
-    uint64_t *m_x = b_s + 4, *m_u = b_s + 5, *m_o = b_s + 6, *m_s = b_s + 7;             // products done
-    uint64_t *drain = b_s + 8;
+    uint64_t *b_s = empty + STAGES, *b_r = b_s + 1, *b_u = b_s + 2;    // vector phases done
+    uint64_t *m_x = b_s + 3, *m_u = b_s + 4, *m_s = b_s + 5;           // products done
+    uint64_t *drain = b_s + 6;
     uint32_t *tslot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -249,15 +237,13 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1 + 8 + (KEEP ? 0 : 4));
+            mbar_init(&empty[i], 1 + 16);
         }
-        mbar_init(b_s, 8);
-        mbar_init(b_r, 8);
-        mbar_init(b_u, 8);
-        mbar_init(b_free, 4);
+        mbar_init(b_s, 16);
+        mbar_init(b_r, 16);
+        mbar_init(b_u, 16);
         mbar_init(m_x, 1);
         mbar_init(m_u, 1);
-        mbar_init(m_o, 1);
         mbar_init(m_s, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -276,7 +262,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto wait_all = [&](uint64_t *bar, int i) { return __all_sync(0xffffffffu, wait(bar, i)) != 0; };
     auto wait_full = [&](int ch) { return wait_all(&full[ch % STAGES], ch / STAGES); };
 
-    if (warp == 12) {
+    if (warp == 16) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             int issued = 0;
@@ -305,9 +291,10 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (seen != p.skip_load_chunk)
                     mbar_wait_timed(&full[seen % STAGES], (uint32_t)((seen / STAGES) & 1), DRAIN_NS);
         }
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // ------------------------------------------------------------ MMAs
-        constexpr uint32_t id_k = idesc_bf16(128, 64, false, false), id_s = idesc_bf16(128, 128, false, true);
+        constexpr int NX = KEEP ? 64 : 128;      // X (and Q S), U (and P U)
+        constexpr uint32_t id_x = idesc_bf16(128, NX, false, false), id_s = idesc_bf16(128, 128, false, true);
         bool ok = true;
         for (int ch = 0; ch < nchunks && ok; ++ch) {
             uint8_t *s = sm + (ch % STAGES) * ST_BYTES;
@@ -321,49 +308,35 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (lane == 0) {
                 const uint32_t kq = smem_u32(s + ST_KQ), mm = smem_u32(s + ST_MM);
-                auto from_state = [&](int out, int rows) {       // S^T [K or Q]^T
+                if (ok && (ok = wait(b_s, ch))) {                // S^T [K; Q]^T
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
-                            mma_ts(tmem + out, tmem + TM_SHL + 64 * hl + 8 * kk,
-                                   sdesc(kq + rows + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024), id_k, kk | hl);
-                };
-                auto from_r = [&](int out, int rows) {           // R^T [M or P M]^T
+                            mma_ts(tmem + TM_X, tmem + TM_SHL + 64 * hl + 8 * kk,
+                                   sdesc(kq + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024), id_x, kk | hl);
+                    mma_commit(m_x);
+                }
+                if (ok && (ok = wait(b_r, ch))) {                // R^T [M; P M]^T
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t rh = tok_step(tmem + TM_X, kk, 0), rl = tok_step(tmem + TM_X, kk, 1);
-                        const uint64_t bh = sdesc(mm + rows + kk * 32, 16, 1024), bl = sdesc(mm + rows + IT_LO + kk * 32, 16, 1024);
-                        mma_ts(tmem + out, rh, bh, id_k, kk);
-                        mma_ts(tmem + out, rl, bh, id_k, 1);
-                        mma_ts(tmem + out, rh, bl, id_k, 1);
+                        const uint32_t rh = tmem + TM_X + 16 * kk, rl = rh + 8;
+                        const uint64_t bh = sdesc(mm + kk * 32, 16, 1024), bl = sdesc(mm + IT_LO + kk * 32, 16, 1024);
+                        mma_ts(tmem + TM_U, rh, bh, id_x, kk);
+                        mma_ts(tmem + TM_U, rl, bh, id_x, 1);
+                        mma_ts(tmem + TM_U, rh, bl, id_x, 1);
                     }
-                };
-                if (ok && (ok = wait(b_s, ch))) {
-                    tc_fence_after();
-                    from_state(TM_X, 0);
-                    mma_commit(m_x);
-                    if (ch > 0) ok = wait(b_free, ch - 1);       // the outputs' warps have read the chunk before
-                    tc_fence_after();
-                    if (!KEEP && ok) from_state(TM_QS, TILE / 2);
-                }
-                if (ok && (ok = wait(b_r, ch))) {
-                    tc_fence_after();
-                    from_r(TM_U, 0);
                     mma_commit(m_u);
-                    if (!KEEP) {
-                        from_r(TM_PU, TILE / 2);
-                        mma_commit(m_o);
-                    }
                 }
-                if (ok && (ok = wait(b_u, ch))) {
+                if (ok && (ok = wait(b_u, ch))) {                // (lam U)^T K
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
-                            mma_ts(tmem + TM_S, tok_step(tmem + (KEEP ? TM_X : TM_U), kk, hl), sdesc(kq + kk * 2048, TILE, 1024),
-                                   id_s, 1);
+                            mma_ts(tmem + TM_S, tmem + TM_X + 16 * kk + 8 * hl, sdesc(kq + kk * 2048, TILE, 1024), id_s, 1);
                     mma_commit(m_s);
                     mma_commit(&empty[ch % STAGES]);
                 }
@@ -374,85 +347,31 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit(drain);
             mbar_wait_timed(drain, 0u, DRAIN_NS);
         }
-    } else if (warp >= 8) {
-        // ------------------------------------------------------------ outputs (KEEP: U)
-        const int dv = 32 * (warp & 3) + lane;
-        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        for (int ch = 0; ch < nchunks; ++ch) {
-            const int st = ch % STAGES, valid = min(CH, span.len - ch * CH);
-            if (KEEP) {
-                if (!wait_all(m_u, ch)) break;
-                tc_fence_after();
-                uint8_t *dst = p.U + ((item0 + ch) * a.Hv + hv) * TILE;   // [dv][64 tokens]
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32];
-                    tmem_ld32(at + TM_U + 32 * hf, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
-                        *(uint4 *)(dst + swz(dv, 4 * hf + j)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_free);
-            } else {
-                if (!wait_full(ch) || !wait_all(m_o, ch)) break;
-                tc_fence_after();
-                const float *gam = (const float *)(sm + st * ST_BYTES + ST_G) + GA_GAM;
-                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + (((size_t)span.row0 + ch * CH) * a.Hv + hv) * D + dv;
-                const size_t step = (size_t)a.Hv * D;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32], y[32];
-                    tmem_ld32(at + TM_QS + 32 * hf, x);
-                    tmem_ld32(at + TM_PU + 32 * hf, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float g4[4];
-                        ld4(gam + 32 * hf + e, g4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (32 * hf + e + i < valid)
-                                dst[(32 * hf + e + i) * step] =
-                                    __float2bfloat16_rn(g4[i] * __uint_as_float(x[e + i]) + __uint_as_float(y[e + i]));
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(b_free);
-                    mbar_arrive(&empty[st]);
-                }
-            }
-        }
     } else {
-        // ------------------------------------------------------------ the chain
+        // ------------------------------------------------------------ the chain, and the outputs
         const int grp = warp >> 2, lq = warp & 3, dv = 32 * lq + lane;
         const uint32_t at = tmem + ((uint32_t)(32 * lq) << 16);
-        const int r0 = 64 * grp;                     // state rows of the thread: r0 .. r0 + 63 of column dv
+        const int r0 = 32 * grp, t0 = 16 * grp;      // the thread's state rows r0 .. + 31 and tokens t0 .. + 15 of column dv
         auto arrive = [&](uint64_t *bar) {           // after the writes to tensor memory
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        auto put_tokens = [&](uint32_t to, const float(&x)[16]) {
+            uint32_t h[8], l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
+            tmem_st8(to, h);
+            tmem_st8(to + 8, l);
+        };
         {
             const int page = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
             const float *src = a.s0 + (((size_t)max(page, 0) * a.Hv + hv) * D + r0) * D + dv;
+            uint32_t x[32];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t x[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = page >= 0 ? __float_as_uint(src[(size_t)(32 * hf + e) * D]) : 0u;
-                tmem_st32(at + TM_S + r0 + 32 * hf, x);
-            }
+            for (int e = 0; e < 32; ++e) x[e] = page >= 0 ? __float_as_uint(src[(size_t)e * D]) : 0u;
+            tmem_st32(at + TM_S + r0, x);
             tmem_wait_st();                          // each thread reads back what it wrote itself
         }
         bool ok = true;
@@ -464,91 +383,107 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!(ok = wait_all(m_s, ch - 1))) break;
                 tc_fence_after();
             }
+            uint32_t S[32];
+            tmem_ld32(at + TM_S + r0, S);
+            tmem_wait_ld();
             {
-                uint32_t x[2][32], h[16];
-                tmem_ld32(at + TM_S + r0, x[0]);
-                tmem_wait_ld();
-                tmem_ld32(at + TM_S + r0 + 32, x[1]);
+                uint32_t h[16], l[16];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (hf) tmem_wait_ld();
-                    float y[32];
+                for (int e = 0; e < 16; ++e) split2(__uint_as_float(S[2 * e]), __uint_as_float(S[2 * e + 1]), h[e], l[e]);
+                tmem_st16(at + TM_SHL + (r0 >> 1), h);
+                tmem_st16(at + TM_SHL + 64 + (r0 >> 1), l);
+                arrive(b_s);
+                if (KEEP) {                          // [dv][state row]
+                    uint8_t *dst = p.S + (((item0 + ch) * a.Hv + hv) * 2 + (grp >> 1)) * TILE;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[hf][e]);
-                    put_hl(at + TM_SHL + (r0 >> 1) + 16 * hf, at + TM_SHL + 64 + (r0 >> 1) + 16 * hf, y, h);
-                    if (KEEP) {                      // [dv][state row]
-                        uint8_t *dst = p.S + (((item0 + ch) * a.Hv + hv) * 2 + grp) * TILE;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *(uint4 *)(dst + swz(dv, 4 * hf + j)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        *(uint4 *)(dst + swz(dv, 4 * (grp & 1) + j)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
                 }
             }
-            arrive(b_s);
             if (!(ok = wait_full(ch))) break;
-            const float gC = gates[GA_GAM + CH - 1];
+            {                                        // the state decayed, in the shadow of the product
+                const float gC = gates[GA_GAM + CH - 1];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {         // the state decayed, in the shadow of the product
-                uint32_t x[32];
-                tmem_ld32(at + TM_S + r0 + 32 * hf, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(gC * __uint_as_float(x[e]));
-                tmem_st32(at + TM_S + r0 + 32 * hf, x);
+                for (int e = 0; e < 32; ++e) S[e] = __float_as_uint(gC * __uint_as_float(S[e]));
+                tmem_st32(at + TM_S + r0, S);
             }
-            // V^T: column dv of the group's 32 tokens
-            float r[32];
+            // beta V^T: column dv of the thread's tokens
+            float r[16], w[16];
             {
-                const uint8_t *vt = s + ST_V + (dv >> 6) * (TILE / 2) + grp * 32 * 128 + 2 * (dv & 7);
+                const uint8_t *vt = s + ST_V + (dv >> 6) * (TILE / 2) + t0 * 128 + 2 * (dv & 7);
                 const int j = (dv & 63) >> 3;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float f = __bfloat162float(*(const __nv_bfloat16 *)(vt + e * 128 + ((j ^ (e & 7)) << 4)));
-                    r[e] = 32 * grp + e < valid ? f : 0.0f;
+                for (int e = 0; e < 16; e += 4) {
+                    float b4[4], c4[4];
+                    ld4(gates + GA_BETA + t0 + e, b4);
+                    ld4(gates + GA_BG + t0 + e, c4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = __bfloat162float(*(const __nv_bfloat16 *)(vt + (e + i) * 128 + ((j ^ ((e + i) & 7)) << 4)));
+                        r[e + i] = t0 + e + i < valid ? b4[i] * f : 0.0f;
+                        w[e + i] = c4[i];
+                    }
                 }
             }
             if (!(ok = wait_all(m_x, ch))) break;
             tc_fence_after();
             {
-                uint32_t x[32], h[16];
-                tmem_ld32(at + TM_X + 32 * grp, x);
+                uint32_t x[16];
+                tmem_ld16(at + TM_X + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float b4[4], c4[4];
-                    ld4(gates + GA_BETA + 32 * grp + e, b4);
-                    ld4(gates + GA_BG + 32 * grp + e, c4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[e + i] = b4[i] * r[e + i] - c4[i] * __uint_as_float(x[e + i]);
-                }
-                put_hl(at + TM_X + 32 * grp, at + TM_X + 32 * grp + 16, r, h);
+                for (int e = 0; e < 16; ++e) r[e] -= w[e] * __uint_as_float(x[e]);
+                put_tokens(at + TM_X + t0, r);
             }
             arrive(b_r);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) ld4(gates + GA_LAM + t0 + e, *(float(*)[4])(w + e));
             if (!(ok = wait_all(m_u, ch))) break;
             tc_fence_after();
             {
-                uint32_t x[32], h[16];
-                tmem_ld32(at + TM_U + 32 * grp, x);
+                uint32_t x[16];
+                tmem_ld16(at + TM_U + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float l4[4];
-                    ld4(gates + GA_LAM + 32 * grp + e, l4);
+                for (int e = 0; e < 16; ++e) r[e] = w[e] * __uint_as_float(x[e]);
+                put_tokens(at + TM_X + t0, r);       // R has been read: U's product is done
+                arrive(b_u);
+                if (KEEP) {                          // [dv][token]
+                    uint8_t *dst = p.U + ((item0 + ch) * a.Hv + hv) * TILE;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) r[e + i] = l4[i] * __uint_as_float(x[e + i]);
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
+                        *(uint4 *)(dst + swz(dv, 2 * grp + j)) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
-                const uint32_t to = at + (KEEP ? TM_X : TM_U) + 32 * grp;
-                put_hl(to, to + 16, r, h);
             }
-            arrive(b_u);
+            if (!KEEP) {                             // outputs, under the state's product
+                uint32_t x[16], y[16];
+                tmem_ld16(at + TM_QS + t0, x);
+                tmem_ld16(at + TM_PU + t0, y);
+                tmem_wait_ld();
+                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + (((size_t)span.row0 + ch * CH + t0) * a.Hv + hv) * D + dv;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    float g4[4];
+                    ld4(gates + GA_GAM + t0 + e, g4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t0 + e + i < valid)
+                            dst[(size_t)((e + i) * a.Hv) * D] =
+                                __float2bfloat16_rn(g4[i] * __uint_as_float(x[e + i]) + __uint_as_float(y[e + i]));
+                }
+            }
+            __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
         if (!KEEP && a.sT) {
-            if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) {
-                tc_fence_after();
-            }
+            if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             const int page = page_of(a.sT_index, n, a.pages, a.err);
-            bool keep = page >= 0 && ok && !*abort_flag;
+            bool keep = page >= 0 && ok;
             if (page >= 0 && (a.sT_index || (a.s0_index && a.sT == a.s0))) {
                 bool clash = false;       // as page_is_free, a warp at a time
                 for (int j = lane; j < a.N; j += 32) {
@@ -562,14 +497,11 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (keep) {
                 float *dst = a.sT + (((size_t)page * a.Hv + hv) * D + r0) * D + dv;
+                uint32_t x[32];
+                tmem_ld32(at + TM_S + r0, x);
+                tmem_wait_ld();
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32];
-                    tmem_ld32(at + TM_S + r0 + 32 * hf, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) dst[(size_t)(32 * hf + e) * D] = __uint_as_float(x[e]);
-                }
+                for (int e = 0; e < 32; ++e) dst[(size_t)e * D] = __uint_as_float(x[e]);
             }
         }
     }
