@@ -41,6 +41,7 @@ bool gdr_tc_shape(int dk, int dv, IoType io);
 bool gdr_tc_available();
 size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward);
 cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s);
+cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s);
 
 struct GdrDecodeArgs {
     const void *q, *k, *v, *g, *beta;   // io [N, T, Hk, dk], ..., [N, T, Hv]

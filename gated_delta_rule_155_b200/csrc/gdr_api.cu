@@ -36,12 +36,12 @@ kda_status_t check_dims(int N, int T, int Hk, int Hv, int dk, int dv, kda_dtype_
 }
 
 // bf16 at dk = dv = 128 runs on the tensor cores and nowhere else
-bool on_tensor_cores(int dk, int dv, kda_dtype_t io, bool backward) { return !backward && kda::gdr_tc_shape(dk, dv, io_of(io)); }
+bool on_tensor_cores(int dk, int dv, kda_dtype_t io) { return kda::gdr_tc_shape(dk, dv, io_of(io)); }
 
 size_t workspace_bytes_of(int N, int T, int Hk, int Hv, int dk, int dv, kda_dtype_t io, bool backward)
 {
     if (T == 0) return 0;
-    return on_tensor_cores(dk, dv, io, backward) ? kda::gdr_tc_workspace(N, T, Hk, Hv, backward)
+    return on_tensor_cores(dk, dv, io) ? kda::gdr_tc_workspace(N, T, Hk, Hv, backward)
                                                  : kda::gdr_simt_workspace(N, T, Hk, Hv, dk, dv, backward);
 }
 
@@ -99,7 +99,7 @@ kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const 
     if (st != KDA_OK) return st;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, initial_index, out, final_state, final_index, pages, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word()};
-    if (on_tensor_cores(dk, dv, io, false)) {
+    if (on_tensor_cores(dk, dv, io)) {
         if (!kda::gdr_tc_available()) return KDA_ERR_UNSUPPORTED;
         return cuda_status(kda::launch_gdr_forward_tc(a, (cudaStream_t)stream));
     }
@@ -124,6 +124,10 @@ kda_status_t kda_gdr_backward(const void *q, const void *k, const void *v, const
     kda::GdrArgs a{q, k, v, g, beta, initial_state, nullptr, nullptr, nullptr, nullptr, 0, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word(),
                    d_out, d_final_state, d_q, d_k, d_v, d_g, d_beta, d_initial_state};
+    if (on_tensor_cores(dk, dv, io)) {
+        if (!kda::gdr_tc_available()) return KDA_ERR_UNSUPPORTED;
+        return cuda_status(kda::launch_gdr_backward_tc(a, (cudaStream_t)stream));
+    }
     return cuda_status(kda::launch_gdr_backward_simt(a, (cudaStream_t)stream));
 }
 

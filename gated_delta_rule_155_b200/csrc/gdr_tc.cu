@@ -202,15 +202,8 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------- the walk
-// shared memory: stages of {K; Q tiles 32 KB, V tiles 16 KB, [M; P M] hi + lo 32 KB, gates 1 KB}
-constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT_GATES, ST_BYTES = ST_G + 1024;
-constexpr int STAGES = 2;
-constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
-static_assert(W_BYTES <= 232448, "shared memory per block");
 // tensor memory columns: S (fp32), S as an operand (hi, lo), X then R, Q S, U, P U
 constexpr int TM_S = 0, TM_SHL = 128, TM_X = 256, TM_QS = 320, TM_U = 384, TM_PU = 448;
-// warps: 4 g .. 4 g + 3, g < 4: tokens 16 g .. and state rows 32 g .. of the chain; 16 the copies, 17 the MMAs
-constexpr int W_THREADS = 576;
 
 // KEEP: leaves each chunk's start state and U for the gradients, and writes no output and no final state
 template <bool KEEP>
@@ -357,13 +350,6 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
-        };
-        auto put_tokens = [&](uint32_t to, const float(&x)[16]) {
-            uint32_t h[8], l[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
-            tmem_st8(to, h);
-            tmem_st8(to + 8, l);
         };
         {
             const int page = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
@@ -518,36 +504,62 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 bool gdr_tc_shape(int dk, int dv, IoType io) { return io == IO_BF16 && dk == D && dv == D; }
 bool gdr_tc_available() { return device_is_sm100() && tensor_maps_available(); }
 
+// items; then 1 KB aligned: for the gradients S, U, dS, H; the sequences' order
 size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
 {
     (void)Hk;
     const size_t items = (size_t)gdr_slots(N, T) * Hv;
-    return backward ? 0 : items * IT_BYTES + 4 * (size_t)N;
+    return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + 4 * (size_t)N;
 }
 
-cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
+void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
 {
-    struct TagP; struct TagW;
     const WaitHooks hk = wait_hooks();
-    TcP p{};
+    const size_t items = (size_t)gdr_slots(a.N, a.T) * a.Hv;
+    p = TcP{};
     p.a = a;
     p.items = (uint8_t *)a.ws;
+    uint8_t *at = p.items + items * IT_BYTES;
+    if (backward) {
+        p.S = at; at += items * 2 * TILE;
+        p.dS = at; at += items * 2 * TILE;
+        p.U = at; at += items * TILE;
+        p.H = at; at += items * TILE;
+    }
+    if (a.T > 0 && a.cu && a.N > 1) p.order = (int *)at;
     p.wait_ns = hk.wait_ns;
     p.skip_load_chunk = hk.skip_load_chunk;
+}
+
+cudaError_t launch_gdr_prep_walk_tc(const TcP &p, bool keep, cudaStream_t s)
+{
+    struct TagP; struct TagW; struct TagK;
+    const GdrArgs &a = p.a;
     CUtensorMap mq{}, mk{}, mv{};
     cudaError_t e;
     if (a.T > 0) {
         if (!make_tile_map(&mq, a.q, 1, a.T, a.Hk, CH) || !make_tile_map(&mk, a.k, 1, a.T, a.Hk, CH) ||
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
-        const size_t slots = (size_t)gdr_slots(a.N, a.T);
-        if (a.cu && a.N > 1) p.order = (int *)(p.items + slots * a.Hv * IT_BYTES);
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        gdr_prep_tc_kernel<<<dim3((unsigned)slots, a.Hv + (p.order ? 1 : 0)), 256, PR_BYTES, s>>>(mq, mk, p);
+        gdr_prep_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), 256, PR_BYTES, s>>>(mq, mk, p);
     }
-    if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel<false>, W_BYTES)) != cudaSuccess) return e;
-    gdr_walk_tc_kernel<false><<<(unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
+    const unsigned blocks = (unsigned)(a.N * a.Hv);
+    if (keep) {
+        if ((e = smem_opt_in<TagK>((const void *)gdr_walk_tc_kernel<true>, W_BYTES)) != cudaSuccess) return e;
+        gdr_walk_tc_kernel<true><<<blocks, W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
+    } else {
+        if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel<false>, W_BYTES)) != cudaSuccess) return e;
+        gdr_walk_tc_kernel<false><<<blocks, W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
+    }
     return cudaGetLastError();
+}
+
+cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
+{
+    TcP p;
+    gdr_tc_plan(a, false, p);
+    return launch_gdr_prep_walk_tc(p, false, s);
 }
 
 }  // namespace kda

@@ -54,5 +54,30 @@ KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
 // issues them; loads that were issued but not waited for) is let finish before its memory is released.
 constexpr unsigned long long DRAIN_NS = 2000000000ull;
 
+// The walks' shared memory: stages of {K; Q tiles 32 KB, V (backward: dO) tiles 16 KB, [M; P M] hi + lo
+// 32 KB, gates 1 KB}.
+constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT_GATES, ST_BYTES = ST_G + 1024;
+constexpr int STAGES = 2;
+constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
+static_assert(W_BYTES <= 232448, "shared memory per block");
+// Their warps: 4 g .. 4 g + 3, g < 4: tokens 16 g .. and state rows 32 g .. of the chain; 16 the copies, 17 the MMAs.
+constexpr int W_THREADS = 576;
+
+// 16 values of a lane (tokens of an A operand's step) as hi + lo words at `to`
+KDA_DEVICE void put_tokens(uint32_t to, const float (&x)[16])
+{
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
+    tmem_st8(to, h);
+    tmem_st8(to + 8, l);
+}
+
 }  // namespace gdr
+
+// Prepares the operand pointers of a call on its workspace; launches prep and the forward walk
+// (keep: of the backward pass).
+void gdr_tc_plan(const GdrArgs &a, bool backward, gdr::TcP &p);
+cudaError_t launch_gdr_prep_walk_tc(const gdr::TcP &p, bool keep, cudaStream_t s);
+
 }  // namespace kda
