@@ -102,11 +102,12 @@ KDA_DEVICE bool page_is_free(const int *sT_index, const int *s0_index, bool same
     return !__syncthreads_or(clash);
 }
 
-// M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats, by 16 x 16 blocks:
-// the diagonal blocks by forward substitution (one column a thread), then block row by block row
-// M_IJ = -M_II sum_{J <= K < I} A_IK M_KJ, every product in fp32, four columns of one row a thread
-// (one 16-byte load of A feeds four of M, 16 FMAs).  `tmp`: 48 rows of LD floats.  256 threads; M's
-// upper triangle is written as zeros.  Ends with a barrier.
+// M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats: the 16 x 16 diagonal blocks
+// by forward substitution (one column a thread: a product form such as (I - A)(I + A^2)... would cancel
+// where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64),
+// every product in fp32.  `tmp`: 32 rows of INV_LT floats.  256 threads; M's upper triangle is written as
+// zeros.  Ends with a barrier.
+constexpr int INV_LT = 36;
 template <int LD>
 KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid)
 {
@@ -128,52 +129,77 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) M[(16 * b + r) * LD + 16 * b + c] = x[r];
-    }
-    {
-        const int r = tid >> 4, c = tid & 15;
-#pragma unroll
-        for (int I = 0; I < 4; ++I)
-#pragma unroll
-            for (int J = I + 1; J < 4; ++J) M[(16 * I + r) * LD + 16 * J + c] = 0.0f;
+    } else {
+        const float z[4] = {};
+        for (int u = tid - 64; u < 6 * 64; u += 192) {   // blocks (0,1) (0,2) (0,3) (1,2) (1,3) (2,3)
+            const int b = u >> 6, I = b < 3 ? 0 : b < 5 ? 1 : 2, J = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
+            st4(M + (16 * I + ((u & 63) >> 2)) * LD + 16 * J + 4 * (u & 3), z);
+        }
     }
     __syncthreads();
-    const int J = tid >> 6, r = (tid & 63) >> 2, c = 4 * (tid & 3);
+    {   // 16 -> 32, two pairs of blocks: two columns a thread
+        const int o = 32 * (tid >> 7), r = (tid & 127) >> 3, c = 2 * (tid & 7);
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int I = 1; I < 4; ++I) {
-        if (J < I) {
-            float s[4] = {};
-            for (int m = 16 * J; m < 16 * I; m += 4) {
-                float a[4];
-                ld4(A + (16 * I + r) * LD + m, a);
+        for (int m = 0; m < 16; m += 4) {
+            float a[4];
+            ld4(A + (o + 16 + r) * LD + o + m, a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float b[4];
-                    ld4(M + (m + e) * LD + 16 * J + c, b);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] += a[e] * b[j];
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 b = *(const float2 *)(M + (o + m + e) * LD + o + c);
+                s0 += a[e] * b.x;
+                s1 += a[e] * b.y;
             }
-            st4(tmp + (16 * J + r) * LD + c, s);
         }
+        float *t = tmp + (o >> 1) * INV_LT;
+        *(float2 *)(t + r * INV_LT + c) = make_float2(s0, s1);
         __syncthreads();
-        if (J < I) {
-            float s[4] = {};
+        s0 = s1 = 0.0f;
 #pragma unroll
-            for (int m = 0; m < 16; m += 4) {
-                float a[4];
-                ld4(M + (16 * I + r) * LD + 16 * I + m, a);
+        for (int m = 0; m < 16; m += 4) {
+            float a[4];
+            ld4(M + (o + 16 + r) * LD + o + 16 + m, a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float b[4];
-                    ld4(tmp + (16 * J + m + e) * LD + c, b);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] -= a[e] * b[j];
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 b = *(const float2 *)(t + (m + e) * INV_LT + c);
+                s0 -= a[e] * b.x;
+                s1 -= a[e] * b.y;
             }
-            st4(M + (16 * I + r) * LD + 16 * J + c, s);
         }
-        __syncthreads();
+        *(float2 *)(M + (o + 16 + r) * LD + o + c) = make_float2(s0, s1);
     }
+    __syncthreads();
+    {   // 32 -> 64: four columns a thread
+        const int r = tid >> 3, c = 4 * (tid & 7);
+        float s[4] = {};
+        for (int m = c; m < 32; m += 4) {        // M is lower
+            float a[4];
+            ld4(A + (32 + r) * LD + m, a);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float b[4];
+                ld4(M + (m + e) * LD + c, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] += a[e] * b[j];
+            }
+        }
+        st4(tmp + r * INV_LT + c, s);
+        __syncthreads();
+        float x[4] = {};
+        for (int m = 0; m <= r; m += 4) {
+            float a[4];
+            ld4(M + (32 + r) * LD + 32 + m, a);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float b[4];
+                ld4(tmp + (m + e) * INV_LT + c, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] -= a[e] * b[j];
+            }
+        }
+        st4(M + (32 + r) * LD + c, x);
+    }
+    __syncthreads();
 }
 
 }  // namespace gdr

@@ -26,11 +26,13 @@ namespace {
 using namespace gdr;
 
 // ---------------------------------------------------------------- prep
+// Shared memory: K; Q tiles, then, once their product is done, P (hi, lo) and M (fp32) in their place;
+// A (fp32) and the inverse's scratch, then the item [M; P M] (hi, lo) in their place.
 constexpr int LM = 68;
-constexpr int PR_KQ = 0, PR_M = 0, PR_TMP = 64 * LM * 4;
-constexpr int PR_A = 2 * TILE, PR_P = PR_A + 64 * LM * 4, PR_G = PR_P + 64 * LM * 4;
-constexpr int PR_BYTES = PR_G + 6 * 256 + 64 + 1024;
-static_assert(PR_TMP + 48 * LM * 4 <= 2 * TILE, "M and its scratch take K's and Q's place");
+constexpr int PR_KQ = 0, PR_P = 0, PR_M = TILE, PR_OUT = 34 * 1024, PR_A = PR_OUT, PR_TMP = PR_A + 64 * LM * 4;
+constexpr int PR_G = PR_OUT + 2 * TILE;
+constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
+static_assert(PR_M + 64 * LM * 4 <= PR_OUT && PR_TMP + 32 * INV_LT * 4 <= PR_G, "regions");
 
 // order[r] <- the sequence whose length is the r-th longest: the walks start with the longest.  A warp a sequence.
 KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
@@ -61,10 +63,10 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *A = (float *)(sm + PR_A), *Pm = (float *)(sm + PR_P), *M = (float *)(sm + PR_M), *tmp = (float *)(sm + PR_TMP);
+    float *A = (float *)(sm + PR_A), *M = (float *)(sm + PR_M), *tmp = (float *)(sm + PR_TMP);
     float *graw = (float *)(sm + PR_G), *ghi = graw + 64, *glo = ghi + 64, *beta = glo + 64;
-    uint64_t *bars = (uint64_t *)(sm + PR_G + 6 * 256);   // tiles, MMA
-    uint32_t *tslot = (uint32_t *)(bars + 2);
+    uint64_t *bars = (uint64_t *)(sm + PR_G + 4 * 256);   // tiles, [K; Q] K^T, P M
+    uint32_t *tslot = (uint32_t *)(bars + 3);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
@@ -72,6 +74,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
+        mbar_init(&bars[2], 1);
         *abort_flag = 0;
         fence_mbar_init();
         mbar_arrive_expect_tx(&bars[0], 2 * TILE);
@@ -122,71 +125,92 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     if (tid == 0 && !*abort_flag) mbar_wait_bounded(&bars[1], 0, abort_flag, a.err, p.wait_ns);
     __syncthreads();
-    const bool ok = !*abort_flag;
+    bool ok = !*abort_flag;
+    const int lq = warp & 3, r = 32 * lq + lane, half = warp >> 2, s0 = 32 * half;   // lane of tensor memory, 32 of its columns
+    const uint32_t at = tmem + ((uint32_t)(32 * lq) << 16) + s0;
     if (ok) {
         tc_fence_after();
-        // thread: row r of [K; Q] K^T, 32 of its columns
-        const int r = 32 * (warp & 3) + lane, t = r & 63, half = warp >> 2, s0 = 32 * half;
-        float *dst = (r < 64 ? A : Pm) + t * LM + s0;
+        const int t = r & 63;
         const int last = t >= valid ? -1 : r < 64 ? t - 1 : t;   // A is strictly lower; rows behind the end may hold NaN
-        if (s0 > 32 * (warp & 1) + 31) {       // the warp's rows all end before its columns
+        float y[32];
+        if (s0 > 32 * (lq & 1) + 31) {         // the warp's rows all end before its columns
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *(float4 *)(dst + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = 0; e < 32; ++e) y[e] = 0.0f;
         } else {
             uint32_t x[32];
-            tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + s0, x);
+            tmem_ld32(at, x);
             tmem_wait_ld();
             const float gh = ghi[t], gl = glo[t], scale = r < 64 ? beta[t] : 1.0f;
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-                float y[4];
+                float h4[4], l4[4];
+                ld4(ghi + s0 + e, h4);
+                ld4(glo + s0 + e, l4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int s = s0 + e + i;
-                    const float d = __expf((gh - ghi[s]) + (gl - glo[s]));
-                    y[i] = s <= last ? scale * d * __uint_as_float(x[e + i]) : 0.0f;
+                    const float d = __expf((gh - h4[i]) + (gl - l4[i]));
+                    y[e + i] = s0 + e + i <= last ? scale * d * __uint_as_float(x[e + i]) : 0.0f;
                 }
-                st4(dst + e, y);
             }
+        }
+        if (r < 64) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) st4(A + t * LM + s0 + e, *(const float(*)[4])(y + e));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                put_split(sm + PR_P, sm + PR_P + TILE / 2, t, 4 * half + j, *(const float(*)[8])(y + 8 * j));
+            fence_proxy_async();
         }
         tc_fence_before();
     }
-    __syncthreads();   // K and Q are consumed (the MMA is done)
+    __syncthreads();
     if (ok) {
         unit_lower_inverse<LM>(A, M, tmp, tid);
-        // [M; P M] as hi + lo; P M's lower triangle: k runs from its column to its row
-        const int ty = tid >> 4, tx = tid & 15;
-        float pm[4][4] = {};
-        if (tx <= ty)
-            for (int k = 4 * tx; k < 4 * ty + 4; k += 4) {
-                float x[4][4];
+        {                                      // M as hi + lo
+            const int t = tid >> 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ld4(Pm + (4 * ty + i) * LM + k, x[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float y[4];
-                    ld4(M + (k + e) * LM + 4 * tx, y);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) pm[i][j] += x[i][e] * y[j];
-                }
+            for (int j = 0; j < 2; ++j) {
+                float y[8];
+                ld4(M + t * LM + 16 * (tid & 3) + 8 * j, *(float(*)[4])y);
+                ld4(M + t * LM + 16 * (tid & 3) + 8 * j + 4, *(float(*)[4])(y + 4));
+                put_split(sm + PR_OUT, sm + PR_OUT + IT_LO, t, 2 * (tid & 3) + j, y);
             }
+        }
+        fence_proxy_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && ok) {                      // P M, rows 64.. of A (M) give lanes that are not read
+        tc_fence_after();
+        const uint32_t pp = smem_u32(sm + PR_P), mm = smem_u32(sm + PR_OUT);
+        constexpr uint32_t id = idesc_bf16(128, 64, false, true);
+        for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ph = sdesc(pp + kk * 32, 16, 1024), pl = sdesc(pp + TILE / 2 + kk * 32, 16, 1024);
+            const uint64_t mh = sdesc(mm + kk * 2048, TILE / 2, 1024), ml = sdesc(mm + IT_LO + kk * 2048, TILE / 2, 1024);
+            mma_ss(tmem, ph, mh, id, kk > 0);
+            mma_ss(tmem, pl, mh, id, 1);
+            mma_ss(tmem, ph, ml, id, 1);
+        }
+        mma_commit(&bars[2]);
+        mbar_wait_bounded(&bars[2], 0, abort_flag, a.err, p.wait_ns);
+    }
+    __syncthreads();
+    ok = ok && !*abort_flag;
+    if (ok) {
+        tc_fence_after();
+        if (r < 64) {
+            uint32_t x[32];
+            tmem_ld32(at, x);
+            tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * ty + i;
-            const uint32_t off = swz(t, tx >> 1) + 8 * (tx & 1);
-            float m[4];
-            ld4(M + t * LM + 4 * tx, m);
-            uint2 hi, lo;
-            split2(m[0], m[1], hi.x, lo.x);
-            split2(m[2], m[3], hi.y, lo.y);
-            *(uint2 *)(item + off) = hi;
-            *(uint2 *)(item + IT_LO + off) = lo;
-            split2(pm[i][0], pm[i][1], hi.x, lo.x);
-            split2(pm[i][2], pm[i][3], hi.y, lo.y);
-            *(uint2 *)(item + TILE / 2 + off) = hi;
-            *(uint2 *)(item + IT_LO + TILE / 2 + off) = lo;
+            for (int j = 0; j < 4; ++j) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[8 * j + e]);
+                put_split(sm + PR_OUT + TILE / 2, sm + PR_OUT + IT_LO + TILE / 2, r, 4 * half + j, y);
+            }
+            fence_proxy_async();
         }
     } else if (tid == 0) {
         mbar_wait_timed(&bars[0], 0, DRAIN_NS);   // the tiles, if they are still on their way
@@ -195,6 +219,11 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 32 && ok) {
+        bulk_store(item, sm + PR_OUT, 2 * TILE);
+        bulk_commit();
+        bulk_wait_read_all();
+    }
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 64);

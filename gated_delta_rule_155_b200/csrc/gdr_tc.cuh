@@ -37,6 +37,11 @@ KDA_DEVICE void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *
                      smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+KDA_DEVICE void bulk_store(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
 KDA_DEVICE void mbar_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -48,6 +53,19 @@ KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
     hi = pack_bf16x2(x0, x1);
     const float2 h = unpack_bf16x2(hi);
     lo = pack_bf16x2(x0 - h.x, x1 - h.y);
+}
+
+// 8 values of a row -> the row's 16-byte pieces of a hi and a lo tile
+KDA_DEVICE void put_split(uint8_t *hi, uint8_t *lo, int row, int j, const float (&x)[8])
+{
+    uint4 h, l;
+    split2(x[0], x[1], h.x, l.x);
+    split2(x[2], x[3], h.y, l.y);
+    split2(x[4], x[5], h.z, l.z);
+    split2(x[6], x[7], h.w, l.w);
+    const uint32_t off = swz(row, j);
+    *(uint4 *)(hi + off) = h;
+    *(uint4 *)(lo + off) = l;
 }
 
 // What a block has in flight when a bounded wait has given up (MMAs, by one commit of the thread that
