@@ -24,17 +24,24 @@ KDA_DEVICE SeqSpan span_of(const int *cu, int n, int N, int T)
 // The first chunk slot of a sequence.
 KDA_DEVICE int slot_base(int row0, int n) { return row0 / CH + n; }
 
-// The sequence and chunk of a slot; false for a slot that no chunk has.
+// The sequence and chunk of a slot; false for a slot that no chunk has.  By whole warps: 32 sequences are
+// looked at a time, so that a search is one round of loads for 32 sequences, two for 1024.
 KDA_DEVICE bool find_slot(const int *cu, int N, int T, int slot, int &n, int &c, SeqSpan &span)
 {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {   // last n with slot_base <= slot
-        const int mid = (lo + hi + 1) >> 1;
-        if (slot_base(span_of(cu, mid, N, T).row0, mid) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = N, step, k;    // the last sequence with slot_base <= slot is in [lo, lo + len)
+    SeqSpan mine;
+    do {
+        step = (len + 31) / 32;
+        const int i = lane * step;
+        mine = span_of(cu, lo + min(i, len - 1), N, T);
+        k = 31 - __clz(__ballot_sync(0xffffffffu, i < len && slot_base(mine.row0, lo + i) <= slot) | 1u);
+        lo += k * step;
+        len = min(step, len - k * step);
+    } while (len > 1);
     n = lo;
-    span = span_of(cu, n, N, T);
+    span.row0 = __shfl_sync(0xffffffffu, mine.row0, k);
+    span.len = __shfl_sync(0xffffffffu, mine.len, k);
     c = slot - slot_base(span.row0, n);
     return c >= 0 && c * CH < span.len;
 }
@@ -105,12 +112,12 @@ KDA_DEVICE bool page_is_free(const int *sT_index, const int *s0_index, bool same
 // M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats: the 16 x 16 diagonal blocks
 // by forward substitution (one column a thread: a product form such as (I - A)(I + A^2)... would cancel
 // where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64),
-// every product in fp32.  `tmp`: 32 rows of INV_LT floats.  256 threads; M's upper triangle is written as
-// zeros.  Ends with a barrier.
-constexpr int INV_LT = 36;
+// every product in fp32.  A's upper right quarter is scratch.  256 threads; M's upper triangle is written
+// as zeros.  Ends with a barrier.
 template <int LD>
-KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid)
+KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
 {
+    float *tmp = A + 32;   // rows 0..31, columns 32..63
     if (tid < 64) {
         const int b = tid >> 4, c = tid & 15;
         float x[16];
@@ -151,8 +158,8 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
                 s1 += a[e] * b.y;
             }
         }
-        float *t = tmp + (o >> 1) * INV_LT;
-        *(float2 *)(t + r * INV_LT + c) = make_float2(s0, s1);
+        float *t = tmp + (o >> 1) * LD;
+        *(float2 *)(t + r * LD + c) = make_float2(s0, s1);
         __syncthreads();
         s0 = s1 = 0.0f;
 #pragma unroll
@@ -161,7 +168,7 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
             ld4(M + (o + 16 + r) * LD + o + 16 + m, a);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 b = *(const float2 *)(t + (m + e) * INV_LT + c);
+                const float2 b = *(const float2 *)(t + (m + e) * LD + c);
                 s0 -= a[e] * b.x;
                 s1 -= a[e] * b.y;
             }
@@ -172,7 +179,8 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
     {   // 32 -> 64: four columns a thread
         const int r = tid >> 3, c = 4 * (tid & 7);
         float s[4] = {};
-        for (int m = c; m < 32; m += 4) {        // M is lower
+#pragma unroll
+        for (int m = 0; m < 32; m += 4) {        // every lane at the same row of M: one wavefront a load, zeros included
             float a[4];
             ld4(A + (32 + r) * LD + m, a);
 #pragma unroll
@@ -183,16 +191,16 @@ KDA_DEVICE void unit_lower_inverse(const float *A, float *M, float *tmp, int tid
                 for (int j = 0; j < 4; ++j) s[j] += a[e] * b[j];
             }
         }
-        st4(tmp + r * INV_LT + c, s);
+        st4(tmp + r * LD + c, s);
         __syncthreads();
         float x[4] = {};
-        for (int m = 0; m <= r; m += 4) {
+        for (int m = 0; m <= (r | 3); m += 4) {  // a warp has four rows
             float a[4];
             ld4(M + (32 + r) * LD + 32 + m, a);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float b[4];
-                ld4(tmp + (m + e) * INV_LT + c, b);
+                ld4(tmp + (m + e) * LD + c, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] -= a[e] * b[j];
             }

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
     extern __shared__ float sm[];
     constexpr int LK = DK + 4;
     float *K = sm, *Q = K + CH * LK, *A = Q + CH * LK, *Pm = A + CH * LM;
-    float *M = K, *tmp = Q;   // K and Q are read only by the Gram products
+    float *M = K;             // K and Q are read only by the Gram products
     __shared__ Gates gs;
     const int tid = threadIdx.x, hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
     const size_t row0 = (size_t)span.row0 + c * CH;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
             Pm[t * LM + s] = s <= t ? d * qk[i][j] : 0.0f;
         }
     __syncthreads();
-    unit_lower_inverse<LM>(A, M, tmp, tid);
+    unit_lower_inverse<LM>(A, M, tid);
     const size_t item = (size_t)blockIdx.x * a.Hv + hv;
     float pm[4][4] = {};
     mm_nn<CH>(pm, Pm + 4 * ty * LM, LM, M + 4 * tx, LM);

@@ -26,13 +26,12 @@ namespace {
 using namespace gdr;
 
 // ---------------------------------------------------------------- prep
-// Shared memory: K; Q tiles, then, once their product is done, P (hi, lo) and M (fp32) in their place;
-// A (fp32) and the inverse's scratch, then the item [M; P M] (hi, lo) in their place.
+// Shared memory: K; Q tiles; once their product is done, P (hi, lo; later P M) and M (fp32) in their
+// place.  A (fp32), later M (hi, lo).  53 KB, so that four blocks share an SM.
 constexpr int LM = 68;
-constexpr int PR_KQ = 0, PR_P = 0, PR_M = TILE, PR_OUT = 34 * 1024, PR_A = PR_OUT, PR_TMP = PR_A + 64 * LM * 4;
-constexpr int PR_G = PR_OUT + 2 * TILE;
+constexpr int PR_KQ = 0, PR_P = 0, PR_M = TILE, PR_A = 33 * 1024, PR_MHL = PR_A, PR_G = PR_A + 64 * LM * 4;
 constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
-static_assert(PR_M + 64 * LM * 4 <= PR_OUT && PR_TMP + 32 * INV_LT * 4 <= PR_G, "regions");
+static_assert(PR_M + 64 * LM * 4 <= PR_A && PR_MHL + TILE <= PR_G && PR_BYTES <= 57344, "regions");
 
 // order[r] <- the sequence whose length is the r-th longest: the walks start with the longest.  A warp a sequence.
 KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
@@ -50,7 +49,7 @@ KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
     }
 }
 
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 4)
 gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
 {
     const GdrArgs &a = p.a;
@@ -63,7 +62,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *A = (float *)(sm + PR_A), *M = (float *)(sm + PR_M), *tmp = (float *)(sm + PR_TMP);
+    float *A = (float *)(sm + PR_A), *M = (float *)(sm + PR_M);
     float *graw = (float *)(sm + PR_G), *ghi = graw + 64, *glo = ghi + 64, *beta = glo + 64;
     uint64_t *bars = (uint64_t *)(sm + PR_G + 4 * 256);   // tiles, [K; Q] K^T, P M
     uint32_t *tslot = (uint32_t *)(bars + 3);
@@ -132,49 +131,54 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         const int t = r & 63;
         const int last = t >= valid ? -1 : r < 64 ? t - 1 : t;   // A is strictly lower; rows behind the end may hold NaN
-        float y[32];
-        if (s0 > 32 * (lq & 1) + 31) {         // the warp's rows all end before its columns
+        const float gh = ghi[t], gl = glo[t], scale = r < 64 ? beta[t] : 1.0f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = 0.0f;
-        } else {
-            uint32_t x[32];
-            tmem_ld32(at, x);
-            tmem_wait_ld();
-            const float gh = ghi[t], gl = glo[t], scale = r < 64 ? beta[t] : 1.0f;
+        for (int hf = 0; hf < 2; ++hf) {       // 16 columns at a time
+            const int c0 = s0 + 16 * hf;
+            float y[16];
+            if (c0 > 32 * (lq & 1) + 31) {     // the warp's rows all end before these columns
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float h4[4], l4[4];
-                ld4(ghi + s0 + e, h4);
-                ld4(glo + s0 + e, l4);
+                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
+            } else {
+                uint32_t x[16];
+                tmem_ld16(at + 16 * hf, x);
+                tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float d = __expf((gh - h4[i]) + (gl - l4[i]));
-                    y[e + i] = s0 + e + i <= last ? scale * d * __uint_as_float(x[e + i]) : 0.0f;
+                for (int e = 0; e < 16; e += 4) {
+                    float h4[4], l4[4];
+                    ld4(ghi + c0 + e, h4);
+                    ld4(glo + c0 + e, l4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float d = __expf((gh - h4[i]) + (gl - l4[i]));
+                        y[e + i] = c0 + e + i <= last ? scale * d * __uint_as_float(x[e + i]) : 0.0f;
+                    }
                 }
             }
-        }
-        if (r < 64) {
+            if (r < 64) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) st4(A + t * LM + s0 + e, *(const float(*)[4])(y + e));
-        } else {
+                for (int e = 0; e < 16; e += 4) st4(A + t * LM + c0 + e, *(const float(*)[4])(y + e));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                put_split(sm + PR_P, sm + PR_P + TILE / 2, t, 4 * half + j, *(const float(*)[8])(y + 8 * j));
-            fence_proxy_async();
+                for (int j = 0; j < 2; ++j)
+                    put_split(sm + PR_P, sm + PR_P + TILE / 2, t, c0 / 8 + j, *(const float(*)[8])(y + 8 * j));
+            }
         }
+        fence_proxy_async();
         tc_fence_before();
     }
     __syncthreads();
     if (ok) {
-        unit_lower_inverse<LM>(A, M, tmp, tid);
+        unit_lower_inverse<LM>(A, M, tid);
         {                                      // M as hi + lo
             const int t = tid >> 2;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float y[8];
-                ld4(M + t * LM + 16 * (tid & 3) + 8 * j, *(float(*)[4])y);
-                ld4(M + t * LM + 16 * (tid & 3) + 8 * j + 4, *(float(*)[4])(y + 4));
-                put_split(sm + PR_OUT, sm + PR_OUT + IT_LO, t, 2 * (tid & 3) + j, y);
+                const int q8 = (tid & 3) + 4 * j;      // a quarter of a warp reads 8 different bank groups
+                ld4(M + t * LM + 8 * q8, *(float(*)[4])y);
+                ld4(M + t * LM + 8 * q8 + 4, *(float(*)[4])(y + 4));
+                put_split(sm + PR_MHL, sm + PR_MHL + TILE / 2, t, q8, y);
             }
         }
         fence_proxy_async();
@@ -183,11 +187,11 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     if (tid == 0 && ok) {                      // P M, rows 64.. of A (M) give lanes that are not read
         tc_fence_after();
-        const uint32_t pp = smem_u32(sm + PR_P), mm = smem_u32(sm + PR_OUT);
+        const uint32_t pp = smem_u32(sm + PR_P), mm = smem_u32(sm + PR_MHL);
         constexpr uint32_t id = idesc_bf16(128, 64, false, true);
         for (int kk = 0; kk < 4; ++kk) {
             const uint64_t ph = sdesc(pp + kk * 32, 16, 1024), pl = sdesc(pp + TILE / 2 + kk * 32, 16, 1024);
-            const uint64_t mh = sdesc(mm + kk * 2048, TILE / 2, 1024), ml = sdesc(mm + IT_LO + kk * 2048, TILE / 2, 1024);
+            const uint64_t mh = sdesc(mm + kk * 2048, TILE / 2, 1024), ml = sdesc(mm + TILE / 2 + kk * 2048, TILE / 2, 1024);
             mma_ss(tmem, ph, mh, id, kk > 0);
             mma_ss(tmem, pl, mh, id, 1);
             mma_ss(tmem, ph, ml, id, 1);
@@ -200,15 +204,18 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (ok) {
         tc_fence_after();
         if (r < 64) {
-            uint32_t x[32];
-            tmem_ld32(at, x);
-            tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float y[8];
+            for (int hf = 0; hf < 2; ++hf) {   // over P, which has been read
+                uint32_t x[16];
+                tmem_ld16(at + 16 * hf, x);
+                tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[8 * j + e]);
-                put_split(sm + PR_OUT + TILE / 2, sm + PR_OUT + IT_LO + TILE / 2, r, 4 * half + j, y);
+                for (int j = 0; j < 2; ++j) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[8 * j + e]);
+                    put_split(sm + PR_P, sm + PR_P + TILE / 2, r, 4 * half + 2 * hf + j, y);
+                }
             }
             fence_proxy_async();
         }
@@ -220,7 +227,10 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_before();
     __syncthreads();
     if (tid == 32 && ok) {
-        bulk_store(item, sm + PR_OUT, 2 * TILE);
+        bulk_store(item, sm + PR_MHL, TILE / 2);
+        bulk_store(item + TILE / 2, sm + PR_P, TILE / 2);
+        bulk_store(item + IT_LO, sm + PR_MHL + TILE / 2, TILE / 2);
+        bulk_store(item + IT_LO + TILE / 2, sm + PR_P + TILE / 2, TILE / 2);
         bulk_commit();
         bulk_wait_read_all();
     }
