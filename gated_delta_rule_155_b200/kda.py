@@ -10,6 +10,7 @@ importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -103,22 +104,28 @@ def library():
     return _lib
 
 
+# The marshalling runs before every launch, and a decode kernel takes 4 us: raw pointers as ints (what the
+# argument types convert), the device and stream of torch's C side, and one look at a well-formed tensor.
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
+_IO_CODES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 
 
 def _io_code(dtype):
-    if dtype == torch.float32:
-        return KDA_F32
-    if dtype == torch.bfloat16:
-        return KDA_BF16
-    raise TypeError(f"unsupported io dtype {dtype}")
+    code = _IO_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported io dtype {dtype}")
+    return code
 
 
 def _check(status, where):
@@ -144,6 +151,16 @@ def _need(t, shape, dtype, name, *, allow_none=False):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_all(checks):
+    """_need for each (tensor, shape, dtype, name), with one look at those that are well-formed."""
+    cur = torch._C._cuda_getDevice()
+    for c in checks:
+        t = c[0]
+        if not (isinstance(t, torch.Tensor) and t.get_device() == cur and t.shape == c[1] and t.dtype is c[2]
+                and t.is_contiguous()):
+            _need(*c)
 
 
 def kda_forward_chunked(q, k, v, g, beta, initial_state=None, out=None, final_state=None,
@@ -412,8 +429,8 @@ def _gdr_shapes(q, k, v, g, beta, cu_seqlens):
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
-        N = cu_seqlens.numel() - 1
-        _need(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens")
+        N = cu_seqlens.shape[0] - 1
+        _need_all(((cu_seqlens, (N + 1,), torch.int32, "cu_seqlens"),))
         if q.dim() != 3 or v.dim() != 3:
             raise ValueError("with cu_seqlens, q and v are [T_total, H, d]")
         lead = (q.shape[0],)
@@ -423,11 +440,11 @@ def _gdr_shapes(q, k, v, g, beta, cu_seqlens):
             raise ValueError("without cu_seqlens, q and v are [B, T, H, d]")
         lead = (q.shape[0], q.shape[1])
         N, Tt = q.shape[0], q.shape[0] * q.shape[1]
-    Hk, dk = q.shape[-2:]
-    Hv, dv = v.shape[-2:]
-    for t, s, n in ((q, lead + (Hk, dk), "q"), (k, lead + (Hk, dk), "k"), (v, lead + (Hv, dv), "v"),
-                    (g, lead + (Hv,), "g"), (beta, lead + (Hv,), "beta")):
-        _need(t, s, q.dtype, n)
+    sq, sv, io = q.shape, v.shape, q.dtype
+    (Hk, dk), (Hv, dv) = sq[-2:], sv[-2:]
+    gates = lead + (Hv,)
+    _need_all(((q, lead + (Hk, dk), io, "q"), (k, sq, io, "k"), (v, gates + (dv,), io, "v"), (g, gates, io, "g"),
+               (beta, gates, io, "beta")))
     return N, Tt, Hk, Hv, dk, dv, lead
 
 
@@ -446,13 +463,14 @@ def _paged_state(state, index, N, tail, name):
             raise ValueError(f"{name}_index needs {name}_state")
         return 0
     if index is None:
-        _need(state, (N,) + tail, torch.float32, f"{name}_state")
+        _need_all(((state, (N,) + tail, torch.float32, f"{name}_state"),))
         return 0
-    _need(index, (N,), torch.int32, f"{name}_index")
-    _need(state, (state.shape[0],) + tail, torch.float32, f"{name}_state")
-    return state.shape[0]
+    P = state.shape[0]
+    _need_all(((index, (N,), torch.int32, f"{name}_index"), (state, (P,) + tail, torch.float32, f"{name}_state")))
+    return P
 
 
+@functools.lru_cache(maxsize=256)
 def kda_gdr_workspace_size(N, T_total, Hk, Hv, dk, dv, dtype, *, backward=False):
     n = ctypes.c_size_t(0)
     _check(_lib.kda_gdr_workspace_size(N, T_total, Hk, Hv, dk, dv, _io_code(dtype), int(backward), ctypes.byref(n)),
@@ -475,7 +493,8 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
         raise ValueError(f"initial_state has {p0} pages, final_state {p1}")
     if out is None:
         out = torch.empty(lead + (Hv, dv), dtype=q.dtype, device=q.device)
-    _need(out, lead + (Hv, dv), q.dtype, "out")
+    else:
+        _need_all(((out, lead + (Hv, dv), q.dtype, "out"),))
     if workspace is None:
         workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype), q.device)
     _check(_lib.kda_gdr_forward(
@@ -499,7 +518,8 @@ def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=Non
     for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
         if gr.get(n) is None:
             gr[n] = torch.empty_like(t)
-        _need(gr[n], t.shape, q.dtype, n)
+        else:
+            _need_all(((gr[n], t.shape, q.dtype, n),))
     if workspace is None:
         workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype, backward=True), q.device)
     _check(_lib.kda_gdr_backward(
@@ -518,24 +538,21 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
     one = q.dim() == 3
     if q.dim() not in (3, 4) or v.dim() != q.dim():
         raise ValueError("q and v are [N, T, H, d], or [N, H, d] for one token")
-    lead = tuple(q.shape[:-2])
+    sq, sv, io = q.shape, v.shape, q.dtype
+    lead = sq[:-2]
     N, T = (lead[0], 1) if one else lead
-    Hk, dk = q.shape[-2:]
-    Hv, dv = v.shape[-2:]
-    io = q.dtype
-    for t, s, n in ((q, lead + (Hk, dk), "q"), (k, lead + (Hk, dk), "k"), (v, lead + (Hv, dv), "v"),
-                    (g, lead + (Hv,), "g"), (beta, lead + (Hv,), "beta")):
-        _need(t, s, io, n)
-    if index is None:
-        _need(state, (N, Hv, dk, dv), torch.float32, "state")
-    else:
-        _need(index, (N,), torch.int32, "index")
-        _need(state, (state.shape[0], Hv, dk, dv), torch.float32, "state")
+    (Hk, dk), (Hv, dv) = sq[-2:], sv[-2:]
+    gates = lead + (Hv,)
+    shape = gates + (dv,)
     if out is None:
-        out = torch.empty(lead + (Hv, dv), dtype=io, device=q.device)
-    _need(out, lead + (Hv, dv), io, "out")
+        out = torch.empty(shape, dtype=io, device=q.device)
+    P = N if index is None else state.shape[0]
+    _need_all(((q, lead + (Hk, dk), io, "q"), (k, sq, io, "k"), (v, shape, io, "v"), (g, gates, io, "g"),
+               (beta, gates, io, "beta"), (state, (P, Hv, dk, dv), torch.float32, "state"), (out, shape, io, "out")))
+    if index is not None:
+        _need_all(((index, (N,), torch.int32, "index"),))
     _check(_lib.kda_gdr_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(index),
-                               state.shape[0], _ptr(out), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream)),
+                               P, _ptr(out), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream)),
            "kda_gdr_decode")
     return out
 
@@ -544,7 +561,7 @@ def _cache(cache):
     """(layers, pages, bytes of a page) of a cache [layers, pages, ...] of any dtype."""
     if cache.dim() < 3:
         raise ValueError("cache must be [layers, pages, ...]")
-    _need(cache, cache.shape, cache.dtype, "cache")
+    _need_all(((cache, cache.shape, cache.dtype, "cache"),))
     L, P = cache.shape[:2]
     return L, P, (cache.numel() // max(1, L * P)) * cache.element_size()
 
@@ -552,8 +569,8 @@ def _cache(cache):
 def _ids(t, name):
     if t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D tensor of page numbers")
-    _need(t, t.shape, torch.int32, name)
-    return t.numel()
+    _need_all(((t, t.shape, torch.int32, name),))
+    return t.shape[0]
 
 
 def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
@@ -562,10 +579,9 @@ def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
     Returns their numbers, int32 [n]: -1 where no page is left or the parent is not live."""
     L, P, nbytes = _cache(cache)
     n = _ids(parents, "parents")
-    _need(refs, (P,), torch.int32, "refs")
     if children is None:
         children = torch.empty_like(parents)
-    _need(children, (n,), torch.int32, "children")
+    _need_all(((refs, (P,), torch.int32, "refs"), (children, (n,), torch.int32, "children")))
     _check(_lib.kda_pages_fork(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(parents), _ptr(children), n, _stream(stream)),
            "kda_pages_fork")
     return children
@@ -586,6 +602,7 @@ def kda_pages_free(refs, ids, *, stream=None):
     _check(_lib.kda_pages_free(_ptr(refs), P, _ptr(ids), n, _stream(stream)), "kda_pages_free")
 
 
+@functools.lru_cache(maxsize=256)
 def kda_pages_workspace_size(pages):
     n = ctypes.c_size_t(0)
     _check(_lib.kda_pages_workspace_size(pages, ctypes.byref(n)), "kda_pages_workspace_size")
@@ -596,14 +613,15 @@ def kda_pages_compact(cache, refs, table=None, live=None, *, workspace=None, str
     """Moves the live pages of ``cache`` [L, P, ...] to the lowest numbers, ``refs`` (int32 [P]) with them,
     and renumbers ``table`` (int32, any page numbers, -1 stays) in place.  Returns their count, int32 [1]."""
     L, P, nbytes = _cache(cache)
-    _need(refs, (P,), torch.int32, "refs")
+    _need_all(((refs, (P,), torch.int32, "refs"),))
     n = 0
     if table is not None:
-        _need(table, table.shape, torch.int32, "table")
+        _need_all(((table, table.shape, torch.int32, "table"),))
         n = table.numel()
     if live is None:
         live = torch.empty(1, dtype=torch.int32, device=cache.device)
-    _need(live, (1,), torch.int32, "live")
+    else:
+        _need_all(((live, (1,), torch.int32, "live"),))
     if workspace is None:
         workspace = _workspace(kda_pages_workspace_size(P), cache.device)
     _check(_lib.kda_pages_compact(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(table), n, _ptr(live), _ptr(workspace),
