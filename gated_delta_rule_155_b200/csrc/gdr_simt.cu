@@ -24,7 +24,7 @@
 //
 // M and P M are the same products in both directions, so one kernel makes them for every chunk at
 // once (prep); what is left between chunks is three products a chunk, walked in order by one block
-// per (sequence, value head, 32 state columns) — the columns of S never mix.  The gradients of
+// per (sequence, value head, 16 state columns) — the columns of S never mix.  The gradients of
 // q, k, g, beta need only their own chunk's S and dS, which the two walks leave in the workspace.
 #include "gdr.cuh"
 
@@ -33,28 +33,34 @@ namespace {
 
 using namespace gdr;
 
-constexpr int NT = 256;
-constexpr int NS = 32;          // state columns of a chain block
+constexpr int NT = 256;         // threads of prep and of the gradients
+constexpr int WT = 128;         // threads of a walk
+constexpr int NS = 16;          // state columns of a walk's block
 constexpr int LM = 68;          // row stride of 64 x 64 fp32 tiles
 constexpr int LS = NS + 4;      // row stride of state slices
+constexpr int ITEM = 2 * CH * CH + 256;   // floats of a chunk and value head: M, P M, then gamma, lam, beta (64 each)
 
 struct Ws {                     // fp32 workspace, items = slots * Hv
-    float *M, *PM;              // [items, 64, 64]
+    float *I;                   // [items, ITEM]
     float *S, *dS;              // [items, dk, dv]   (backward)
     float *U, *H;               // [items, 64, dv]   (backward)
+    float *dq, *dk;             // [items, 64, dk]   (backward, grouped heads): each value head's part
 };
 
-Ws carve(void *ws, long long items, int dk, int dv, bool backward)
+Ws carve(void *ws, long long items, int dk, int dv, bool backward, bool grouped)
 {
     float *p = (float *)ws;
     Ws w{};
-    w.M = p; p += items * CH * CH;
-    w.PM = p; p += items * CH * CH;
+    w.I = p; p += items * ITEM;
     if (backward) {
         w.S = p; p += items * dk * dv;
         w.dS = p; p += items * dk * dv;
         w.U = p; p += items * CH * dv;
         w.H = p; p += items * CH * dv;
+        if (grouped) {
+            w.dq = p; p += items * CH * dk;
+            w.dk = p; p += items * CH * dk;
+        }
     }
     return w;
 }
@@ -137,22 +143,6 @@ KDA_DEVICE void mm_nn(float (&acc)[4][4], const float *A, int lda, const float *
         }
     }
 }
-// acc[i][j] += sum_k A[k][i] B[k][j]   (4 consecutive columns of both)
-template <int K>
-KDA_DEVICE void mm_tn(float (&acc)[4][4], const float *A, int lda, const float *B, int ldb)
-{
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        float a[4], b[4];
-        ld4(A + k * lda, a);
-        ld4(B + k * ldb, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] += a[i] * b[j];
-    }
-}
-
 // ---------------------------------------------------------------- prep: M and P M of every chunk
 template <typename IO, int DK>
 __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
@@ -193,12 +183,353 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
     mm_nn<CH>(pm, Pm + 4 * ty * LM, LM, M + 4 * tx, LM);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        st4(p.w.PM + item * CH * CH + (4 * ty + i) * CH + 4 * tx, pm[i]);
-        st4(p.w.M + item * CH * CH + (4 * ty + i) * CH + 4 * tx, *(const float(*)[4])(M + (4 * ty + i) * LM + 4 * tx));
+        st4(p.w.I + item * ITEM + CH * CH + (4 * ty + i) * CH + 4 * tx, pm[i]);
+        st4(p.w.I + item * ITEM + (4 * ty + i) * CH + 4 * tx, *(const float(*)[4])(M + (4 * ty + i) * LM + 4 * tx));
+    }
+    if (tid < CH) {
+        float *g = p.w.I + item * ITEM + 2 * CH * CH + tid;
+        g[0] = gs.gam[tid];
+        g[CH] = gs.lam[tid];
+        g[2 * CH] = gs.beta[tid];
     }
 }
 
-// ---------------------------------------------------------------- the walk along a sequence
+// ---------------------------------------------------------------- the walks along a sequence
+// A block has 16 columns of a head's state, its rows in registers (and as an operand in shared memory).
+// Thread (rg, cg): tokens rg and rg + 32 of the chunk's products, or dk / 32 state rows, of columns
+// cg .. cg + 3, so a product's step of four k is 4 + 4 16-byte loads for 64 FMAs and what a token's rows
+// of one product give stays in registers for the next.  The next chunk's tiles come by cp.async (bf16:
+// through registers) under this chunk's products.
+KDA_DEVICE void cp_async16(void *dst, const void *src, bool take)
+{
+    const int n = take ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(n)
+                 : "memory");
+}
+KDA_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+KDA_DEVICE void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <typename IO, int DK>
+struct Tiles {
+    static constexpr int LK = DK + 4;
+    static constexpr int KQ = 2 * CH * LK, MM = 2 * CH * LM, STAGE = KQ + MM + 256;   // floats
+    static constexpr bool DIRECT = sizeof(IO) == 4;
+    static constexpr int U = DIRECT ? 1 : CH * DK * 2 * 2 / 16 / WT;   // 16-byte pieces of bf16 K and Q rows a thread
+    uint4 hold[U];
+    // starts the copies of a chunk into the stage `b`; K, Q rows behind `valid` are zeros
+    KDA_DEVICE void fetch(float *b, const GdrArgs &a, const float *item, size_t row0, int hk, int valid, int tid)
+    {
+        if (DIRECT) {
+            for (int u = tid; u < 2 * CH * (DK / 4); u += WT) {
+                const int r = u / (DK / 4), c = 4 * (u % (DK / 4)), t = r & (CH - 1);
+                const float *src = (const float *)(r < CH ? a.k : a.q) + ((row0 + min(t, valid - 1)) * a.Hk + hk) * DK + c;
+                cp_async16(b + r * LK + c, src, t < valid);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = tid + i * WT, r = u / (DK / 8), c = 8 * (u % (DK / 8)), t = r & (CH - 1);
+                hold[i] = t < valid ? *(const uint4 *)((const IO *)(r < CH ? a.k : a.q) + ((row0 + t) * a.Hk + hk) * DK + c)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        for (int u = tid; u < 2 * CH * (CH / 4); u += WT)
+            cp_async16(b + KQ + (u / (CH / 4)) * LM + 4 * (u % (CH / 4)), item + 4 * u, true);
+        if (tid < 48) cp_async16(b + KQ + MM + 4 * tid, item + 2 * CH * CH + 4 * tid, true);
+        cp_async_commit();
+    }
+    KDA_DEVICE void put(float *b, int tid)   // bf16: the rows that fetch has read
+    {
+        if (DIRECT) return;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = tid + i * WT, r = u / (DK / 8), c = 8 * (u % (DK / 8));
+            const uint32_t w[4] = {hold[i].x, hold[i].y, hold[i].z, hold[i].w};
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+            st4(b + r * LK + c, *(const float(*)[4])x);
+            st4(b + r * LK + c + 4, *(const float(*)[4])(x + 4));
+        }
+    }
+};
+
+// acc[i][j] += sum_{k < K} A[32 i ld + k] B[k][j]: NI rows 32 apart, four columns
+template <int K, int NI>
+KDA_DEVICE void mm_rows(float (&acc)[NI][4], const float *A, int lda, int step, const float *B)
+{
+#pragma unroll 4
+    for (int k = 0; k < K; k += 4) {
+        float a[NI][4];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) ld4(A + i * step * lda + k, a[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float b[4];
+            ld4(B + (k + e) * LS, b);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] += a[i][e] * b[j];
+        }
+    }
+}
+// SR consecutive floats
+template <int SR>
+KDA_DEVICE void ld_row(const float *p, float (&x)[SR])
+{
+    if constexpr (SR == 4) ld4(p, x);
+    else { const float2 t = *(const float2 *)p; x[0] = t.x; x[1] = t.y; }
+}
+
+// KEEP: leaves each chunk's start state and U in the workspace for the gradients, and writes no output
+template <typename IO, int DK, int DV, bool KEEP>
+__global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
+{
+    const GdrArgs &a = p.a;
+    extern __shared__ float sm[];
+    using T = Tiles<IO, DK>;
+    constexpr int LK = T::LK, SR = DK / 32;
+    float *S = sm + 2 * T::STAGE, *R = S + DK * LS, *Ub = R + CH * LS;
+    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
+    const SeqSpan span = span_of(a.cu, n, a.N, a.T);
+    const int nchunks = (span.len + CH - 1) / CH;
+    const int rg = tid >> 2, cg = 4 * (tid & 3), r0 = rg * SR, col = col0 + cg;
+    const int page0 = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
+    float s[SR][4];
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+        if (page0 >= 0) ld4(a.s0 + (((size_t)page0 * a.Hv + hv) * DK + r0 + i) * DV + col, s[i]);
+        st4(S + (r0 + i) * LS + cg, s[i]);
+    }
+    T tiles;
+    float v[2][4], vn[2][4];
+    const size_t item0 = (size_t)slot_base(span.row0, n);
+    auto fetch = [&](int ch) {
+        const size_t row0 = (size_t)span.row0 + ch * CH;
+        const int valid = min(CH, span.len - ch * CH);
+        tiles.fetch(sm + (ch & 1) * T::STAGE, a, p.w.I + ((item0 + ch) * a.Hv + hv) * ITEM, row0, hk, valid, tid);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) vn[i][j] = 0.0f;
+            if (rg + 32 * i < valid) ld4((const IO *)a.v + ((row0 + rg + 32 * i) * a.Hv + hv) * DV + col, vn[i]);
+        }
+    };
+    if (nchunks > 0) {
+        fetch(0);
+        tiles.put(sm, tid);
+    }
+    for (int ch = 0; ch < nchunks; ++ch) {
+        const size_t row0 = (size_t)span.row0 + ch * CH, item = (item0 + ch) * a.Hv + hv;
+        const int valid = min(CH, span.len - ch * CH);
+        const float *KQ = sm + (ch & 1) * T::STAGE, *MM = KQ + T::KQ, *g = MM + T::MM;
+        cp_async_wait();
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = vn[i][j];
+        if (ch + 1 < nchunks) fetch(ch + 1);
+        if (KEEP)
+#pragma unroll
+            for (int i = 0; i < SR; ++i) st4(p.w.S + (item * DK + r0 + i) * DV + col, s[i]);
+        float x[4][4] = {};                          // rows: X of the two tokens, Q S of the two tokens
+        if (KEEP) mm_rows<DK, 2>(*(float(*)[2][4])x, KQ + rg * LK, LK, 32, S + cg);
+        else mm_rows<DK, 4>(x, KQ + rg * LK, LK, 32, S + cg);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = rg + 32 * i;
+            const float gam = g[t], beta = g[2 * CH + t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = beta * (v[i][j] - gam * x[i][j]);
+                x[2 + i][j] *= gam;
+            }
+            st4(R + t * LS + cg, x[i]);
+        }
+        __syncthreads();
+        float u[4][4] = {};                          // U of the two tokens, P U of the two tokens; M, P M are lower
+        if (KEEP) {
+            mm_rows<32, 2>(*(float(*)[2][4])u, MM + rg * LM, LM, 32, R + cg);
+            mm_rows<32, 1>(*(float(*)[1][4])u[1], MM + (rg + 32) * LM + 32, LM, 0, R + 32 * LS + cg);
+        } else {
+            mm_rows<32, 4>(u, MM + rg * LM, LM, 32, R + cg);
+            float w[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { w[0][j] = u[1][j]; w[1][j] = u[3][j]; }
+            mm_rows<32, 2>(w, MM + (rg + 32) * LM + 32, LM, 64, R + 32 * LS + cg);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { u[1][j] = w[0][j]; u[3][j] = w[1][j]; }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = rg + 32 * i;
+            if (KEEP) st4(p.w.U + (item * CH + t) * DV + col, u[i]);
+            const float lam = g[CH + t];
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = lam * u[i][j];
+            st4(Ub + t * LS + cg, y);
+            if (!KEEP && t < valid) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = x[2 + i][j] + u[2 + i][j];
+                st4((IO *)a.out + ((row0 + t) * a.Hv + hv) * DV + col, y);
+            }
+        }
+        __syncthreads();
+        const float gc = g[CH - 1];
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] *= gc;
+#pragma unroll 8
+        for (int t = 0; t < CH; ++t) {
+            float kr[SR], b[4];
+            ld_row<SR>(KQ + t * LK + r0, kr);
+            ld4(Ub + t * LS + cg, b);
+#pragma unroll
+            for (int i = 0; i < SR; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] += kr[i] * b[j];
+        }
+#pragma unroll
+        for (int i = 0; i < SR; ++i) st4(S + (r0 + i) * LS + cg, s[i]);
+        if (ch + 1 < nchunks) tiles.put(sm + ((ch + 1) & 1) * T::STAGE, tid);
+    }
+    if (KEEP || !a.sT) return;
+    const int page = page_of(a.sT_index, n, a.pages, a.err);
+    if (page < 0) return;
+    if ((a.sT_index || (a.s0_index && a.sT == a.s0)) &&
+        !page_is_free(a.sT_index, a.s0_index, a.sT == a.s0, n, a.N, page, tid, WT)) {
+        if (tid == 0) raise_error(a.err, ERR_PAGE_INDEX);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < SR; ++i) st4(a.sT + (((size_t)page * a.Hv + hv) * DK + r0 + i) * DV + col, s[i]);
+}
+
+template <typename IO, int DK, int DV>
+__global__ void __launch_bounds__(WT) gdr_reverse_simt_kernel(P p)
+{
+    const GdrArgs &a = p.a;
+    extern __shared__ float sm[];
+    using T = Tiles<IO, DK>;
+    constexpr int LK = T::LK, SR = DK / 32;
+    float *S = sm + 2 * T::STAGE, *Yb = S + DK * LS, *dO = Yb + CH * LS, *W = dO + CH * LS;
+    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
+    const SeqSpan span = span_of(a.cu, n, a.N, a.T);
+    const int nchunks = (span.len + CH - 1) / CH;
+    const int rg = tid >> 2, cg = 4 * (tid & 3), r0 = rg * SR, col = col0 + cg;
+    const size_t st = (((size_t)n * a.Hv + hv) * DK + r0) * DV + col;
+    float s[SR][4];
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+        if (a.dST) ld4(a.dST + st + (size_t)i * DV, s[i]);
+        st4(S + (r0 + i) * LS + cg, s[i]);
+    }
+    T tiles;
+    float y[2][4];
+    const size_t item0 = (size_t)slot_base(span.row0, n);
+    auto fetch = [&](int ch) {
+        const size_t row0 = (size_t)span.row0 + ch * CH;
+        const int valid = min(CH, span.len - ch * CH);
+        tiles.fetch(sm + (ch & 1) * T::STAGE, a, p.w.I + ((item0 + ch) * a.Hv + hv) * ITEM, row0, hk, valid, tid);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[i][j] = 0.0f;
+            if (rg + 32 * i < valid) ld4((const IO *)a.dO + ((row0 + rg + 32 * i) * a.Hv + hv) * DV + col, y[i]);
+        }
+    };
+    if (nchunks > 0) {
+        fetch(nchunks - 1);
+        tiles.put(sm + ((nchunks - 1) & 1) * T::STAGE, tid);
+    }
+    for (int ch = nchunks - 1; ch >= 0; --ch) {
+        const size_t row0 = (size_t)span.row0 + ch * CH, item = (item0 + ch) * a.Hv + hv;
+        const int valid = min(CH, span.len - ch * CH);
+        const float *KQ = sm + (ch & 1) * T::STAGE, *MM = KQ + T::KQ, *g = MM + T::MM;
+        cp_async_wait();
+        __syncthreads();
+        st4(dO + rg * LS + cg, y[0]);
+        st4(dO + (rg + 32) * LS + cg, y[1]);
+        if (ch > 0) fetch(ch - 1);
+#pragma unroll
+        for (int i = 0; i < SR; ++i) st4(p.w.dS + (item * DK + r0 + i) * DV + col, s[i]);
+        float x[2][4] = {};
+        mm_rows<DK, 2>(x, KQ + rg * LK, LK, 32, S + cg);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float lam = g[CH + rg + 32 * i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] *= lam;
+            st4(Yb + (rg + 32 * i) * LS + cg, x[i]);
+        }
+        __syncthreads();
+        float h[2][4] = {};                          // H of tokens 2 rg, 2 rg + 1: rows from the warp's first token on
+#pragma unroll 4
+        for (int t = 16 * (tid >> 5); t < CH; ++t) {
+            const float2 m = *(const float2 *)(MM + t * LM + 2 * rg), pm = *(const float2 *)(MM + (CH + t) * LM + 2 * rg);
+            float b[4], c[4];
+            ld4(Yb + t * LS + cg, b);
+            ld4(dO + t * LS + cg, c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[0][j] += m.x * b[j] + pm.x * c[j];
+                h[1][j] += m.y * b[j] + pm.y * c[j];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * rg + i;
+            const float gam = g[t], beta = g[2 * CH + t];
+            st4(p.w.H + (item * CH + t) * DV + col, h[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[i][j] *= beta;
+            if (t < valid) st4((IO *)a.dv_ + ((row0 + t) * a.Hv + hv) * DV + col, h[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[i][j] *= -gam;
+            st4(W + t * LS + cg, h[i]);
+        }
+        __syncthreads();
+        const float gc = g[CH - 1];
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] *= gc;
+#pragma unroll 4
+        for (int t = 0; t < CH; ++t) {
+            float kr[SR], qr[SR], b[4], c[4];
+            ld_row<SR>(KQ + t * LK + r0, kr);
+            ld_row<SR>(KQ + (CH + t) * LK + r0, qr);
+            ld4(W + t * LS + cg, b);
+            ld4(dO + t * LS + cg, c);
+            const float gam = g[t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] *= gam;
+#pragma unroll
+            for (int i = 0; i < SR; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] += kr[i] * b[j] + qr[i] * c[j];
+        }
+#pragma unroll
+        for (int i = 0; i < SR; ++i) st4(S + (r0 + i) * LS + cg, s[i]);
+        if (ch > 0) tiles.put(sm + ((ch - 1) & 1) * T::STAGE, tid);
+    }
+    if (!a.ds0) return;
+#pragma unroll
+    for (int i = 0; i < SR; ++i) st4(a.ds0 + st + (size_t)i * DV, s[i]);
+}
+
+// ---------------------------------------------------------------- gradients of q, k, g, beta, a chunk and value head a block
 template <int D>
 KDA_DEVICE void load_item(float *dst, int ld, const float *src, int tid)   // 64 rows of D floats
 {
@@ -208,188 +539,6 @@ KDA_DEVICE void load_item(float *dst, int ld, const float *src, int tid)   // 64
     }
 }
 
-// KEEP: leaves each chunk's start state and U in the workspace for the gradients, and writes no output
-template <typename IO, int DK, int DV, bool KEEP>
-__global__ void __launch_bounds__(NT) gdr_forward_simt_kernel(P p)
-{
-    const GdrArgs &a = p.a;
-    extern __shared__ float sm[];
-    constexpr int LK = DK + 4;
-    float *KQ = sm, *MM = KQ + 2 * CH * LK, *S = MM + 2 * CH * LM, *R = S + DK * LS, *Y = R + CH * LS;
-    __shared__ Gates gs;
-    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
-    const SeqSpan span = span_of(a.cu, n, a.N, a.T);
-    const int nchunks = (span.len + CH - 1) / CH;
-    const int page0 = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
-    const float *s0 = page0 >= 0 ? a.s0 + ((size_t)page0 * a.Hv + hv) * DK * DV + col0 : nullptr;
-    for (int u = tid; u < DK * NS; u += NT) {
-        const int r = u / NS, c = u % NS;
-        S[r * LS + c] = s0 ? s0[(size_t)r * DV + c] : 0.0f;
-    }
-    const int rg = tid >> 3, cg = 4 * (tid & 7);   // rows 4 rg .. + 3, columns cg .. + 3
-    for (int ch = 0; ch < nchunks; ++ch) {
-        const size_t row0 = (size_t)span.row0 + ch * CH;
-        const int valid = min(CH, span.len - ch * CH);
-        const size_t item = (size_t)(slot_base(span.row0, n) + ch) * a.Hv + hv;
-        __syncthreads();
-        load_rows<IO, DK, LK>(KQ, (const IO *)a.k, row0, a.Hk, hk, valid, tid);
-        load_rows<IO, DK, LK>(KQ + CH * LK, (const IO *)a.q, row0, a.Hk, hk, valid, tid);
-        load_item<CH>(MM, LM, p.w.M + item * CH * CH, tid);
-        load_item<CH>(MM + CH * LM, LM, p.w.PM + item * CH * CH, tid);
-        load_rows<IO, NS, LS>(R, (const IO *)a.v, row0, a.Hv, hv, valid, tid, col0, DV);
-        load_gates<IO>(gs, (const IO *)a.g, (const IO *)a.beta, row0, a.Hv, hv, valid, tid);
-        if (KEEP)
-            for (int u = tid; u < DK * NS; u += NT)
-                p.w.S[(item * DK + u / NS) * DV + col0 + u % NS] = S[(u / NS) * LS + u % NS];
-        __syncthreads();
-        float d1[4][4] = {};
-        mm_nn<DK>(d1, KQ + 4 * rg * LK, LK, S + cg, LS);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * rg + i;
-            if (t < CH) {   // X = K S -> R
-                float v[4];
-                ld4(R + t * LS + cg, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = gs.beta[t] * (v[j] - gs.gam[t] * d1[i][j]);
-                st4(R + t * LS + cg, v);
-            } else {        // Q S
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d1[i][j] *= gs.gam[t - CH];
-                st4(Y + (t - CH) * LS + cg, d1[i]);
-            }
-        }
-        __syncthreads();
-        float d2[4][4] = {};
-        mm_nn<CH>(d2, MM + 4 * rg * LM, LM, R + cg, LS);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * rg + i;
-            if (t < CH) {
-                if (KEEP) st4(p.w.U + (item * CH + t) * DV + col0 + cg, d2[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d2[i][j] *= gs.lam[t];
-                st4(R + t * LS + cg, d2[i]);
-            } else if (!KEEP && t - CH < valid) {
-                float y[4];
-                ld4(Y + (t - CH) * LS + cg, y);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] += d2[i][j];
-                st4((IO *)a.out + ((row0 + t - CH) * a.Hv + hv) * DV + col0 + cg, y);
-            }
-        }
-        __syncthreads();
-        if (rg < DK / 4) {
-            float s[4][4];
-            const float gc = gs.gam[CH - 1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ld4(S + (4 * rg + i) * LS + cg, s[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] *= gc;
-            }
-            mm_tn<CH>(s, KQ + 4 * rg, LK, R + cg, LS);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st4(S + (4 * rg + i) * LS + cg, s[i]);
-        }
-    }
-    __syncthreads();
-    if (KEEP || !a.sT) return;
-    const int page = page_of(a.sT_index, n, a.pages, a.err);
-    if (page < 0) return;
-    if ((a.sT_index || (a.s0_index && a.sT == a.s0)) &&
-        !page_is_free(a.sT_index, a.s0_index, a.sT == a.s0, n, a.N, page, tid, NT)) {
-        if (tid == 0) raise_error(a.err, ERR_PAGE_INDEX);
-        return;
-    }
-    float *sT = a.sT + ((size_t)page * a.Hv + hv) * DK * DV + col0;
-    for (int u = tid; u < DK * NS; u += NT) sT[(size_t)(u / NS) * DV + u % NS] = S[(u / NS) * LS + u % NS];
-}
-
-template <typename IO, int DK, int DV>
-__global__ void __launch_bounds__(NT) gdr_reverse_simt_kernel(P p)
-{
-    const GdrArgs &a = p.a;
-    extern __shared__ float sm[];
-    constexpr int LK = DK + 4;
-    float *KQ = sm, *MM = KQ + 2 * CH * LK, *S = MM + 2 * CH * LM, *R = S + DK * LS;   // R: 128 rows
-    __shared__ Gates gs;
-    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
-    const SeqSpan span = span_of(a.cu, n, a.N, a.T);
-    const int nchunks = (span.len + CH - 1) / CH;
-    const size_t st = ((size_t)n * a.Hv + hv) * DK * DV + col0;
-    for (int u = tid; u < DK * NS; u += NT)
-        S[(u / NS) * LS + u % NS] = a.dST ? a.dST[st + (size_t)(u / NS) * DV + u % NS] : 0.0f;
-    const int rg = tid >> 3, cg = 4 * (tid & 7);
-    for (int ch = nchunks - 1; ch >= 0; --ch) {
-        const size_t row0 = (size_t)span.row0 + ch * CH;
-        const int valid = min(CH, span.len - ch * CH);
-        const size_t item = (size_t)(slot_base(span.row0, n) + ch) * a.Hv + hv;
-        __syncthreads();
-        load_rows<IO, DK, LK>(KQ, (const IO *)a.k, row0, a.Hk, hk, valid, tid);
-        load_rows<IO, DK, LK>(KQ + CH * LK, (const IO *)a.q, row0, a.Hk, hk, valid, tid);
-        load_item<CH>(MM, LM, p.w.M + item * CH * CH, tid);
-        load_item<CH>(MM + CH * LM, LM, p.w.PM + item * CH * CH, tid);
-        load_rows<IO, NS, LS>(R + CH * LS, (const IO *)a.dO, row0, a.Hv, hv, valid, tid, col0, DV);
-        load_gates<IO>(gs, (const IO *)a.g, (const IO *)a.beta, row0, a.Hv, hv, valid, tid);
-        for (int u = tid; u < DK * NS; u += NT)
-            p.w.dS[(item * DK + u / NS) * DV + col0 + u % NS] = S[(u / NS) * LS + u % NS];
-        __syncthreads();
-        const int t0 = 4 * rg;   // rows of the 64-row products: the first 128 threads
-        if (t0 < CH) {
-            float d1[4][4] = {};
-            mm_nn<DK>(d1, KQ + t0 * LK, LK, S + cg, LS);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d1[i][j] *= gs.lam[t0 + i];
-                st4(R + (t0 + i) * LS + cg, d1[i]);
-            }
-        }
-        __syncthreads();
-        float h[4][4] = {};
-        if (t0 < CH) mm_tn<2 * CH>(h, MM + t0, LM, R + cg, LS);
-        __syncthreads();
-        if (t0 < CH) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + i;
-                st4(p.w.H + (item * CH + t) * DV + col0 + cg, h[i]);
-                float w[4], x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = gs.beta[t] * h[i][j];
-                if (t < valid) st4((IO *)a.dv_ + ((row0 + t) * a.Hv + hv) * DV + col0 + cg, w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] *= -gs.gam[t];
-                st4(R + t * LS + cg, w);
-                ld4(R + (CH + t) * LS + cg, x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= gs.gam[t];
-                st4(R + (CH + t) * LS + cg, x);
-            }
-        }
-        __syncthreads();
-        if (rg < DK / 4) {
-            float s[4][4];
-            const float gc = gs.gam[CH - 1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ld4(S + (4 * rg + i) * LS + cg, s[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] *= gc;
-            }
-            mm_tn<2 * CH>(s, KQ + 4 * rg, LK, R + cg, LS);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st4(S + (4 * rg + i) * LS + cg, s[i]);
-        }
-    }
-    __syncthreads();
-    if (!a.ds0) return;
-    for (int u = tid; u < DK * NS; u += NT) a.ds0[st + (size_t)(u / NS) * DV + u % NS] = S[(u / NS) * LS + u % NS];
-}
-
-// ---------------------------------------------------------------- gradients of q, k, g, beta, a chunk and key head a block
 template <typename IO, int DK, int DV>
 __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
 {
@@ -404,7 +553,7 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
     static_assert(LV >= LM, "the 64 x 64 tiles fit over dO and U");
     __shared__ Gates gs;
     __shared__ float s_row[CH], s_col[4][CH], s_db[CH], s_red[NT / 32];
-    const int tid = threadIdx.x, hk = blockIdx.y, rep = a.Hv / a.Hk;
+    const int tid = threadIdx.x, hv = blockIdx.y, rep = a.Hv / a.Hk, hk = hv / rep;
     const int ty = tid >> 4, tx = tid & 15;
     const size_t row0 = (size_t)span.row0 + c * CH;
     const int valid = min(CH, span.len - c * CH);
@@ -416,11 +565,9 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
-    for (int r = 0; r < rep; ++r) {
-        const int hv = hk * rep + r;
-        const size_t item = (size_t)blockIdx.x * a.Hv + hv;
+    const size_t item = (size_t)blockIdx.x * a.Hv + hv;
+    {
         const float *S = p.w.S + item * DK * DV, *dS = p.w.dS + item * DK * DV;
-        __syncthreads();
         load_rows<IO, DV, LV>(dO, (const IO *)a.dO, row0, a.Hv, hv, valid, tid);
         load_item<DV>(U, LV, p.w.U + item * CH * DV, tid);
         load_item<DV>(H, LV, p.w.H + item * CH * DV, tid);
@@ -577,6 +724,15 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
     for (int i = 0; i < 4; ++i) {
         const int t = 4 * ty + i;
         if (t >= valid) continue;
+        if (rep > 1) {                       // a part of the group's sum
+            const size_t o = (item * CH + t) * DK;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                p.w.dq[o + tx + 16 * j] = dq[i][j];
+                p.w.dk[o + tx + 16 * j] = dk[i][j];
+            }
+            continue;
+        }
         const size_t o = ((row0 + t) * a.Hk + hk) * DK;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -586,20 +742,50 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
     }
 }
 
+// dq, dk of a chunk and key head: the sum of its value heads' parts, in order
+template <typename IO, int DK>
+__global__ void __launch_bounds__(NT) gdr_group_sum_kernel(P p)
+{
+    const GdrArgs &a = p.a;
+    int n, c;
+    SeqSpan span;
+    if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
+    const int hk = blockIdx.y, rep = a.Hv / a.Hk, valid = min(CH, span.len - c * CH);
+    const size_t row0 = (size_t)span.row0 + c * CH, item = (size_t)blockIdx.x * a.Hv + hk * rep;
+    for (int u = threadIdx.x; u < valid * (DK / 4); u += NT) {
+        const int t = u / (DK / 4), col = 4 * (u % (DK / 4));
+        float x[4] = {}, y[4] = {};
+        for (int r = 0; r < rep; ++r) {
+            float e[4], f[4];
+            ld4(p.w.dq + ((item + r) * CH + t) * DK + col, e);
+            ld4(p.w.dk + ((item + r) * CH + t) * DK + col, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] += e[j];
+                y[j] += f[j];
+            }
+        }
+        const size_t o = ((row0 + t) * a.Hk + hk) * DK + col;
+        st4((IO *)a.dq + o, x);
+        st4((IO *)a.dk_ + o, y);
+    }
+}
+
 template <int DK>
 constexpr int prep_bytes() { return (2 * CH * (DK + 4) + 2 * CH * LM) * 4; }
 template <int DK>
-constexpr int chain_bytes() { return (2 * CH * (DK + 4) + 2 * CH * LM + DK * LS + 2 * CH * LS) * 4; }
+constexpr int walk_bytes(int buffers) { return (2 * (2 * CH * (DK + 4) + 2 * CH * LM + 256) + DK * LS + buffers * CH * LS) * 4; }
 template <int DK, int DV>
 constexpr int grads_bytes() { return (2 * CH * (DK + 4) + 3 * CH * (DV + 4)) * 4; }
-static_assert(chain_bytes<128>() <= 227 * 1024 && grads_bytes<128, 128>() <= 227 * 1024, "shared memory per block");
+static_assert(walk_bytes<128>(3) <= 227 * 1024 && grads_bytes<128, 128>() <= 227 * 1024, "shared memory per block");
 
 template <typename IO, int DK, int DV>
 cudaError_t launch_all(const GdrArgs &a, bool backward, cudaStream_t s)
 {
     struct TagP; struct TagF; struct TagK; struct TagR; struct TagG;
+    constexpr int FB = walk_bytes<DK>(2), RB = walk_bytes<DK>(3);
     const long long slots = gdr_slots(a.N, a.T);
-    P p{a, carve(a.ws, slots * a.Hv, DK, DV, backward)};
+    P p{a, carve(a.ws, slots * a.Hv, DK, DV, backward, a.Hv > a.Hk)};
     cudaError_t e;
     if (a.T > 0) {
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_simt_kernel<IO, DK>, prep_bytes<DK>())) != cudaSuccess) return e;
@@ -608,22 +794,23 @@ cudaError_t launch_all(const GdrArgs &a, bool backward, cudaStream_t s)
     const dim3 chain((unsigned)a.N * (DV / NS), a.Hv);
     if (!backward) {
         auto fn = gdr_forward_simt_kernel<IO, DK, DV, false>;
-        if ((e = smem_opt_in<TagF>((const void *)fn, chain_bytes<DK>())) != cudaSuccess) return e;
-        fn<<<chain, NT, chain_bytes<DK>(), s>>>(p);
+        if ((e = smem_opt_in<TagF>((const void *)fn, FB)) != cudaSuccess) return e;
+        fn<<<chain, WT, FB, s>>>(p);
         return cudaGetLastError();
     }
     if (a.T > 0) {
         auto fn = gdr_forward_simt_kernel<IO, DK, DV, true>;
-        if ((e = smem_opt_in<TagK>((const void *)fn, chain_bytes<DK>())) != cudaSuccess) return e;
-        fn<<<chain, NT, chain_bytes<DK>(), s>>>(p);
+        if ((e = smem_opt_in<TagK>((const void *)fn, FB)) != cudaSuccess) return e;
+        fn<<<chain, WT, FB, s>>>(p);
     }
     auto rv = gdr_reverse_simt_kernel<IO, DK, DV>;
-    if ((e = smem_opt_in<TagR>((const void *)rv, chain_bytes<DK>())) != cudaSuccess) return e;
-    rv<<<chain, NT, chain_bytes<DK>(), s>>>(p);
+    if ((e = smem_opt_in<TagR>((const void *)rv, RB)) != cudaSuccess) return e;
+    rv<<<chain, WT, RB, s>>>(p);
     if (a.T > 0) {
         auto gr = gdr_grads_simt_kernel<IO, DK, DV>;
         if ((e = smem_opt_in<TagG>((const void *)gr, grads_bytes<DK, DV>())) != cudaSuccess) return e;
-        gr<<<dim3((unsigned)slots, a.Hk), NT, grads_bytes<DK, DV>(), s>>>(p);
+        gr<<<dim3((unsigned)slots, a.Hv), NT, grads_bytes<DK, DV>(), s>>>(p);
+        if (a.Hv > a.Hk) gdr_group_sum_kernel<IO, DK><<<dim3((unsigned)slots, a.Hk), NT, 0, s>>>(p);
     }
     return cudaGetLastError();
 }
@@ -639,9 +826,8 @@ cudaError_t launch_dims(const GdrArgs &a, bool backward, cudaStream_t s)
 
 size_t gdr_simt_workspace(int N, int T, int Hk, int Hv, int dk, int dv, bool backward)
 {
-    (void)Hk;
     const size_t items = (size_t)gdr_slots(N, T) * Hv;
-    return 4 * items * (2 * gdr::CH * gdr::CH + (backward ? 2 * (size_t)dk * dv + 2 * gdr::CH * dv : 0));
+    return 4 * items * (ITEM + (backward ? 2 * (size_t)dk * dv + 2 * gdr::CH * dv + (Hv > Hk ? 2 * gdr::CH * dk : 0) : 0));
 }
 
 cudaError_t launch_gdr_forward_simt(const GdrArgs &a, cudaStream_t s)
