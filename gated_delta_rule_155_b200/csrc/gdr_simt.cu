@@ -819,7 +819,9 @@ template <typename IO>
 cudaError_t launch_dims(const GdrArgs &a, bool backward, cudaStream_t s)
 {
     if (a.dk == 64) return a.dv == 64 ? launch_all<IO, 64, 64>(a, backward, s) : launch_all<IO, 64, 128>(a, backward, s);
-    return a.dv == 64 ? launch_all<IO, 128, 64>(a, backward, s) : launch_all<IO, 128, 128>(a, backward, s);
+    if (a.dv == 64) return launch_all<IO, 128, 64>(a, backward, s);
+    if constexpr (sizeof(IO) == 4) return launch_all<IO, 128, 128>(a, backward, s);
+    else return cudaErrorInvalidValue;   // the tensor-core kernels' shape
 }
 
 }  // namespace

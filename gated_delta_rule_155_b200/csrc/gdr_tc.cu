@@ -327,6 +327,10 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ------------------------------------------------------------ MMAs
         constexpr int NX = KEEP ? 64 : 128;      // X (and Q S), U (and P U)
         constexpr uint32_t id_x = idesc_bf16(128, NX, false, false), id_s = idesc_bf16(128, 128, false, true);
+        auto keep_u = [&](int ch) {
+            bulk_store(p.U + ((item0 + ch) * a.Hv + hv) * TILE, sm + W_KEEP_U, TILE);
+            bulk_commit();
+        };
         bool ok = true;
         for (int ch = 0; ch < nchunks && ok; ++ch) {
             uint8_t *s = sm + (ch % STAGES) * ST_BYTES;
@@ -349,6 +353,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             mma_ts(tmem + TM_X, tmem + TM_SHL + 64 * hl + 8 * kk,
                                    sdesc(kq + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024), id_x, kk | hl);
                     mma_commit(m_x);
+                    if (KEEP && ch > 0) keep_u(ch - 1);
                 }
                 if (ok && (ok = wait(b_r, ch))) {                // R^T [M; P M]^T
                     tc_fence_after();
@@ -360,7 +365,12 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         mma_ts(tmem + TM_U, rl, bh, id_x, 1);
                         mma_ts(tmem + TM_U, rh, bl, id_x, 1);
                     }
+                    if (KEEP) bulk_wait_read_all();              // U's tile may be written again
                     mma_commit(m_u);
+                    if (KEEP) {
+                        bulk_store(p.S + ((item0 + ch) * a.Hv + hv) * 2 * TILE, sm + W_KEEP_S, 2 * TILE);
+                        bulk_commit();
+                    }
                 }
                 if (ok && (ok = wait(b_u, ch))) {                // (lam U)^T K
                     tc_fence_after();
@@ -369,11 +379,16 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
                             mma_ts(tmem + TM_S, tmem + TM_X + 16 * kk + 8 * hl, sdesc(kq + kk * 2048, TILE, 1024), id_s, 1);
+                    if (KEEP) bulk_wait_read_all();              // and S's
                     mma_commit(m_s);
                     mma_commit(&empty[ch % STAGES]);
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        }
+        if (KEEP && lane == 0) {
+            if (ok && nchunks > 0 && wait(b_s, nchunks)) keep_u(nchunks - 1);
+            bulk_wait_read_all();
         }
         if (lane == 0 && *abort_flag) {
             mma_commit(drain);
@@ -419,10 +434,11 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_st16(at + TM_SHL + 64 + (r0 >> 1), l);
                 arrive(b_s);
                 if (KEEP) {                          // [dv][state row]
-                    uint8_t *dst = p.S + (((item0 + ch) * a.Hv + hv) * 2 + (grp >> 1)) * TILE;
+                    uint8_t *dst = sm + W_KEEP_S + (grp >> 1) * TILE;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *(uint4 *)(dst + swz(dv, 4 * (grp & 1) + j)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                    fence_proxy_async();
                 }
             }
             if (!(ok = wait_full(ch))) break;
@@ -474,7 +490,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 put_tokens(at + TM_X + t0, r);       // R has been read: U's product is done
                 arrive(b_u);
                 if (KEEP) {                          // [dv][token]
-                    uint8_t *dst = p.U + ((item0 + ch) * a.Hv + hv) * TILE;
+                    uint8_t *dst = sm + W_KEEP_U;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t u[4];
@@ -483,6 +499,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             u[e] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
                         *(uint4 *)(dst + swz(dv, 2 * grp + j)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
+                    fence_proxy_async();
                 }
             }
             if (!KEEP) {                             // outputs, under the state's product
@@ -505,6 +522,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
+        if (KEEP && ok && nchunks > 0) arrive(b_s);  // the last U's tile is written
         if (!KEEP && a.sT) {
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             const int page = page_of(a.sT_index, n, a.pages, a.err);
@@ -585,8 +603,8 @@ cudaError_t launch_gdr_prep_walk_tc(const TcP &p, bool keep, cudaStream_t s)
     }
     const unsigned blocks = (unsigned)(a.N * a.Hv);
     if (keep) {
-        if ((e = smem_opt_in<TagK>((const void *)gdr_walk_tc_kernel<true>, W_BYTES)) != cudaSuccess) return e;
-        gdr_walk_tc_kernel<true><<<blocks, W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
+        if ((e = smem_opt_in<TagK>((const void *)gdr_walk_tc_kernel<true>, W_KEEP_BYTES)) != cudaSuccess) return e;
+        gdr_walk_tc_kernel<true><<<blocks, W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mv, p);
     } else {
         if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel<false>, W_BYTES)) != cudaSuccess) return e;
         gdr_walk_tc_kernel<false><<<blocks, W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);

@@ -77,7 +77,10 @@ constexpr unsigned long long DRAIN_NS = 2000000000ull;
 constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT_GATES, ST_BYTES = ST_G + 1024;
 constexpr int STAGES = 2;
 constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
-static_assert(W_BYTES <= 232448, "shared memory per block");
+// and, in the backward pass, what goes to the workspace: the state's tile (32 KB) and U's or H's (16 KB), each
+// stored by one bulk copy (as 16-byte pieces of 128-byte rows from the registers the walks took a fifth longer)
+constexpr int W_KEEP_S = W_BAR + 1024, W_KEEP_U = W_KEEP_S + 2 * TILE, W_KEEP_BYTES = W_KEEP_U + TILE + 1024;
+static_assert(W_KEEP_BYTES <= 232448, "shared memory per block");
 // Their warps: 4 g .. 4 g + 3, g < 4: tokens 16 g .. and state rows 32 g .. of the chain; 16 the copies, 17 the MMAs.
 constexpr int W_THREADS = 576;
 

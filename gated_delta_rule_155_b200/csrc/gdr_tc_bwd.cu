@@ -101,6 +101,10 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t id_y = idesc_bf16(128, 64, false, false), id_h = idesc_bf16(128, 64, false, true),
                            id_p = idesc_bf16(128, 64, true, true), id_s = idesc_bf16(128, 128, false, true);
+        auto keep_h = [&](int i) {
+            bulk_store(p.H + ((item0 + nchunks - 1 - i) * a.Hv + hv) * TILE, sm + W_KEEP_U, TILE);
+            bulk_commit();
+        };
         bool ok = true;
         for (int i = 0; i < nchunks && ok; ++i) {
             uint8_t *s = sm + (i % STAGES) * ST_BYTES;
@@ -126,6 +130,7 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             mma_ts(tmem + TM_Y, tmem + TM_SHL + 64 * hl + 8 * kk,
                                    sdesc(kq + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024), id_y, kk | hl);
                     mma_commit(m_y);
+                    if (i > 0) keep_h(i - 1);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -143,7 +148,10 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         mma_ts(tmem + TM_H, yl, bh, id_h, 1);
                         mma_ts(tmem + TM_H, yh, bl, id_h, 1);
                     }
+                    bulk_wait_read_all();                        // H's tile may be written again
                     mma_commit(m_h);
+                    bulk_store(p.dS + ((item0 + nchunks - 1 - i) * a.Hv + hv) * 2 * TILE, sm + W_KEEP_S, 2 * TILE);
+                    bulk_commit();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -157,11 +165,16 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll
                         for (int hl = 0; hl < 2; ++hl)
                             mma_ts(tmem + TM_S, tmem + TM_Y + 16 * kk + 8 * hl, sdesc(kq + kk * 2048, TILE, 1024), id_s, 1);
+                    bulk_wait_read_all();                        // and dS's
                     mma_commit(m_s);
                     mma_commit(&empty[i % STAGES]);
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        }
+        if (lane == 0) {
+            if (ok && nchunks > 0 && wait(b_s, nchunks)) keep_h(nchunks - 1);
+            bulk_wait_read_all();
         }
         if (lane == 0 && *abort_flag) {
             mma_commit(drain);
@@ -191,7 +204,6 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int ch = nchunks - 1 - i, st = i % STAGES, valid = min(CH, span.len - ch * CH);
             uint8_t *s = sm + st * ST_BYTES;
             const float *gates = (const float *)(s + ST_G);
-            const size_t item = (item0 + ch) * a.Hv + hv;
             if (i > 0) {
                 if (!(ok = wait_all(m_s, i - 1))) break;
                 tc_fence_after();
@@ -206,10 +218,11 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 tmem_st16(at + TM_SHL + (r0 >> 1), h);
                 tmem_st16(at + TM_SHL + 64 + (r0 >> 1), l);
                 arrive(b_s);
-                uint8_t *dst = p.dS + (item * 2 + (grp >> 1)) * TILE;    // [dv][state row]
+                uint8_t *dst = sm + W_KEEP_S + (grp >> 1) * TILE;        // [dv][state row]
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *(uint4 *)(dst + swz(dv, 4 * (grp & 1) + j)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                fence_proxy_async();
             }
             if (!(ok = wait_full(i))) break;
             {                                        // dS decayed, in the shadow of the product
@@ -260,7 +273,7 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 put_tokens(at + TM_Y + t0, r);       // lam Y has been read: H's product is done
                 arrive(b_w);
                 // H as an operand tile [token][dv], and dv = beta H
-                uint8_t *hd = p.H + item * TILE + (dv >> 6) * (TILE / 2) + t0 * 128 + 2 * (dv & 7);
+                uint8_t *hd = sm + W_KEEP_U + (dv >> 6) * (TILE / 2) + t0 * 128 + 2 * (dv & 7);
                 const int j = (dv & 63) >> 3;
                 __nv_bfloat16 *vd = (__nv_bfloat16 *)a.dv_ + (((size_t)span.row0 + ch * CH + t0) * a.Hv + hv) * D + dv;
 #pragma unroll
@@ -274,10 +287,12 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         if (t0 + e + k < valid) vd[(size_t)((e + k) * a.Hv) * D] = __float2bfloat16_rn(b4[k] * h);
                     }
                 }
+                fence_proxy_async();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
+        if (ok && nchunks > 0) arrive(b_s);          // the last H's tile is written
         if (a.ds0) {
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             if (ok) {
@@ -682,8 +697,8 @@ cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s)
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH) || !make_tile_map(&mo, a.dO, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
     }
-    if ((e = smem_opt_in<TagR>((const void *)gdr_reverse_tc_kernel, W_BYTES)) != cudaSuccess) return e;
-    gdr_reverse_tc_kernel<<<(unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s>>>(mq, mk, mo, p);
+    if ((e = smem_opt_in<TagR>((const void *)gdr_reverse_tc_kernel, W_KEEP_BYTES)) != cudaSuccess) return e;
+    gdr_reverse_tc_kernel<<<(unsigned)(a.N * a.Hv), W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mo, p);
     if (a.T > 0) {
         if ((e = smem_opt_in<TagG>((const void *)gdr_grads_tc_kernel, GS_BYTES)) != cudaSuccess) return e;
         gdr_grads_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hk), G_THREADS, GS_BYTES, s>>>(mq, mk, mv, mo, p);
