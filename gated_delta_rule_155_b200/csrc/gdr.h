@@ -30,7 +30,7 @@ struct GdrArgs {
 
 // Chunk slots: sequence n's chunks start at slot first_row / 64 + n, so that no prefix sum over
 // the sequences is needed; T / 64 + N slots in all.
-inline long long gdr_slots(int N, int T) { return (long long)T / 64 + N; }
+__host__ __device__ inline long long gdr_slots(int N, int T) { return (long long)T / 64 + N; }
 
 size_t gdr_simt_workspace(int N, int T, int Hk, int Hv, int dk, int dv, bool backward);
 cudaError_t launch_gdr_forward_simt(const GdrArgs &a, cudaStream_t s);

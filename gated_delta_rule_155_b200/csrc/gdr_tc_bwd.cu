@@ -322,12 +322,14 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 //     [N; dPD] K, N^T K + dPD^T Q -> dk, dq: sums of all the group's heads in tensor memory
 // and the row sums and column sums that dg and dbeta need, in fp32 registers.  A thread has one token and
 // half the channels (64) of the sums of dk or dq in registers.
+// A block stays on its SM and takes every gridDim-th (chunk, key head); the tiles of the next value head come
+// as soon as this one's have been read (the MMAs' and the dot products'), under the rest of its vector work.
 constexpr int G_VT = 256;                        // vector threads: warps 0..7; warp 8: copies and MMAs
 constexpr int G_THREADS = G_VT + 32;
-constexpr int GS_KQ = 0, GS_HO = 2 * TILE, GS_S = 4 * TILE, GS_DS = 6 * TILE, GS_U = 8 * TILE, GS_V = 9 * TILE,
-              GS_N = 10 * TILE, GS_ZERO = 11 * TILE;
+constexpr int GS_KQ = 0, GS_HO = 4 * TILE, GS_S = 6 * TILE, GS_DS = 8 * TILE, GS_U = 10 * TILE, GS_V = 11 * TILE,
+              GS_N = 12 * TILE, GS_ZERO = 13 * TILE;   // K, Q twice, as are the gates
 constexpr int GS_GATES = GS_ZERO + TILE / 2;     // one head's gates (all six)
-constexpr int GS_ROW = GS_GATES + 1536;          // floats [2 heads][2 halves][128]: row sums of the lanes
+constexpr int GS_ROW = GS_GATES + 2 * 1536;      // floats [2 heads][2 halves][128]: row sums of the lanes
 constexpr int GS_KUD = GS_ROW + 2 * 1024, GS_DB = GS_KUD + 2 * 512, GS_COL = GS_DB + 2 * 512;   // [2][2][64], [2][2][64], [2][4][64]
 constexpr int GS_SUM = GS_COL + 2 * 1024;        // [2][8]
 constexpr int GS_BAR = GS_SUM + 64, GS_BYTES = GS_BAR + 128 + 1024;
@@ -347,20 +349,51 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, TcP p)
 {
     const GdrArgs &a = p.a;
-    int n, c;
-    SeqSpan span;
-    if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *full = (uint64_t *)(sm + GS_BAR);                      // a head's tiles
     uint64_t *m_p = full + 1, *m_st = full + 2, *m_ud = full + 3, *m_acc = full + 4;   // products done
     uint64_t *b_n = full + 5, *b_d = full + 6;                       // [N; dPD] written; TG_ST and TG_UD read
-    uint64_t *drain = full + 7;
-    uint32_t *tslot = (uint32_t *)(full + 8);
+    uint64_t *b_dot = full + 7, *b_out = full + 8;                   // S, dS, H, V read; TG_ACC read
+    uint64_t *drain = full + 9;
+    uint32_t *tslot = (uint32_t *)(full + 10);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = blockIdx.y, rep = a.Hv / a.Hk;
-    const int row0 = span.row0 + c * CH, valid = min(CH, span.len - c * CH);
+    const int rep = a.Hv / a.Hk;
+    const long long nwork = gdr_slots(a.N, a.T) * a.Hk;
+    // the block's value heads in order: (slot, key head, head r of the group), i of them and wi groups before it
+    struct Unit {
+        long long w;
+        int slot, hk, r, row0, valid, i, wi;
+    };
+    auto seek = [&](Unit &u) {               // the first (slot, key head) from u.w on whose slot is a chunk
+        for (; u.w < nwork; u.w += gridDim.x) {
+            int n, c;
+            SeqSpan span;
+            u.slot = (int)(u.w / a.Hk);
+            u.hk = (int)(u.w % a.Hk);
+            if (find_slot(a.cu, a.N, a.T, u.slot, n, c, span)) {
+                u.row0 = span.row0 + c * CH;
+                u.valid = min(CH, span.len - c * CH);
+                return;
+            }
+        }
+    };
+    auto first = [&]() {
+        Unit u{(long long)blockIdx.x, 0, 0, 0, 0, 0, 0, 0};
+        seek(u);
+        return u;
+    };
+    auto next = [&](Unit u) {
+        ++u.i;
+        if (++u.r == rep) {
+            u.r = 0;
+            ++u.wi;
+            u.w += gridDim.x;
+            seek(u);
+        }
+        return u;
+    };
 
     if (tid == 0) {
         mbar_init(full, 1);
@@ -370,6 +403,8 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         mbar_init(m_acc, 1);
         mbar_init(b_n, G_VT / 32);
         mbar_init(b_d, G_VT / 32);
+        mbar_init(b_dot, G_VT / 32);
+        mbar_init(b_out, G_VT / 32);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -390,46 +425,51 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp == 8) {
         // ------------------------------------------------------------ copies and MMAs
         int issued = 0;
-        auto load = [&](int r) {
-            const int hv = hk * rep + r;
-            const size_t item = (size_t)blockIdx.x * a.Hv + hv;
-            mbar_arrive_expect_tx(full, (r == 0 ? 2 * TILE : 0) + 8 * TILE + 1536);
+        auto load = [&](const Unit &u) {
+            const int hv = u.hk * rep + u.r;
+            const size_t item = (size_t)u.slot * a.Hv + hv;
+            uint8_t *kq = sm + GS_KQ + (u.wi & 1) * 2 * TILE;
+            mbar_arrive_expect_tx(full, (u.r == 0 ? 2 * TILE : 0) + 8 * TILE + 1536);
             for (int cb = 0; cb < 2; ++cb) {
-                if (r == 0) {
-                    tma_load_4d(sm + GS_KQ + cb * TILE, &tm_k, cb * 64, hk, row0, 0, full);
-                    tma_load_4d(sm + GS_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row0, 0, full);
+                if (u.r == 0) {
+                    tma_load_4d(kq + cb * TILE, &tm_k, cb * 64, u.hk, u.row0, 0, full);
+                    tma_load_4d(kq + cb * TILE + TILE / 2, &tm_q, cb * 64, u.hk, u.row0, 0, full);
                 }
                 bulk_load(sm + GS_HO + cb * TILE, p.H + item * TILE + cb * (TILE / 2), TILE / 2, full);
-                tma_load_4d(sm + GS_HO + cb * TILE + TILE / 2, &tm_do, cb * 64, hv, row0, 0, full);
-                tma_load_4d(sm + GS_V + cb * (TILE / 2), &tm_v, cb * 64, hv, row0, 0, full);
+                tma_load_4d(sm + GS_HO + cb * TILE + TILE / 2, &tm_do, cb * 64, hv, u.row0, 0, full);
+                tma_load_4d(sm + GS_V + cb * (TILE / 2), &tm_v, cb * 64, hv, u.row0, 0, full);
             }
             bulk_load(sm + GS_U, p.U + item * TILE, TILE, full);
-            bulk_load(sm + GS_GATES, p.items + item * IT_BYTES + IT_GATES, 1536, full);
+            bulk_load(sm + GS_GATES + (u.i & 1) * 1536, p.items + item * IT_BYTES + IT_GATES, 1536, full);
             bulk_load(sm + GS_S, p.S + item * 2 * TILE, 2 * TILE, full);
             bulk_load(sm + GS_DS, p.dS + item * 2 * TILE, 2 * TILE, full);
-            issued = r + 1;
+            issued = u.i + 1;
         };
-        const uint32_t kq = smem_u32(sm + GS_KQ), ho = smem_u32(sm + GS_HO), ss = smem_u32(sm + GS_S), ds = smem_u32(sm + GS_DS),
+        const uint32_t ho = smem_u32(sm + GS_HO), ss = smem_u32(sm + GS_S), ds = smem_u32(sm + GS_DS),
                        uu = smem_u32(sm + GS_U), nn = smem_u32(sm + GS_N), zero = smem_u32(sm + GS_ZERO);
         constexpr uint32_t id_gram = idesc_bf16(128, 64, false, false), id_dp = idesc_bf16(128, 64, false, true),
                            id_st = idesc_bf16(128, 128, false, true), id_ud = idesc_bf16(128, 128, true, true);
         bool ok = true;
-        if (lane == 0) load(0);
-        for (int r = 0; r < rep && ok; ++r) {
-            ok = wait_all(full, r);
-            if (r == 0 && valid < CH) {   // K and Q rows behind the end meet the zeros of N and dPD
-                for (int u = lane; u < (CH - valid) * 32; u += 32) {
-                    const int t = valid + (u >> 5), b = (u >> 3) & 3;
-                    *(uint4 *)(sm + GS_KQ + (b >> 1) * TILE + (b & 1) * (TILE / 2) + swz(t, u & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        Unit u = first();
+        if (lane == 0 && u.w < nwork) load(u);
+        while (u.w < nwork && ok) {
+            const Unit v = next(u);
+            uint8_t *kqt = sm + GS_KQ + (u.wi & 1) * 2 * TILE;
+            const uint32_t kq = smem_u32(kqt);
+            ok = wait_all(full, u.i);
+            if (u.r == 0 && u.valid < CH) {   // K and Q rows behind the end meet the zeros of N and dPD
+                for (int x = lane; x < (CH - u.valid) * 32; x += 32) {
+                    const int t = u.valid + (x >> 5), b = (x >> 3) & 3;
+                    *(uint4 *)(kqt + (b >> 1) * TILE + (b & 1) * (TILE / 2) + swz(t, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async();
                 __syncwarp();
             }
             if (lane == 0 && ok) {
-                if (r > 0) ok = wait(b_d, r - 1);
+                if (u.i > 0) ok = wait(b_d, u.i - 1);
                 if (ok) {
                     tc_fence_after();
-                    if (r == 0)
+                    if (u.r == 0)
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             const uint32_t x = kq + (kk >> 2) * TILE + (kk & 3) * 32;
@@ -450,13 +490,13 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         mma_ss(tmem + TG_UD, sdesc(uu + kk * 2048, TILE, 1024), sdesc(ds + kk * 2048, TILE, 1024), id_ud, kk);
                     mma_commit(m_ud);
                 }
-                // [N; dPD] is there, and H, V, S and dS have been read: the next head's tiles may come
-                if (ok && (ok = wait(b_n, r)) && (ok = wait(m_ud, r))) {
-                    if (r + 1 < rep) load(r + 1);
+                // everything but K, Q and the gates has been read: the next head's tiles may come
+                if (ok && (ok = wait(b_dot, u.i)) && (ok = wait(m_ud, u.i)) && v.w < nwork) load(v);
+                if (ok && (ok = wait(b_n, u.i)) && (u.r > 0 || u.wi == 0 || (ok = wait(b_out, u.wi - 1)))) {
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // [N; dPD] K
-                        mma_ss(tmem + TG_ACC, sdesc(nn + kk * 32, 16, 1024), sdesc(kq + kk * 2048, TILE, 1024), id_st, r | kk);
+                        mma_ss(tmem + TG_ACC, sdesc(nn + kk * 32, 16, 1024), sdesc(kq + kk * 2048, TILE, 1024), id_st, u.r | kk);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)   // rows 0..63 += N^T K, dPD^T Q; rows 64..: zeros
                         mma_ss(tmem + TG_ACC, sdesc(nn + kk * 2048, zero - nn - (kk >> 2) * (TILE / 2), 1024),
@@ -465,6 +505,7 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            u = v;
         }
         if (lane == 0 && *abort_flag) {
             if (issued > 0) mbar_wait_timed(full, (uint32_t)((issued - 1) & 1), DRAIN_NS);
@@ -477,93 +518,97 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int L = 32 * lq + lane, t = L & 63;        // lane of tensor memory, token
         const bool krow = lq < 2;                        // a warp of k rows; else of q rows
         const uint32_t at = tmem + ((uint32_t)(32 * lq) << 16);
-        const float *gates = (const float *)(sm + GS_GATES);
         float acc[64];                                   // channels 64 half ..: sums of dk or dq of row t
-#pragma unroll
-        for (int e = 0; e < 64; ++e) acc[e] = 0.0f;
         bool ok = true;
-        const uint8_t *own = sm + GS_KQ + half * TILE;   // K, Q rows as the tiles have them: row L, channel block `half`
         float gC = 0.0f;
         float *s_row, *s_kud, *s_db, *s_col, *s_sum;     // of even and odd heads in turn
-        auto head = [&](int r) {                         // false: a wait has given up
-            if (!wait_all(full, r)) return false;
+        auto head = [&](const Unit &u) {                 // false: a wait has given up
+            const int valid = u.valid;
+            const float *gates = (const float *)(sm + GS_GATES + (u.i & 1) * 1536);
+            const uint8_t *own = sm + GS_KQ + ((u.wi & 1) * 2 + half) * TILE;   // K, Q rows as the tiles have them: row L, block `half`
+            if (u.r == 0)
+#pragma unroll
+                for (int e = 0; e < 64; ++e) acc[e] = 0.0f;
+            if (!wait_all(full, u.i)) return false;
             gC = gates[GA_GAM + CH - 1];
             const float gm = gates[GA_GAM + t], lm = gates[GA_LAM + t], bt = gates[GA_BETA + t];
             const float ghi = gates[GA_HI + t], glo = gates[GA_LO + t];
             // <S, dS> of the block, H.V of the row
             {
                 float x = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    x += dot8(*(const uint4 *)(sm + GS_S + 16 * (tid + u * G_VT)), *(const uint4 *)(sm + GS_DS + 16 * (tid + u * G_VT)));
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i)
+                    x += dot8(*(const uint4 *)(sm + GS_S + 16 * (tid + i * G_VT)), *(const uint4 *)(sm + GS_DS + 16 * (tid + i * G_VT)));
                 x = warp_sum(x);
                 if (lane == 0) s_sum[warp] = x;
             }
             float db = 0.0f, row = 0.0f;
             if (krow)
-#pragma unroll
+#pragma unroll 2
                 for (int j = 0; j < 8; ++j)
                     db += dot8(*(const uint4 *)(sm + GS_HO + half * TILE + swz(t, j)), *(const uint4 *)(sm + GS_V + half * (TILE / 2) + swz(t, j)));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_dot);
             // [K; Q] K^T and [H; dO] U^T, columns s = 32 half ..
-            if (!wait_all(m_p, r)) return false;
+            if (!wait_all(m_p, u.i)) return false;
             tc_fence_after();
-            float e32[32];
             const int s0 = 32 * half;
-            if (s0 > 32 * (lq & 1) + 31) {               // the warp's rows all end before its columns
+            if (u.i > 0 && !wait_all(m_acc, u.i - 1)) return false;      // the head before has been read
+            const float sc = krow ? -bt : 1.0f;
+            const int last = t >= valid ? -1 : krow ? t - 1 : t;         // N is strictly lower, dPD has the diagonal
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {                // eight columns at a time: code that stays in the instruction cache
+                const int c0 = s0 + 8 * c;
+                float e8[8];
+                uint32_t w[4] = {};
+                if (c0 > 32 * (lq & 1) + 31) {           // the warp's rows all end before these columns
 #pragma unroll
-                for (int e = 0; e < 32; ++e) e32[e] = 0.0f;
-                if (r > 0 && !wait_all(m_acc, r - 1)) return false;
+                    for (int e = 0; e < 8; ++e) e8[e] = 0.0f;
+                } else {
+                    uint32_t g8[8], x8[8];
+                    tmem_ld8(at + TG_GRAM + c0, g8);
+                    tmem_ld8(at + TG_DP + c0, x8);
+                    float h[8], l[8];
+                    ld4(gates + GA_HI + c0, *(float(*)[4])h);
+                    ld4(gates + GA_HI + c0 + 4, *(float(*)[4])(h + 4));
+                    ld4(gates + GA_LO + c0, *(float(*)[4])l);
+                    ld4(gates + GA_LO + c0 + 4, *(float(*)[4])(l + 4));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *(uint4 *)(sm + GS_N + swz(L, 4 * half + j)) = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                uint32_t g32[32], x32[32];
-                tmem_ld32(at + TG_GRAM + s0, g32);
-                tmem_ld32(at + TG_DP + s0, x32);
-                tmem_wait_ld();
-                const float sc = krow ? -bt : 1.0f;
-                const int last = t >= valid ? -1 : krow ? t - 1 : t;   // N is strictly lower, dPD has the diagonal
+                    for (int e = 0; e < 8; ++e) h[e] = __expf((ghi - h[e]) + (glo - l[e]));
+                    tmem_wait_ld();
+                    float y[8];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float h4[4], l4[4];
-                    ld4(gates + GA_HI + s0 + e, h4);
-                    ld4(gates + GA_LO + s0 + e, l4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int s = s0 + e + i;
-                        const float y = s <= last ? __expf((ghi - h4[i]) + (glo - l4[i])) * __uint_as_float(x32[e + i]) : 0.0f;
-                        const float g = s <= last && s < t ? __uint_as_float(g32[e + i]) : 0.0f;   // s == t cancels in rows - columns
-                        e32[e + i] = sc * y * g;
-                        row += e32[e + i];
-                        if (krow) db -= y * g;
-                        x32[e + i] = __float_as_uint(sc * y);
+                    for (int e = 0; e < 8; ++e) {
+                        const float z = h[e] * __uint_as_float(x8[e]), zg = z * __uint_as_float(g8[e]);
+                        const bool in = c0 + e <= last, off = in && c0 + e < t;      // s == t cancels in rows - columns
+                        y[e] = in ? sc * z : 0.0f;
+                        e8[e] = off ? sc * zg : 0.0f;
+                        row += e8[e];
+                        if (krow) db -= off ? zg : 0.0f;
                     }
-                }
-                if (r > 0 && !wait_all(m_acc, r - 1)) return false;      // the head before has been read
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = pack_bf16x2(__uint_as_float(x32[8 * j + 2 * i]), __uint_as_float(x32[8 * j + 2 * i + 1]));
-                    *(uint4 *)(sm + GS_N + swz(L, 4 * half + j)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
                 }
+                *(uint4 *)(sm + GS_N + swz(L, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                // column sums over the warp's 32 rows: lane l gets column c0 + l / 4
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                    for (int e = 0; e < o; ++e) {
+                        const bool up = lane & (4 * o);
+                        const float mine = up ? e8[e + o] : e8[e], give = up ? e8[e] : e8[e + o];
+                        e8[e] = mine + __shfl_xor_sync(0xffffffffu, give, 4 * o);
+                    }
+                e8[0] += __shfl_xor_sync(0xffffffffu, e8[0], 2);
+                e8[0] += __shfl_xor_sync(0xffffffffu, e8[0], 1);
+                if ((lane & 3) == 0) s_col[lq * 64 + c0 + (lane >> 2)] = e8[0];
             }
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_n);
-            // column sums over the warp's 32 rows: lane l gets column s0 + l
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int e = 0; e < o; ++e) {
-                    const bool up = lane & o;
-                    const float mine = up ? e32[e + o] : e32[e], give = up ? e32[e] : e32[e + o];
-                    e32[e] = mine + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-            s_col[lq * 64 + s0 + lane] = e32[0];
             // [H; dO] S^T
-            if (!wait_all(m_st, r)) return false;
+            if (!wait_all(m_st, u.i)) return false;
             tc_fence_after();
             {
                 const float sc = krow ? -bt * gm : gm;
@@ -591,7 +636,7 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             // U dS^T
             float kud = 0.0f;
-            if (!wait_all(m_ud, r)) return false;
+            if (!wait_all(m_ud, u.i)) return false;
             tc_fence_after();
             if (krow) {
 #pragma unroll
@@ -621,14 +666,14 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (lane == 0) mbar_arrive(b_d);
             return true;
         };
-        for (int r = 0; r < rep; ++r) {
-            const int hv = hk * rep + r, par = r & 1;
+        for (Unit u = first(); u.w < nwork; u = next(u)) {
+            const int hv = u.hk * rep + u.r, par = u.i & 1, row0 = u.row0, valid = u.valid;
             s_row = (float *)(sm + GS_ROW) + par * 256;
             s_kud = (float *)(sm + GS_KUD) + par * 128;
             s_db = (float *)(sm + GS_DB) + par * 128;
             s_col = (float *)(sm + GS_COL) + par * 256;
             s_sum = (float *)(sm + GS_SUM) + par * 8;
-            ok = ok && head(r);
+            ok = ok && head(u);
             named_bar_sync(1, G_VT);                     // by all warps, whatever their waits said
             if (!ok) continue;
             if (warp == 0) {
@@ -637,11 +682,11 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 base *= gC;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int u = lane + 32 * i;
-                    x[i] = (s_row[u] + s_row[128 + u]) + (s_row[64 + u] + s_row[192 + u]);
-                    x[i] -= (s_col[u] + s_col[64 + u]) + (s_col[128 + u] + s_col[192 + u]);
-                    w[i] = s_kud[u] + s_kud[64 + u];
-                    if (u >= valid) x[i] = w[i] = 0.0f;
+                    const int t = lane + 32 * i;
+                    x[i] = (s_row[t] + s_row[128 + t]) + (s_row[64 + t] + s_row[192 + t]);
+                    x[i] -= (s_col[t] + s_col[64 + t]) + (s_col[128 + t] + s_col[192 + t]);
+                    w[i] = s_kud[t] + s_kud[64 + t];
+                    if (t >= valid) x[i] = w[i] = 0.0f;
                 }
                 float lo, hi, wl, wh;
                 sums_across(x[0], x[1], w[0], w[1], lo, hi, wl, wh, lane);
@@ -649,13 +694,13 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (lane < valid) dg[(size_t)lane * a.Hv] = __float2bfloat16_rn(base + wl + lo);
                 if (lane + 32 < valid) dg[(size_t)(lane + 32) * a.Hv] = __float2bfloat16_rn(base + wh + hi);
             } else if (warp < 3) {
-                const int u = 32 * (warp - 1) + lane;
-                if (u < valid) ((__nv_bfloat16 *)a.dbeta)[(size_t)(row0 + u) * a.Hv + hv] = __float2bfloat16_rn(s_db[u] + s_db[64 + u]);
+                const int t = 32 * (warp - 1) + lane;
+                if (t < valid) ((__nv_bfloat16 *)a.dbeta)[(size_t)(row0 + t) * a.Hv + hv] = __float2bfloat16_rn(s_db[t] + s_db[64 + t]);
             }
-        }
-        if (ok && (ok = wait_all(m_acc, rep - 1))) {
+            if (u.r + 1 < rep) continue;
+            if (!(ok = wait_all(m_acc, u.i))) continue;
             tc_fence_after();
-            __nv_bfloat16 *dst = (__nv_bfloat16 *)(krow ? a.dk_ : a.dq) + ((size_t)(row0 + t) * a.Hk + hk) * D + 64 * half;
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)(krow ? a.dk_ : a.dq) + ((size_t)(row0 + t) * a.Hk + u.hk) * D + 64 * half;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t x[32];
@@ -672,6 +717,9 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         *(uint4 *)(dst + 32 * hf + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_out);
         }
     }
     tc_fence_before();
@@ -701,7 +749,11 @@ cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s)
     gdr_reverse_tc_kernel<<<(unsigned)(a.N * a.Hv), W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mo, p);
     if (a.T > 0) {
         if ((e = smem_opt_in<TagG>((const void *)gdr_grads_tc_kernel, GS_BYTES)) != cudaSuccess) return e;
-        gdr_grads_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hk), G_THREADS, GS_BYTES, s>>>(mq, mk, mv, mo, p);
+        int dev = 0, sms = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        const long long work = gdr_slots(a.N, a.T) * a.Hk;
+        gdr_grads_tc_kernel<<<(unsigned)(work < sms ? work : sms), G_THREADS, GS_BYTES, s>>>(mq, mk, mv, mo, p);
     }
     return cudaGetLastError();
 }
