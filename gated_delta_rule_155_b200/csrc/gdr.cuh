@@ -179,7 +179,7 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
     {   // 32 -> 64: four columns a thread
         const int r = tid >> 3, c = 4 * (tid & 7);
         float s[4] = {};
-#pragma unroll
+#pragma unroll 2
         for (int m = 0; m < 32; m += 4) {        // every lane at the same row of M: one wavefront a load, zeros included
             float a[4];
             ld4(A + (32 + r) * LD + m, a);
@@ -194,6 +194,7 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
         st4(tmp + r * LD + c, s);
         __syncthreads();
         float x[4] = {};
+#pragma unroll 1
         for (int m = 0; m <= (r | 3); m += 4) {  // a warp has four rows
             float a[4];
             ld4(M + (32 + r) * LD + 32 + m, a);

@@ -100,6 +100,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (mbar_wait_bounded(&bars[0], 0, abort_flag, a.err, p.wait_ns)) {
             const uint32_t kq = smem_u32(sm + PR_KQ);
             constexpr uint32_t id = idesc_bf16(128, 64, false, false);
+#pragma unroll 2
             for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t at = kq + (kk >> 2) * TILE + (kk & 3) * 32;
                 mma_ss(tmem, sdesc(at, 16, 1024), sdesc(at, 16, 1024), id, kk > 0);
@@ -132,36 +133,29 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int t = r & 63;
         const int last = t >= valid ? -1 : r < 64 ? t - 1 : t;   // A is strictly lower; rows behind the end may hold NaN
         const float gh = ghi[t], gl = glo[t], scale = r < 64 ? beta[t] : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {          // eight columns at a time: the instruction cache bounds this kernel
+            const int c0 = s0 + 8 * c;
+            float y[8] = {};
+            if (c0 <= 32 * (lq & 1) + 31) {    // else the warp's rows all end before these columns
+                uint32_t x[8];
+                tmem_ld8(at + 8 * c, x);
+                float h[8], l[8];
+                ld4(ghi + c0, *(float(*)[4])h);
+                ld4(ghi + c0 + 4, *(float(*)[4])(h + 4));
+                ld4(glo + c0, *(float(*)[4])l);
+                ld4(glo + c0 + 4, *(float(*)[4])(l + 4));
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {       // 16 columns at a time
-            const int c0 = s0 + 16 * hf;
-            float y[16];
-            if (c0 > 32 * (lq & 1) + 31) {     // the warp's rows all end before these columns
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-            } else {
-                uint32_t x[16];
-                tmem_ld16(at + 16 * hf, x);
+                for (int e = 0; e < 8; ++e) h[e] = scale * __expf((gh - h[e]) + (gl - l[e]));
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    float h4[4], l4[4];
-                    ld4(ghi + c0 + e, h4);
-                    ld4(glo + c0 + e, l4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float d = __expf((gh - h4[i]) + (gl - l4[i]));
-                        y[e + i] = c0 + e + i <= last ? scale * d * __uint_as_float(x[e + i]) : 0.0f;
-                    }
-                }
+                for (int e = 0; e < 8; ++e) y[e] = c0 + e <= last ? h[e] * __uint_as_float(x[e]) : 0.0f;
             }
             if (r < 64) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) st4(A + t * LM + c0 + e, *(const float(*)[4])(y + e));
+                st4(A + t * LM + c0, *(const float(*)[4])y);
+                st4(A + t * LM + c0 + 4, *(const float(*)[4])(y + 4));
             } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    put_split(sm + PR_P, sm + PR_P + TILE / 2, t, c0 / 8 + j, *(const float(*)[8])(y + 8 * j));
+                put_split(sm + PR_P, sm + PR_P + TILE / 2, t, c0 / 8, y);
             }
         }
         fence_proxy_async();
@@ -172,7 +166,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         unit_lower_inverse<LM>(A, M, tid);
         {                                      // M as hi + lo
             const int t = tid >> 2;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 float y[8];
                 const int q8 = (tid & 3) + 4 * j;      // a quarter of a warp reads 8 different bank groups
@@ -189,6 +183,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         const uint32_t pp = smem_u32(sm + PR_P), mm = smem_u32(sm + PR_MHL);
         constexpr uint32_t id = idesc_bf16(128, 64, false, true);
+#pragma unroll 1
         for (int kk = 0; kk < 4; ++kk) {
             const uint64_t ph = sdesc(pp + kk * 32, 16, 1024), pl = sdesc(pp + TILE / 2 + kk * 32, 16, 1024);
             const uint64_t mh = sdesc(mm + kk * 2048, TILE / 2, 1024), ml = sdesc(mm + TILE / 2 + kk * 2048, TILE / 2, 1024);
@@ -204,18 +199,15 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (ok) {
         tc_fence_after();
         if (r < 64) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {   // over P, which has been read
-                uint32_t x[16];
-                tmem_ld16(at + 16 * hf, x);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {      // over P, which has been read
+                uint32_t x[8];
+                tmem_ld8(at + 8 * c, x);
                 tmem_wait_ld();
+                float y[8];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float y[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[8 * j + e]);
-                    put_split(sm + PR_P, sm + PR_P + TILE / 2, r, 4 * half + 2 * hf + j, y);
-                }
+                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[e]);
+                put_split(sm + PR_P, sm + PR_P + TILE / 2, r, 4 * half + c, y);
             }
             fence_proxy_async();
         }

@@ -55,6 +55,16 @@ KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
     lo = pack_bf16x2(x0 - h.x, x1 - h.y);
 }
 
+// find_slot for a chunk's first row and its rows: {row, rows}, rows 0 for a slot that no chunk has (out of
+// line: where it is called from four places, the instruction cache bounds the kernel)
+static __device__ __noinline__ int2 slot_rows(const int *cu, int N, int T, int slot)
+{
+    int n, c;
+    SeqSpan span;
+    if (!find_slot(cu, N, T, slot, n, c, span)) return make_int2(0, 0);
+    return make_int2(span.row0 + c * CH, min(CH, span.len - c * CH));
+}
+
 // 8 values of a row -> the row's 16-byte pieces of a hi and a lo tile
 KDA_DEVICE void put_split(uint8_t *hi, uint8_t *lo, int row, int j, const float (&x)[8])
 {

@@ -368,15 +368,12 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     };
     auto seek = [&](Unit &u) {               // the first (slot, key head) from u.w on whose slot is a chunk
         for (; u.w < nwork; u.w += gridDim.x) {
-            int n, c;
-            SeqSpan span;
             u.slot = (int)(u.w / a.Hk);
             u.hk = (int)(u.w % a.Hk);
-            if (find_slot(a.cu, a.N, a.T, u.slot, n, c, span)) {
-                u.row0 = span.row0 + c * CH;
-                u.valid = min(CH, span.len - c * CH);
-                return;
-            }
+            const int2 rows = slot_rows(a.cu, a.N, a.T, u.slot);
+            u.row0 = rows.x;
+            u.valid = rows.y;
+            if (rows.y) return;
         }
     };
     auto first = [&]() {
