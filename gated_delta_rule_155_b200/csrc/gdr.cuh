@@ -109,10 +109,50 @@ KDA_DEVICE bool page_is_free(const int *sT_index, const int *s0_index, bool same
     return !__syncthreads_or(clash);
 }
 
+// c += A B for an A of 16 x 8 K floats (rows of lda) and a B of 8 K x 8 (rows of ldb), one warp: tf32 products
+// of hi and lo parts (hi: the upper 11 bits, exact; lo x lo left out), so good to about 2^-21 of the terms.
+// Lane l has rows l / 4 and l / 4 + 8 of columns 2 (l % 4) and the next.  A 16-byte load from shared memory
+// costs four cycles however many lanes share its address, so products of 16 x 16 blocks on CUDA cores (20
+// loads for 64 FMAs) spent four times the cycles that these fragments do.
+template <int K>
+KDA_DEVICE void mma_block(float (&c)[4], const float *A, int lda, const float *B, int ldb, int lane)
+{
+    const float *a = A + (lane >> 2) * lda + (lane & 3), *b = B + (lane & 3) * ldb + (lane >> 2);
+#pragma unroll
+    for (int k = 0; k < 8 * K; k += 8) {
+        const float x[4] = {a[k], a[8 * lda + k], a[k + 4], a[8 * lda + k + 4]}, y[2] = {b[k * ldb], b[(k + 4) * ldb]};
+        uint32_t xh[4], xl[4], yh[2], yl[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            xh[i] = __float_as_uint(x[i]) & 0xffffe000u;
+            xl[i] = __float_as_uint(x[i] - __uint_as_float(xh[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            yh[i] = __float_as_uint(y[i]) & 0xffffe000u;
+            yl[i] = __float_as_uint(y[i] - __uint_as_float(yh[i]));
+        }
+        auto mma = [&](const uint32_t (&p)[4], const uint32_t (&q)[2]) {
+            asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(q[0]), "r"(q[1]));
+        };
+        mma(xl, yh);
+        mma(xh, yl);
+        mma(xh, yh);
+    }
+}
+KDA_DEVICE void put_block(float *dst, int ld, const float (&c)[4], float sign, int lane)
+{
+    float *d = dst + (lane >> 2) * ld + 2 * (lane & 3);
+    *(float2 *)d = make_float2(sign * c[0], sign * c[1]);
+    *(float2 *)(d + 8 * ld) = make_float2(sign * c[2], sign * c[3]);
+}
+
 // M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats: the 16 x 16 diagonal blocks
 // by forward substitution (one column a thread: a product form such as (I - A)(I + A^2)... would cancel
-// where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64),
-// every product in fp32.  A's upper right quarter is scratch.  256 threads; M's upper triangle is written
+// where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64)
+// with mma_block's products.  A's upper right quarter is scratch.  256 threads; M's upper triangle is written
 // as zeros.  Ends with a barrier.
 template <int LD>
 KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
@@ -144,69 +184,31 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
         }
     }
     __syncthreads();
-    {   // 16 -> 32, two pairs of blocks: two columns a thread
-        const int o = 32 * (tid >> 7), r = (tid & 127) >> 3, c = 2 * (tid & 7);
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int m = 0; m < 16; m += 4) {
-            float a[4];
-            ld4(A + (o + 16 + r) * LD + o + m, a);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 b = *(const float2 *)(M + (o + m + e) * LD + o + c);
-                s0 += a[e] * b.x;
-                s1 += a[e] * b.y;
-            }
+    const int w = tid >> 5, lane = tid & 31;
+    {   // 16 -> 32: two pairs of blocks, eight columns a warp
+        const int o = 32 * (w >> 1), n = 8 * (w & 1);
+        if (w < 4) {
+            float c[4] = {};
+            mma_block<2>(c, A + (o + 16) * LD + o, LD, M + o * LD + o + n, LD, lane);
+            put_block(tmp + (o >> 1) * LD + n, LD, c, 1.0f, lane);
         }
-        float *t = tmp + (o >> 1) * LD;
-        *(float2 *)(t + r * LD + c) = make_float2(s0, s1);
         __syncthreads();
-        s0 = s1 = 0.0f;
-#pragma unroll
-        for (int m = 0; m < 16; m += 4) {
-            float a[4];
-            ld4(M + (o + 16 + r) * LD + o + 16 + m, a);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 b = *(const float2 *)(t + (m + e) * LD + c);
-                s0 -= a[e] * b.x;
-                s1 -= a[e] * b.y;
-            }
+        if (w < 4) {
+            float c[4] = {};
+            mma_block<2>(c, M + (o + 16) * LD + o + 16, LD, tmp + (o >> 1) * LD + n, LD, lane);
+            put_block(M + (o + 16) * LD + o + n, LD, c, -1.0f, lane);
         }
-        *(float2 *)(M + (o + 16 + r) * LD + o + c) = make_float2(s0, s1);
     }
     __syncthreads();
-    {   // 32 -> 64: four columns a thread
-        const int r = tid >> 3, c = 4 * (tid & 7);
-        float s[4] = {};
-#pragma unroll 2
-        for (int m = 0; m < 32; m += 4) {        // every lane at the same row of M: one wavefront a load, zeros included
-            float a[4];
-            ld4(A + (32 + r) * LD + m, a);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float b[4];
-                ld4(M + (m + e) * LD + c, b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += a[e] * b[j];
-            }
-        }
-        st4(tmp + r * LD + c, s);
+    {   // 32 -> 64: sixteen rows and eight columns a warp
+        const int m = 16 * (w >> 2), n = 8 * (w & 3);
+        float c[4] = {};
+        mma_block<4>(c, A + (32 + m) * LD, LD, M + n, LD, lane);
+        put_block(tmp + m * LD + n, LD, c, 1.0f, lane);
         __syncthreads();
         float x[4] = {};
-#pragma unroll 1
-        for (int m = 0; m <= (r | 3); m += 4) {  // a warp has four rows
-            float a[4];
-            ld4(M + (32 + r) * LD + 32 + m, a);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float b[4];
-                ld4(tmp + (m + e) * LD + c, b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] -= a[e] * b[j];
-            }
-        }
-        st4(M + (32 + r) * LD + c, x);
+        mma_block<4>(x, M + (32 + m) * LD + 32, LD, tmp + n, LD, lane);
+        put_block(M + (32 + m) * LD + n, LD, x, -1.0f, lane);
     }
     __syncthreads();
 }
