@@ -1,5 +1,5 @@
-// gdr_simt.cu — the head-gated delta rule in chunks of 64 tokens, exact fp32 on CUDA cores: every
-// dtype and head size (bf16 at dk = dv = 128 has its own tensor-core kernels).
+// gdr_simt.cu — the head-gated delta rule in chunks of 64 tokens, to fp32 accuracy: every dtype and
+// head size (bf16 at dk = dv = 128 has its own tensor-core kernels).
 //
 // One value head, one chunk, with G the running sum of the log-decays, gamma = e^G,
 // lam_s = e^(G_C - G_s), D_ts = e^(G_t - G_s) for s <= t (all differences are <= 0 for g <= 0, so no
@@ -34,10 +34,12 @@ namespace {
 using namespace gdr;
 
 constexpr int NT = 256;         // threads of prep and of the gradients
-constexpr int WT = 128;         // threads of a walk
+constexpr int WT = 256;         // threads of a walk
 constexpr int NS = 16;          // state columns of a walk's block
 constexpr int LM = 68;          // row stride of 64 x 64 fp32 tiles
-constexpr int LS = NS + 4;      // row stride of state slices
+// Row stride of 16-column operands: 24 spreads the four rows and eight columns of a fragment over all banks
+// (at dk = 128 there is room for 20 only, where two of the rows share eight banks)
+template <int DK> constexpr int LS = DK == 64 ? 24 : 20;
 constexpr int ITEM = 2 * CH * CH + 256;   // floats of a chunk and value head: M, P M, then gamma, lam, beta (64 each)
 
 struct Ws {                     // fp32 workspace, items = slots * Hv
@@ -105,44 +107,57 @@ KDA_DEVICE void load_gates(Gates &s, const IO *g, const IO *beta, size_t row0, i
 }
 KDA_DEVICE float decay(const Gates &s, int t, int u) { return __expf((s.hi[t] - s.hi[u]) + (s.lo[t] - s.lo[u])); }
 
-// acc[i][j] += sum_k A[ra + i][k] B[rb + 16 j][k]   (both rows along k, K a multiple of 4)
-template <int K, int NI, int NJ>
-KDA_DEVICE void mm_nt(float (&acc)[NI][NJ], const float *A, int lda, const float *B, int ldb)
+// Products of shared-memory operands by warps, to fp32 accuracy on tf32 MMAs: x = hi + lo with hi rounded to
+// tf32's 11 bits and lo the exact rest (read to 11 bits: x is off by 2^-23), products lo hi, hi lo, hi hi;
+// lo lo is left out (2^-24).  Eight products at a time are summed by the MMA, which truncates, and added to
+// the result with a rounded addition, so that long sums do not drift.
+//   acc[i] += A[16 rows, k0 .. k1) B[k0 .. k1, columns 8 i ..), row r and k of A at A[r ar + k ak], k and
+//   column n of B at B[k bk + n bn]; SCALED: row k of B times scale[k].
+// Lane l has rows l / 4 (elements 0, 1) and l / 4 + 8 (2, 3), columns 2 (l % 4) and the next.
+KDA_DEVICE void split_tf32(float x, uint32_t &hi, uint32_t &lo)
 {
-#pragma unroll 4
-    for (int k = 0; k < K; k += 4) {
-        float4 a[NI];
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+KDA_DEVICE void mma_tf32(float (&c)[4], const uint32_t (&p)[4], const uint32_t (&q)[2])
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(q[0]), "r"(q[1]));
+}
+template <int NTL, bool SCALED = false>
+KDA_DEVICE void mm(float (&acc)[NTL][4], int k0, int k1, const float *A, int ar, int ak, const float *B, int bk, int bn, int lane,
+                   const float *scale = nullptr)
+{
+    const float *a = A + (lane >> 2) * ar + (lane & 3) * ak, *b = B + (lane & 3) * bk + (lane >> 2) * bn;
+    constexpr int AHEAD = NTL >= 4 ? 1 : 2;  // (a wide step is enough independent work, and code is what the caches lack)
+#pragma unroll AHEAD
+    for (int k = k0; k < k1; k += 8) {
+        uint32_t ah[4], al[4];
+        split_tf32(a[k * ak], ah[0], al[0]);
+        split_tf32(a[8 * ar + k * ak], ah[1], al[1]);
+        split_tf32(a[(k + 4) * ak], ah[2], al[2]);
+        split_tf32(a[8 * ar + (k + 4) * ak], ah[3], al[3]);
+        float s0 = 1.0f, s1 = 1.0f;
+        if (SCALED) {
+            s0 = scale[k + (lane & 3)];
+            s1 = scale[k + 4 + (lane & 3)];
+        }
 #pragma unroll
-        for (int i = 0; i < NI; ++i) a[i] = *(const float4 *)(A + i * lda + k);
+        for (int i = 0; i < NTL; ++i) {
+            uint32_t bh[2], bl[2];
+            split_tf32(SCALED ? s0 * b[k * bk + 8 * i * bn] : b[k * bk + 8 * i * bn], bh[0], bl[0]);
+            split_tf32(SCALED ? s1 * b[(k + 4) * bk + 8 * i * bn] : b[(k + 4) * bk + 8 * i * bn], bh[1], bl[1]);
+            float c[4] = {};
+            mma_tf32(c, al, bh);
+            mma_tf32(c, ah, bl);
+            mma_tf32(c, ah, bh);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const float4 b = *(const float4 *)(B + 16 * j * ldb + k);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                acc[i][j] += a[i].x * b.x + a[i].y * b.y + a[i].z * b.z + a[i].w * b.w;
+            for (int e = 0; e < 4; ++e) acc[i][e] += c[e];
         }
     }
 }
-// acc[i][j] += sum_k A[i][k] B[k][j]   (A rows along k, B rows of 4 consecutive columns)
-template <int K>
-KDA_DEVICE void mm_nn(float (&acc)[4][4], const float *A, int lda, const float *B, int ldb)
-{
-#pragma unroll 4
-    for (int k = 0; k < K; k += 4) {
-        float a[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ld4(A + i * lda + k, a[i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float b[4];
-            ld4(B + (k + e) * ldb, b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[i][e] * b[j];
-        }
-    }
-}
+
 // ---------------------------------------------------------------- prep: M and P M of every chunk
 template <typename IO, int DK>
 __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
@@ -163,29 +178,41 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
     load_rows<IO, DK, LK>(Q, (const IO *)a.q, row0, a.Hk, hk, valid, tid);
     load_gates<IO>(gs, (const IO *)a.g, (const IO *)a.beta, row0, a.Hv, hv, valid, tid);
     __syncthreads();
-    const int ty = tid >> 4, tx = tid & 15;
-    float kk[4][4] = {}, qk[4][4] = {};
-    mm_nt<DK>(kk, K + 4 * ty * LK, LK, K + tx * LK, LK);
-    mm_nt<DK>(qk, Q + 4 * ty * LK, LK, K + tx * LK, LK);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = 4 * ty + i, s = tx + 16 * j;
-            const float d = s <= t ? decay(gs, t, s) : 0.0f;
-            A[t * LM + s] = s < t ? gs.beta[t] * d * kk[i][j] : 0.0f;
-            Pm[t * LM + s] = s <= t ? d * qk[i][j] : 0.0f;
+    // rows 16 m .. of the warp, columns 32 h ..
+    const int w = tid >> 5, lane = tid & 31, m = 16 * (w >> 1), h = 32 * (w & 1), g4 = lane >> 2, c2 = 2 * (lane & 3);
+    {
+        float kk[4][4] = {}, qk[4][4] = {};
+        if (h <= m) {
+            mm<4>(kk, 0, DK, K + m * LK, LK, 1, K + h * LK, 1, LK, lane);
+            mm<4>(qk, 0, DK, Q + m * LK, LK, 1, K + h * LK, 1, LK, lane);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int t = m + g4 + 4 * e, s = h + 8 * i + c2;
+                float2 x, y;
+                const float d0 = s <= t ? decay(gs, t, s) : 0.0f, d1 = s + 1 <= t ? decay(gs, t, s + 1) : 0.0f;
+                x.x = s < t ? gs.beta[t] * d0 * kk[i][e] : 0.0f;
+                x.y = s + 1 < t ? gs.beta[t] * d1 * kk[i][e + 1] : 0.0f;
+                y.x = s <= t ? d0 * qk[i][e] : 0.0f;
+                y.y = s + 1 <= t ? d1 * qk[i][e + 1] : 0.0f;
+                *(float2 *)(A + t * LM + s) = x;
+                *(float2 *)(Pm + t * LM + s) = y;
+            }
+    }
     __syncthreads();
     unit_lower_inverse<LM>(A, M, tid);
     const size_t item = (size_t)blockIdx.x * a.Hv + hv;
+    float *dst = p.w.I + item * ITEM;
     float pm[4][4] = {};
-    mm_nn<CH>(pm, Pm + 4 * ty * LM, LM, M + 4 * tx, LM);
+    if (h <= m) mm<4>(pm, h, m + 16, Pm + m * LM, LM, 1, M + h, LM, 1, lane);   // both lower
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        st4(p.w.I + item * ITEM + CH * CH + (4 * ty + i) * CH + 4 * tx, pm[i]);
-        st4(p.w.I + item * ITEM + (4 * ty + i) * CH + 4 * tx, *(const float(*)[4])(M + (4 * ty + i) * LM + 4 * tx));
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+            *(float2 *)(dst + CH * CH + (m + g4 + 4 * e) * CH + h + 8 * i + c2) = make_float2(pm[i][e], pm[i][e + 1]);
+    for (int u = tid; u < CH * CH / 4; u += NT) *(float4 *)(dst + 4 * u) = *(const float4 *)(M + (u >> 4) * LM + 4 * (u & 15));
     if (tid < CH) {
         float *g = p.w.I + item * ITEM + 2 * CH * CH + tid;
         g[0] = gs.gam[tid];
@@ -195,11 +222,9 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
 }
 
 // ---------------------------------------------------------------- the walks along a sequence
-// A block has 16 columns of a head's state, its rows in registers (and as an operand in shared memory).
-// Thread (rg, cg): tokens rg and rg + 32 of the chunk's products, or dk / 32 state rows, of columns
-// cg .. cg + 3, so a product's step of four k is 4 + 4 16-byte loads for 64 FMAs and what a token's rows
-// of one product give stays in registers for the next.  The next chunk's tiles come by cp.async (bf16:
-// through registers) under this chunk's products.
+// A block has 16 columns of a head's state, in registers as the MMAs' results lie (and as an operand in shared
+// memory).  What a warp has of one product's rows stays in its registers for the next, three barriers a chunk;
+// the next chunk's tiles come by cp.async (bf16: through registers) under this chunk's products.
 KDA_DEVICE void cp_async16(void *dst, const void *src, bool take)
 {
     const int n = take ? 16 : 0;
@@ -240,7 +265,7 @@ struct Tiles {
     }
     KDA_DEVICE void put(float *b, int tid)   // bf16: the rows that fetch has read
     {
-        if (DIRECT) return;
+        if constexpr (!DIRECT)
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int u = tid + i * WT, r = u / (DK / 8), c = 8 * (u % (DK / 8));
@@ -257,33 +282,11 @@ struct Tiles {
     }
 };
 
-// acc[i][j] += sum_{k < K} A[32 i ld + k] B[k][j]: NI rows 32 apart, four columns
-template <int K, int NI>
-KDA_DEVICE void mm_rows(float (&acc)[NI][4], const float *A, int lda, int step, const float *B)
-{
-#pragma unroll 4
-    for (int k = 0; k < K; k += 4) {
-        float a[NI][4];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) ld4(A + i * step * lda + k, a[i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float b[4];
-            ld4(B + (k + e) * LS, b);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[i][e] * b[j];
-        }
-    }
-}
-// SR consecutive floats
-template <int SR>
-KDA_DEVICE void ld_row(const float *p, float (&x)[SR])
-{
-    if constexpr (SR == 4) ld4(p, x);
-    else { const float2 t = *(const float2 *)p; x[0] = t.x; x[1] = t.y; }
-}
+// two neighbouring elements
+KDA_DEVICE float2 ld2(const float *p) { return *(const float2 *)p; }
+KDA_DEVICE float2 ld2(const __nv_bfloat16 *p) { return __bfloat1622float2(*(const __nv_bfloat162 *)p); }
+KDA_DEVICE void st2(float *p, float x, float y) { *(float2 *)p = make_float2(x, y); }
+KDA_DEVICE void st2(__nv_bfloat16 *p, float x, float y) { *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x, y); }
 
 // KEEP: leaves each chunk's start state and U in the workspace for the gradients, and writes no output
 template <typename IO, int DK, int DV, bool KEEP>
@@ -292,34 +295,53 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
     const GdrArgs &a = p.a;
     extern __shared__ float sm[];
     using T = Tiles<IO, DK>;
-    constexpr int LK = T::LK, SR = DK / 32;
-    float *S = sm + 2 * T::STAGE, *R = S + DK * LS, *Ub = R + CH * LS;
+    constexpr int LK = T::LK, L = LS<DK>;
+    constexpr int NSR = DK == 64 ? 1 : 2;            // state tiles (16 rows, 8 columns) of a warp
+    constexpr int NT1 = KEEP ? 1 : 2;                // token tiles: KEEP X's, a warp 16 tokens and 8 columns; else X's and Q S's, 16 columns
+    float *S = sm + 2 * T::STAGE, *R = S + DK * L, *Ub = R + CH * L;
     const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
-    const int rg = tid >> 2, cg = 4 * (tid & 3), r0 = rg * SR, col = col0 + cg;
+    const int w = tid >> 5, lane = tid & 31, g4 = lane >> 2, c2 = 2 * (lane & 3);
+    const int rs = DK == 64 ? 16 * (w >> 1) : 16 * w, ns = DK == 64 ? 8 * (w & 1) : 0;   // state tile
+    const int m = KEEP ? 16 * (w >> 1) : 16 * (w & 3), nt = KEEP ? 8 * (w & 1) : 0;       // token tile
+    const bool xrow = KEEP || w < 4;                 // of X and U; else of Q S and P U
+    const int arow = m + (xrow ? 0 : CH);            // its rows in [K; Q] and [M; P M]
     const int page0 = a.s0 ? page_of(a.s0_index, n, a.pages, a.err) : -1;
-    float s[SR][4];
+    float s[NSR][4];
+    auto each_state = [&](auto f) {                  // f(tile, element pair, row, column)
 #pragma unroll
-    for (int i = 0; i < SR; ++i) {
+        for (int i = 0; i < NSR; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-        if (page0 >= 0) ld4(a.s0 + (((size_t)page0 * a.Hv + hv) * DK + r0 + i) * DV + col, s[i]);
-        st4(S + (r0 + i) * LS + cg, s[i]);
-    }
+            for (int e = 0; e < 4; e += 2) f(i, e, rs + g4 + 4 * e, ns + 8 * i + c2);
+    };
+    auto each_token = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < NT1; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) f(i, e, m + g4 + 4 * e, nt + 8 * i + c2);
+    };
+    each_state([&](int i, int e, int row, int c) {
+        float2 x = make_float2(0.0f, 0.0f);
+        if (page0 >= 0) x = ld2(a.s0 + (((size_t)page0 * a.Hv + hv) * DK + row) * DV + col0 + c);
+        s[i][e] = x.x;
+        s[i][e + 1] = x.y;
+        st2(S + row * L + c, x.x, x.y);
+    });
     T tiles;
-    float v[2][4], vn[2][4];
+    float vn[NT1][4];
     const size_t item0 = (size_t)slot_base(span.row0, n);
     auto fetch = [&](int ch) {
         const size_t row0 = (size_t)span.row0 + ch * CH;
         const int valid = min(CH, span.len - ch * CH);
         tiles.fetch(sm + (ch & 1) * T::STAGE, a, p.w.I + ((item0 + ch) * a.Hv + hv) * ITEM, row0, hk, valid, tid);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) vn[i][j] = 0.0f;
-            if (rg + 32 * i < valid) ld4((const IO *)a.v + ((row0 + rg + 32 * i) * a.Hv + hv) * DV + col, vn[i]);
-        }
+        if (xrow)
+            each_token([&](int i, int e, int t, int c) {
+                float2 x = make_float2(0.0f, 0.0f);
+                if (t < valid) x = ld2((const IO *)a.v + ((row0 + t) * a.Hv + hv) * DV + col0 + c);
+                vn[i][e] = x.x;
+                vn[i][e + 1] = x.y;
+            });
     };
     if (nchunks > 0) {
         fetch(0);
@@ -331,75 +353,45 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
         const float *KQ = sm + (ch & 1) * T::STAGE, *MM = KQ + T::KQ, *g = MM + T::MM;
         cp_async_wait();
         __syncthreads();
+        float v[NT1][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NT1; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = vn[i][j];
+            for (int e = 0; e < 4; ++e) v[i][e] = vn[i][e];
         if (ch + 1 < nchunks) fetch(ch + 1);
         if (KEEP)
-#pragma unroll
-            for (int i = 0; i < SR; ++i) st4(p.w.S + (item * DK + r0 + i) * DV + col, s[i]);
-        float x[4][4] = {};                          // rows: X of the two tokens, Q S of the two tokens
-        if (KEEP) mm_rows<DK, 2>(*(float(*)[2][4])x, KQ + rg * LK, LK, 32, S + cg);
-        else mm_rows<DK, 4>(x, KQ + rg * LK, LK, 32, S + cg);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = rg + 32 * i;
+            each_state([&](int i, int e, int row, int c) { st2(p.w.S + (item * DK + row) * DV + col0 + c, s[i][e], s[i][e + 1]); });
+        float x[NT1][4] = {};                        // X, or gamma Q S
+        mm<NT1>(x, 0, DK, KQ + arow * LK, LK, 1, S + nt, L, 1, lane);
+        each_token([&](int i, int e, int t, int c) {
             const float gam = g[t], beta = g[2 * CH + t];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][j] = beta * (v[i][j] - gam * x[i][j]);
-                x[2 + i][j] *= gam;
+            if (xrow) {
+                st2(R + t * L + c, beta * (v[i][e] - gam * x[i][e]), beta * (v[i][e + 1] - gam * x[i][e + 1]));
+            } else {
+                x[i][e] *= gam;
+                x[i][e + 1] *= gam;
             }
-            st4(R + t * LS + cg, x[i]);
-        }
+        });
         __syncthreads();
-        float u[4][4] = {};                          // U of the two tokens, P U of the two tokens; M, P M are lower
-        if (KEEP) {
-            mm_rows<32, 2>(*(float(*)[2][4])u, MM + rg * LM, LM, 32, R + cg);
-            mm_rows<32, 1>(*(float(*)[1][4])u[1], MM + (rg + 32) * LM + 32, LM, 0, R + 32 * LS + cg);
-        } else {
-            mm_rows<32, 4>(u, MM + rg * LM, LM, 32, R + cg);
-            float w[2][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { w[0][j] = u[1][j]; w[1][j] = u[3][j]; }
-            mm_rows<32, 2>(w, MM + (rg + 32) * LM + 32, LM, 64, R + 32 * LS + cg);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { u[1][j] = w[0][j]; u[3][j] = w[1][j]; }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = rg + 32 * i;
-            if (KEEP) st4(p.w.U + (item * CH + t) * DV + col, u[i]);
-            const float lam = g[CH + t];
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = lam * u[i][j];
-            st4(Ub + t * LS + cg, y);
-            if (!KEEP && t < valid) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = x[2 + i][j] + u[2 + i][j];
-                st4((IO *)a.out + ((row0 + t) * a.Hv + hv) * DV + col, y);
+        float u[NT1][4] = {};                        // U, or P U; M and P M are lower
+        mm<NT1>(u, 0, m + 16, MM + arow * LM, LM, 1, R + nt, L, 1, lane);
+        each_token([&](int i, int e, int t, int c) {
+            if (xrow) {
+                const float lam = g[CH + t];
+                st2(Ub + t * L + c, lam * u[i][e], lam * u[i][e + 1]);
+                if (KEEP) st2(p.w.U + (item * CH + t) * DV + col0 + c, u[i][e], u[i][e + 1]);
+            } else if (t < valid) {
+                st2((IO *)a.out + ((row0 + t) * a.Hv + hv) * DV + col0 + c, x[i][e] + u[i][e], x[i][e + 1] + u[i][e + 1]);
             }
-        }
+        });
         __syncthreads();
         const float gc = g[CH - 1];
 #pragma unroll
-        for (int i = 0; i < SR; ++i)
+        for (int i = 0; i < NSR; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] *= gc;
-#pragma unroll 8
-        for (int t = 0; t < CH; ++t) {
-            float kr[SR], b[4];
-            ld_row<SR>(KQ + t * LK + r0, kr);
-            ld4(Ub + t * LS + cg, b);
-#pragma unroll
-            for (int i = 0; i < SR; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] += kr[i] * b[j];
-        }
-#pragma unroll
-        for (int i = 0; i < SR; ++i) st4(S + (r0 + i) * LS + cg, s[i]);
+            for (int e = 0; e < 4; ++e) s[i][e] *= gc;
+        mm<NSR>(s, 0, CH, KQ + rs, 1, LK, Ub + ns, L, 1, lane);
+        each_state([&](int i, int e, int row, int c) { st2(S + row * L + c, s[i][e], s[i][e + 1]); });
         if (ch + 1 < nchunks) tiles.put(sm + ((ch + 1) & 1) * T::STAGE, tid);
     }
     if (KEEP || !a.sT) return;
@@ -410,8 +402,9 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
         if (tid == 0) raise_error(a.err, ERR_PAGE_INDEX);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < SR; ++i) st4(a.sT + (((size_t)page * a.Hv + hv) * DK + r0 + i) * DV + col, s[i]);
+    each_state([&](int i, int e, int row, int c) {
+        st2(a.sT + (((size_t)page * a.Hv + hv) * DK + row) * DV + col0 + c, s[i][e], s[i][e + 1]);
+    });
 }
 
 template <typename IO, int DK, int DV>
@@ -420,34 +413,46 @@ __global__ void __launch_bounds__(WT) gdr_reverse_simt_kernel(P p)
     const GdrArgs &a = p.a;
     extern __shared__ float sm[];
     using T = Tiles<IO, DK>;
-    constexpr int LK = T::LK, SR = DK / 32;
-    float *S = sm + 2 * T::STAGE, *Yb = S + DK * LS, *dO = Yb + CH * LS, *W = dO + CH * LS;
+    constexpr int LK = T::LK, L = LS<DK>, NSR = DK == 64 ? 1 : 2;
+    float *S = sm + 2 * T::STAGE, *Yb = S + DK * L, *dO = Yb + CH * L, *W = dO + CH * L;
     const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
-    const int rg = tid >> 2, cg = 4 * (tid & 3), r0 = rg * SR, col = col0 + cg;
-    const size_t st = (((size_t)n * a.Hv + hv) * DK + r0) * DV + col;
-    float s[SR][4];
+    const int w = tid >> 5, lane = tid & 31, g4 = lane >> 2, c2 = 2 * (lane & 3);
+    const int rs = DK == 64 ? 16 * (w >> 1) : 16 * w, ns = DK == 64 ? 8 * (w & 1) : 0;   // state tile
+    const int m = 16 * (w >> 1), nt = 8 * (w & 1);                                        // token tile
+    const size_t st = ((size_t)n * a.Hv + hv) * DK * DV + col0;
+    float s[NSR][4];
+    auto each_state = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < SR; ++i) {
+        for (int i = 0; i < NSR; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-        if (a.dST) ld4(a.dST + st + (size_t)i * DV, s[i]);
-        st4(S + (r0 + i) * LS + cg, s[i]);
-    }
+            for (int e = 0; e < 4; e += 2) f(i, e, rs + g4 + 4 * e, ns + 8 * i + c2);
+    };
+    auto each_token = [&](auto f) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) f(e, m + g4 + 4 * e, nt + c2);
+    };
+    each_state([&](int i, int e, int row, int c) {
+        float2 x = make_float2(0.0f, 0.0f);
+        if (a.dST) x = ld2(a.dST + st + (size_t)row * DV + c);
+        s[i][e] = x.x;
+        s[i][e + 1] = x.y;
+        st2(S + row * L + c, x.x, x.y);
+    });
     T tiles;
-    float y[2][4];
+    float y[4];
     const size_t item0 = (size_t)slot_base(span.row0, n);
     auto fetch = [&](int ch) {
         const size_t row0 = (size_t)span.row0 + ch * CH;
         const int valid = min(CH, span.len - ch * CH);
         tiles.fetch(sm + (ch & 1) * T::STAGE, a, p.w.I + ((item0 + ch) * a.Hv + hv) * ITEM, row0, hk, valid, tid);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = 0.0f;
-            if (rg + 32 * i < valid) ld4((const IO *)a.dO + ((row0 + rg + 32 * i) * a.Hv + hv) * DV + col, y[i]);
-        }
+        each_token([&](int e, int t, int c) {
+            float2 x = make_float2(0.0f, 0.0f);
+            if (t < valid) x = ld2((const IO *)a.dO + ((row0 + t) * a.Hv + hv) * DV + col0 + c);
+            y[e] = x.x;
+            y[e + 1] = x.y;
+        });
     };
     if (nchunks > 0) {
         fetch(nchunks - 1);
@@ -459,74 +464,39 @@ __global__ void __launch_bounds__(WT) gdr_reverse_simt_kernel(P p)
         const float *KQ = sm + (ch & 1) * T::STAGE, *MM = KQ + T::KQ, *g = MM + T::MM;
         cp_async_wait();
         __syncthreads();
-        st4(dO + rg * LS + cg, y[0]);
-        st4(dO + (rg + 32) * LS + cg, y[1]);
+        each_token([&](int e, int t, int c) { st2(dO + t * L + c, y[e], y[e + 1]); });
         if (ch > 0) fetch(ch - 1);
-#pragma unroll
-        for (int i = 0; i < SR; ++i) st4(p.w.dS + (item * DK + r0 + i) * DV + col, s[i]);
-        float x[2][4] = {};
-        mm_rows<DK, 2>(x, KQ + rg * LK, LK, 32, S + cg);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float lam = g[CH + rg + 32 * i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] *= lam;
-            st4(Yb + (rg + 32 * i) * LS + cg, x[i]);
-        }
+        each_state([&](int i, int e, int row, int c) { st2(p.w.dS + (item * DK + row) * DV + col0 + c, s[i][e], s[i][e + 1]); });
+        float x[1][4] = {};
+        mm<1>(x, 0, DK, KQ + m * LK, LK, 1, S + nt, L, 1, lane);
+        each_token([&](int e, int t, int c) {
+            const float lam = g[CH + t];
+            st2(Yb + t * L + c, lam * x[0][e], lam * x[0][e + 1]);
+        });
         __syncthreads();
-        float h[2][4] = {};                          // H of tokens 2 rg, 2 rg + 1: rows from the warp's first token on
-#pragma unroll 4
-        for (int t = 16 * (tid >> 5); t < CH; ++t) {
-            const float2 m = *(const float2 *)(MM + t * LM + 2 * rg), pm = *(const float2 *)(MM + (CH + t) * LM + 2 * rg);
-            float b[4], c[4];
-            ld4(Yb + t * LS + cg, b);
-            ld4(dO + t * LS + cg, c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[0][j] += m.x * b[j] + pm.x * c[j];
-                h[1][j] += m.y * b[j] + pm.y * c[j];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * rg + i;
+        float h[1][4] = {};                          // H: rows of M and P M from the tile's first token on
+        mm<1>(h, m, CH, MM + m, 1, LM, Yb + nt, L, 1, lane);
+        mm<1>(h, m, CH, MM + CH * LM + m, 1, LM, dO + nt, L, 1, lane);
+        each_token([&](int e, int t, int c) {
             const float gam = g[t], beta = g[2 * CH + t];
-            st4(p.w.H + (item * CH + t) * DV + col, h[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[i][j] *= beta;
-            if (t < valid) st4((IO *)a.dv_ + ((row0 + t) * a.Hv + hv) * DV + col, h[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[i][j] *= -gam;
-            st4(W + t * LS + cg, h[i]);
-        }
+            st2(p.w.H + (item * CH + t) * DV + col0 + c, h[0][e], h[0][e + 1]);
+            const float d0 = beta * h[0][e], d1 = beta * h[0][e + 1];
+            if (t < valid) st2((IO *)a.dv_ + ((row0 + t) * a.Hv + hv) * DV + col0 + c, d0, d1);
+            st2(W + t * L + c, -gam * d0, -gam * d1);
+        });
         __syncthreads();
         const float gc = g[CH - 1];
 #pragma unroll
-        for (int i = 0; i < SR; ++i)
+        for (int i = 0; i < NSR; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] *= gc;
-#pragma unroll 4
-        for (int t = 0; t < CH; ++t) {
-            float kr[SR], qr[SR], b[4], c[4];
-            ld_row<SR>(KQ + t * LK + r0, kr);
-            ld_row<SR>(KQ + (CH + t) * LK + r0, qr);
-            ld4(W + t * LS + cg, b);
-            ld4(dO + t * LS + cg, c);
-            const float gam = g[t];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] *= gam;
-#pragma unroll
-            for (int i = 0; i < SR; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] += kr[i] * b[j] + qr[i] * c[j];
-        }
-#pragma unroll
-        for (int i = 0; i < SR; ++i) st4(S + (r0 + i) * LS + cg, s[i]);
+            for (int e = 0; e < 4; ++e) s[i][e] *= gc;
+        mm<NSR>(s, 0, CH, KQ + rs, 1, LK, W + ns, L, 1, lane);
+        mm<NSR, true>(s, 0, CH, KQ + CH * LK + rs, 1, LK, dO + ns, L, 1, lane, g);
+        each_state([&](int i, int e, int row, int c) { st2(S + row * L + c, s[i][e], s[i][e + 1]); });
         if (ch > 0) tiles.put(sm + ((ch - 1) & 1) * T::STAGE, tid);
     }
     if (!a.ds0) return;
-#pragma unroll
-    for (int i = 0; i < SR; ++i) st4(a.ds0 + st + (size_t)i * DV, s[i]);
+    each_state([&](int i, int e, int row, int c) { st2(a.ds0 + st + (size_t)row * DV + c, s[i][e], s[i][e + 1]); });
 }
 
 // ---------------------------------------------------------------- gradients of q, k, g, beta, a chunk and value head a block
@@ -547,197 +517,214 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
     SeqSpan span;
     if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
     extern __shared__ float sm[];
-    constexpr int LK = DK + 4, LV = DV + 4, NJ = DK / 16;
+    constexpr int LK = DK + 4, LV = DV + 4, NTL = DK / 16;   // column tiles of a warp: half the channels
+    constexpr bool STAGED = DK == 64 && DV == 64;            // S and dS fit in shared memory beside the rest
     float *K = sm, *Q = K + CH * LK, *dO = Q + CH * LK, *U = dO + CH * LV, *H = U + CH * LV;
+    float *S = H + CH * LV, *dS = S + DK * LV;               // (STAGED)
     float *DP = dO, *NM = U;                 // after their last use: dP.D and N, 64 x LM
     static_assert(LV >= LM, "the 64 x 64 tiles fit over dO and U");
     __shared__ Gates gs;
-    __shared__ float s_row[CH], s_col[4][CH], s_db[CH], s_red[NT / 32];
+    __shared__ float s_row[2][CH], s_kud[2][CH], s_db[2][CH], s_col[4][CH], s_red[NT / 32];
     const int tid = threadIdx.x, hv = blockIdx.y, rep = a.Hv / a.Hk, hk = hv / rep;
-    const int ty = tid >> 4, tx = tid & 15;
+    // the warp: tokens 16 m .., channels (or columns) of half h
+    const int w = tid >> 5, lane = tid & 31, m = 16 * (w >> 1), h = w & 1, g4 = lane >> 2, c2 = 2 * (lane & 3);
     const size_t row0 = (size_t)span.row0 + c * CH;
     const int valid = min(CH, span.len - c * CH);
+    const size_t item = (size_t)blockIdx.x * a.Hv + hv;
     load_rows<IO, DK, LK>(K, (const IO *)a.k, row0, a.Hk, hk, valid, tid);
     load_rows<IO, DK, LK>(Q, (const IO *)a.q, row0, a.Hk, hk, valid, tid);
-    float dq[4][NJ] = {}, dk[4][NJ] = {};    // rows 4 ty + i, columns tx + 16 j
-    auto sum16 = [](float v) {               // over the 16 threads of a row
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    };
-    const size_t item = (size_t)blockIdx.x * a.Hv + hv;
-    {
-        const float *S = p.w.S + item * DK * DV, *dS = p.w.dS + item * DK * DV;
-        load_rows<IO, DV, LV>(dO, (const IO *)a.dO, row0, a.Hv, hv, valid, tid);
-        load_item<DV>(U, LV, p.w.U + item * CH * DV, tid);
-        load_item<DV>(H, LV, p.w.H + item * CH * DV, tid);
-        load_gates<IO>(gs, (const IO *)a.g, (const IO *)a.beta, row0, a.Hv, hv, valid, tid);
-        // <dS, S> of the start state
+    load_rows<IO, DV, LV>(dO, (const IO *)a.dO, row0, a.Hv, hv, valid, tid);
+    load_item<DV>(U, LV, p.w.U + item * CH * DV, tid);
+    load_item<DV>(H, LV, p.w.H + item * CH * DV, tid);
+    load_gates<IO>(gs, (const IO *)a.g, (const IO *)a.beta, row0, a.Hv, hv, valid, tid);
+    const float *Sg = p.w.S + item * DK * DV, *dSg = p.w.dS + item * DK * DV;
+    int ls = DV;
+    {   // <dS, S>
         float ss = 0.0f;
         for (int u = tid; u < DK * DV / 4; u += NT) {
-            const float4 x = *(const float4 *)(S + 4 * u), y = *(const float4 *)(dS + 4 * u);
+            const float4 x = *(const float4 *)(Sg + 4 * u), y = *(const float4 *)(dSg + 4 * u);
             ss += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            if (STAGED) {
+                *(float4 *)(S + (u / (DV / 4)) * LV + 4 * (u % (DV / 4))) = x;
+                *(float4 *)(dS + (u / (DV / 4)) * LV + 4 * (u % (DV / 4))) = y;
+            }
         }
         ss = warp_sum(ss);
-        if ((tid & 31) == 0) s_red[tid >> 5] = ss;
-        __syncthreads();
-        float row[4], kud[4], db[4];         // per row: the part of dG, k.(lam U dS^T), dbeta
-        {
-            float x[4][NJ] = {};
-            mm_nt<DV>(x, dO + 4 * ty * LV, LV, S + (size_t)tx * DV, DV);
+        if (lane == 0) s_red[w] = ss;
+    }
+    if (STAGED) {
+        Sg = S;
+        dSg = dS;
+        ls = LV;
+    }
+    __syncthreads();
+    // sums over a row: of the four lanes that share it (its other half is another warp's)
+    auto row_sum = [](float v) {
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        return v + __shfl_xor_sync(0xffffffffu, v, 2);
+    };
+    const int t2[2] = {m + g4, m + g4 + 8};
+    const float gm[2] = {gs.gam[t2[0]], gs.gam[t2[1]]}, bt[2] = {gs.beta[t2[0]], gs.beta[t2[1]]};
+    float dq[NTL][4], dk[NTL][4], row[2] = {}, kud[2] = {}, db[2] = {};
+    const int c0 = h * (DK / 2) + c2;        // the lane's channels: c0 + 8 i and the next
+    auto dot_row = [&](const float(&x)[NTL][4], const float *R, float (&d)[2]) {
+        d[0] = d[1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float gm = gs.gam[4 * ty + i];
-                float s = 0.0f;
+        for (int i = 0; i < NTL; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    x[i][j] *= gm;
-                    dq[i][j] += x[i][j];
-                    s += x[i][j] * Q[(4 * ty + i) * LK + tx + 16 * j];
-                }
-                row[i] = sum16(s);
+            for (int e = 0; e < 2; ++e) {
+                const float2 r = *(const float2 *)(R + t2[e] * LK + c0 + 8 * i);
+                d[e] += x[i][2 * e] * r.x + x[i][2 * e + 1] * r.y;
             }
-        }
-        {
-            float x[4][NJ] = {};
-            mm_nt<DV>(x, H + 4 * ty * LV, LV, S + (size_t)tx * DV, DV);
+    };
+    {   // gamma (dO S^T)
+        float d[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * ty + i;
-                const float gm = gs.gam[t], bt = gs.beta[t];
-                float s = 0.0f, hvv = 0.0f;
+        for (int i = 0; i < NTL; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    x[i][j] *= gm;
-                    dk[i][j] -= bt * x[i][j];
-                    s += x[i][j] * K[t * LK + tx + 16 * j];
+            for (int e = 0; e < 4; ++e) dq[i][e] = 0.0f;
+        mm<NTL>(dq, 0, DV, dO + m * LV, LV, 1, Sg + h * (DK / 2) * ls, 1, ls, lane);
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dq[i][e] *= gm[e >> 1];
+        dot_row(dq, Q, d);
+        row[0] += d[0];
+        row[1] += d[1];
+    }
+    {   // - beta gamma (H S^T)
+        float d[2];
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dk[i][e] = 0.0f;
+        mm<NTL>(dk, 0, DV, H + m * LV, LV, 1, Sg + h * (DK / 2) * ls, 1, ls, lane);
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dk[i][e] *= gm[e >> 1];
+        dot_row(dk, K, d);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            row[e] -= bt[e] * d[e];
+            db[e] -= d[e];
+            if (t2[e] < valid)               // H.V, a quarter of a half row a lane
+                for (int x = h * (DV / 2) + 4 * (lane & 3); x < (h + 1) * (DV / 2); x += 16) {
+                    float v[4], y[4];
+                    ld4((const IO *)a.v + ((row0 + t2[e]) * a.Hv + hv) * DV + x, v);
+                    ld4(H + t2[e] * LV + x, y);
+                    db[e] += (v[0] * y[0] + v[1] * y[1]) + (v[2] * y[2] + v[3] * y[3]);
                 }
-                if (t < valid)
-                    for (int e = tx; e < DV; e += 16)
-                        hvv += H[t * LV + e] * ld_f32((const IO *)a.v + ((row0 + t) * a.Hv + hv) * DV + e);
-                s = sum16(s);
-                row[i] -= bt * s;
-                db[i] = sum16(hvv) - s;
-            }
         }
-        {
-            float x[4][NJ] = {};
-            mm_nt<DV>(x, U + 4 * ty * LV, LV, dS + (size_t)tx * DV, DV);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float lm = gs.lam[4 * ty + i];
-                float s = 0.0f;
+        for (int i = 0; i < NTL; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    x[i][j] *= lm;
-                    dk[i][j] += x[i][j];
-                    s += x[i][j] * K[(4 * ty + i) * LK + tx + 16 * j];
-                }
-                kud[i] = sum16(s);
+            for (int e = 0; e < 4; ++e) dk[i][e] *= -bt[e >> 1];
+    }
+    {   // lam (U dS^T)
+        float x[NTL][4] = {};
+        mm<NTL>(x, 0, DV, U + m * LV, LV, 1, dSg + h * (DK / 2) * ls, 1, ls, lane);
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[i][e] *= gs.lam[t2[e >> 1]];
+                dk[i][e] += x[i][e];
             }
+        dot_row(x, K, kud);
+    }
+    // the pairwise products: rows 16 m .., columns s = 32 h .., zero above the diagonal
+    float dp[4][4] = {}, nm[4][4] = {};
+    {
+        float qk[4][4] = {}, kk[4][4] = {};
+        if (32 * h <= m) {
+            mm<4>(dp, 0, DV, dO + m * LV, LV, 1, U + 32 * h * LV, 1, LV, lane);
+            mm<4>(nm, 0, DV, H + m * LV, LV, 1, U + 32 * h * LV, 1, LV, lane);
+            mm<4>(qk, 0, DK, Q + m * LK, LK, 1, K + 32 * h * LK, 1, LK, lane);
+            mm<4>(kk, 0, DK, K + m * LK, LK, 1, K + 32 * h * LK, 1, LK, lane);
         }
-        // 64 x 64 products: rows 4 ty + i, columns tx + 16 j
-        float dp[4][4] = {}, hu[4][4] = {}, qk[4][4] = {}, kk[4][4] = {};
-        mm_nt<DV>(dp, dO + 4 * ty * LV, LV, U + tx * LV, LV);
-        mm_nt<DV>(hu, H + 4 * ty * LV, LV, U + tx * LV, LV);
-        mm_nt<DK>(qk, Q + 4 * ty * LK, LK, K + tx * LK, LK);
-        mm_nt<DK>(kk, K + 4 * ty * LK, LK, K + tx * LK, LK);
-        __syncthreads();                     // dO and U are consumed
-        float ecol[4] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 4 * ty + i;
-            float er = 0.0f, dbs = 0.0f;
+            float col[2] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int s = tx + 16 * j;
+            for (int e = 0; e < 4; ++e) {
+                const int t = t2[e >> 1], s = 32 * h + 8 * i + c2 + (e & 1);
                 const float d = s <= t ? decay(gs, t, s) : 0.0f;
-                const float dpd = s <= t ? dp[i][j] * d : 0.0f;
-                const float hud = s < t ? hu[i][j] * d : 0.0f;
-                const float nm = -gs.beta[t] * hud;
-                DP[t * LM + s] = dpd;
-                NM[t * LM + s] = nm;
-                const float e = s < t ? dpd * qk[i][j] + nm * kk[i][j] : 0.0f;   // s == t cancels in rowsum - colsum
-                er += e;
-                ecol[j] += e;
-                dbs += hud * kk[i][j];
-            }
-            row[i] += sum16(er);
-            db[i] -= sum16(dbs);
-        }
-        // column sums over the 16 row groups: two per warp, eight warps
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ecol[j] += __shfl_xor_sync(0xffffffffu, ecol[j], 16);
-        if (tx == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s_row[4 * ty + i] = row[i];
-                s_db[4 * ty + i] = db[i];
-                s_col[0][4 * ty + i] = kud[i];
-            }
-        }
-        __syncthreads();
-        float *cs = H;                       // H's last use was hu; 8 rows of partial column sums
-        if ((tid & 16) == 0)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cs[(tid >> 5) * CH + tx + 16 * j] = ecol[j];
-        __syncthreads();
-        if (tid < CH) {
-            float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < NT / 32; ++w) s += cs[w * CH + tid];
-            s_col[1][tid] = s_row[tid] - s;
-        }
-        __syncthreads();
-        if (tid < 32) {
-            float base = 0.0f;
-            for (int w = 0; w < NT / 32; ++w) base += s_red[w];
-            base *= gs.gam[CH - 1];
-            float lo, hi, wl, wh;
-            sums_across(s_col[1][tid], s_col[1][tid + 32], s_col[0][tid], s_col[0][tid + 32], lo, hi, wl, wh, tid);
-            if (tid < valid) ((IO *)a.dg)[(row0 + tid) * a.Hv + hv] = from_f32<IO>(base + wl + lo);
-            if (tid + 32 < valid) ((IO *)a.dg)[(row0 + tid + 32) * a.Hv + hv] = from_f32<IO>(base + wh + hi);
-        } else if (tid >= 64 && tid - 64 < valid) {
-            if (tid < 128) ((IO *)a.dbeta)[(row0 + tid - 64) * a.Hv + hv] = from_f32<IO>(s_db[tid - 64]);
-        }
-        // dQ += dPD K;  dK += N K + dPD^T Q + N^T K
-        for (int s = 0; s < CH; ++s) {
-            float kv[NJ], qv[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                kv[j] = K[s * LK + tx + 16 * j];
-                qv[j] = Q[s * LK + tx + 16 * j];
+                const float dpd = s <= t ? dp[i][e] * d : 0.0f, hud = s < t ? nm[i][e] * d : 0.0f;
+                dp[i][e] = dpd;
+                nm[i][e] = -bt[e >> 1] * hud;
+                const float x = s < t ? dpd * qk[i][e] + nm[i][e] * kk[i][e] : 0.0f;   // s == t cancels in rowsum - colsum
+                row[e >> 1] += x;
+                col[e & 1] += x;
+                db[e >> 1] -= hud * kk[i][e];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * ty + i;
-                const float x = DP[t * LM + s], y = NM[t * LM + s] + NM[s * LM + t], z = DP[s * LM + t];
+            for (int e = 0; e < 2; ++e) {    // over the warp's 16 rows
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    dq[i][j] += x * kv[j];
-                    dk[i][j] += y * kv[j] + z * qv[j];
-                }
+                for (int o = 4; o < 32; o <<= 1) col[e] += __shfl_xor_sync(0xffffffffu, col[e], o);
+                if (g4 == 0) s_col[w >> 1][32 * h + 8 * i + c2 + e] = col[e];
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ty + i;
+    for (int e = 0; e < 2; ++e) {
+        const float x = row_sum(row[e]), y = row_sum(kud[e]), z = row_sum(db[e]);
+        if ((lane & 3) == 0) {
+            s_row[h][t2[e]] = x;
+            s_kud[h][t2[e]] = y;
+            s_db[h][t2[e]] = z;
+        }
+    }
+    __syncthreads();                         // dO, U are consumed
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            st2(DP + t2[e] * LM + 32 * h + 8 * i + c2, dp[i][2 * e], dp[i][2 * e + 1]);
+            st2(NM + t2[e] * LM + 32 * h + 8 * i + c2, nm[i][2 * e], nm[i][2 * e + 1]);
+        }
+    if (w == 0) {
+        const float base = gs.gam[CH - 1] * warp_sum(lane < NT / 32 ? s_red[lane] : 0.0f);
+        float x[2], y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = lane + 32 * i;
+            x[i] = (s_row[0][t] + s_row[1][t]) - ((s_col[0][t] + s_col[1][t]) + (s_col[2][t] + s_col[3][t]));
+            y[i] = s_kud[0][t] + s_kud[1][t];
+        }
+        float lo, hi, wl, wh;
+        sums_across(x[0], x[1], y[0], y[1], lo, hi, wl, wh, lane);
+        if (lane < valid) ((IO *)a.dg)[(row0 + lane) * a.Hv + hv] = from_f32<IO>(base + wl + lo);
+        if (lane + 32 < valid) ((IO *)a.dg)[(row0 + lane + 32) * a.Hv + hv] = from_f32<IO>(base + wh + hi);
+    } else if (w < 3) {
+        const int t = 32 * (w - 1) + lane;
+        if (t < valid) ((IO *)a.dbeta)[(row0 + t) * a.Hv + hv] = from_f32<IO>(s_db[0][t] + s_db[1][t]);
+    }
+    __syncthreads();
+    // dQ += (dP.D) K;  dK += N K + N^T K + (dP.D)^T Q
+    const float *Kh = K + h * (DK / 2), *Qh = Q + h * (DK / 2);
+    mm<NTL>(dq, 0, m + 16, DP + m * LM, LM, 1, Kh, LK, 1, lane);
+    mm<NTL>(dk, 0, m + 16, NM + m * LM, LM, 1, Kh, LK, 1, lane);
+    mm<NTL>(dk, m, CH, NM + m, 1, LM, Kh, LK, 1, lane);
+    mm<NTL>(dk, m, CH, DP + m, 1, LM, Qh, LK, 1, lane);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int t = t2[e];
         if (t >= valid) continue;
         if (rep > 1) {                       // a part of the group's sum
-            const size_t o = (item * CH + t) * DK;
+            const size_t o = (item * CH + t) * DK + c0;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                p.w.dq[o + tx + 16 * j] = dq[i][j];
-                p.w.dk[o + tx + 16 * j] = dk[i][j];
+            for (int i = 0; i < NTL; ++i) {
+                st2(p.w.dq + o + 8 * i, dq[i][2 * e], dq[i][2 * e + 1]);
+                st2(p.w.dk + o + 8 * i, dk[i][2 * e], dk[i][2 * e + 1]);
             }
-            continue;
-        }
-        const size_t o = ((row0 + t) * a.Hk + hk) * DK;
+        } else {
+            const size_t o = ((row0 + t) * a.Hk + hk) * DK + c0;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            ((IO *)a.dq)[o + tx + 16 * j] = from_f32<IO>(dq[i][j]);
-            ((IO *)a.dk_)[o + tx + 16 * j] = from_f32<IO>(dk[i][j]);
+            for (int i = 0; i < NTL; ++i) {
+                st2((IO *)a.dq + o + 8 * i, dq[i][2 * e], dq[i][2 * e + 1]);
+                st2((IO *)a.dk_ + o + 8 * i, dk[i][2 * e], dk[i][2 * e + 1]);
+            }
         }
     }
 }
@@ -774,9 +761,9 @@ __global__ void __launch_bounds__(NT) gdr_group_sum_kernel(P p)
 template <int DK>
 constexpr int prep_bytes() { return (2 * CH * (DK + 4) + 2 * CH * LM) * 4; }
 template <int DK>
-constexpr int walk_bytes(int buffers) { return (2 * (2 * CH * (DK + 4) + 2 * CH * LM + 256) + DK * LS + buffers * CH * LS) * 4; }
+constexpr int walk_bytes(int buffers) { return (2 * (2 * CH * (DK + 4) + 2 * CH * LM + 256) + (DK + buffers * CH) * LS<DK>) * 4; }
 template <int DK, int DV>
-constexpr int grads_bytes() { return (2 * CH * (DK + 4) + 3 * CH * (DV + 4)) * 4; }
+constexpr int grads_bytes() { return (2 * CH * (DK + 4) + 3 * CH * (DV + 4) + (DK == 64 && DV == 64 ? 2 * DK * (DV + 4) : 0)) * 4; }
 static_assert(walk_bytes<128>(3) <= 227 * 1024 && grads_bytes<128, 128>() <= 227 * 1024, "shared memory per block");
 
 template <typename IO, int DK, int DV>
