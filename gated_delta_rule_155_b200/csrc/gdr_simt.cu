@@ -130,7 +130,10 @@ KDA_DEVICE void mm(float (&acc)[NTL][4], int k0, int k1, const float *A, int ar,
                    const float *scale = nullptr)
 {
     const float *a = A + (lane >> 2) * ar + (lane & 3) * ak, *b = B + (lane & 3) * bk + (lane >> 2) * bn;
-    constexpr int AHEAD = NTL >= 4 ? 1 : 2;  // (a wide step is enough independent work, and code is what the caches lack)
+    // a narrow product has little independent work: the small products run on along k in accumulators of their own
+    constexpr bool NARROW = NTL < 4;
+    constexpr int AHEAD = NARROW ? 4 : 1;
+    float s1[NARROW ? NTL : 1][4] = {}, s2[NARROW ? NTL : 1][4] = {};
 #pragma unroll AHEAD
     for (int k = k0; k < k1; k += 8) {
         uint32_t ah[4], al[4];
@@ -138,24 +141,34 @@ KDA_DEVICE void mm(float (&acc)[NTL][4], int k0, int k1, const float *A, int ar,
         split_tf32(a[8 * ar + k * ak], ah[1], al[1]);
         split_tf32(a[(k + 4) * ak], ah[2], al[2]);
         split_tf32(a[8 * ar + (k + 4) * ak], ah[3], al[3]);
-        float s0 = 1.0f, s1 = 1.0f;
+        float f0 = 1.0f, f1 = 1.0f;
         if (SCALED) {
-            s0 = scale[k + (lane & 3)];
-            s1 = scale[k + 4 + (lane & 3)];
+            f0 = scale[k + (lane & 3)];
+            f1 = scale[k + 4 + (lane & 3)];
         }
 #pragma unroll
         for (int i = 0; i < NTL; ++i) {
             uint32_t bh[2], bl[2];
-            split_tf32(SCALED ? s0 * b[k * bk + 8 * i * bn] : b[k * bk + 8 * i * bn], bh[0], bl[0]);
-            split_tf32(SCALED ? s1 * b[(k + 4) * bk + 8 * i * bn] : b[(k + 4) * bk + 8 * i * bn], bh[1], bl[1]);
+            split_tf32(SCALED ? f0 * b[k * bk + 8 * i * bn] : b[k * bk + 8 * i * bn], bh[0], bl[0]);
+            split_tf32(SCALED ? f1 * b[(k + 4) * bk + 8 * i * bn] : b[(k + 4) * bk + 8 * i * bn], bh[1], bl[1]);
             float c[4] = {};
-            mma_tf32(c, al, bh);
-            mma_tf32(c, ah, bl);
+            if constexpr (NARROW) {
+                mma_tf32(s1[i], al, bh);
+                mma_tf32(s2[i], ah, bl);
+            } else {
+                mma_tf32(c, al, bh);
+                mma_tf32(c, ah, bl);
+            }
             mma_tf32(c, ah, bh);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][e] += c[e];
         }
     }
+    if constexpr (NARROW)
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] += s1[i][e] + s2[i][e];
 }
 
 // ---------------------------------------------------------------- prep: M and P M of every chunk
@@ -245,10 +258,16 @@ struct Tiles {
     KDA_DEVICE void fetch(float *b, const GdrArgs &a, const float *item, size_t row0, int hk, int valid, int tid)
     {
         if (DIRECT) {
-            for (int u = tid; u < 2 * CH * (DK / 4); u += WT) {
-                const int r = u / (DK / 4), c = 4 * (u % (DK / 4)), t = r & (CH - 1);
-                const float *src = (const float *)(r < CH ? a.k : a.q) + ((row0 + min(t, valid - 1)) * a.Hk + hk) * DK + c;
-                cp_async16(b + r * LK + c, src, t < valid);
+            constexpr int STEP = WT / (DK / 4);      // rows between a thread's pieces
+            const int t0 = tid / (DK / 4), c = 4 * (tid % (DK / 4));
+            const size_t at = ((row0 + t0) * a.Hk + hk) * DK + c, step = (size_t)STEP * a.Hk * DK;
+            const float *k = (const float *)a.k + at, *q = (const float *)a.q + at;
+            float *d = b + t0 * LK + c;
+#pragma unroll
+            for (int i = 0; i < CH / STEP; ++i) {
+                const bool in = t0 + i * STEP < valid;   // behind the end: 16 zero bytes, and an address that exists
+                cp_async16(d + i * STEP * LK, in ? k + i * step : (const float *)a.k, in);
+                cp_async16(d + (CH + i * STEP) * LK, in ? q + i * step : (const float *)a.q, in);
             }
         } else {
 #pragma unroll
@@ -258,8 +277,12 @@ struct Tiles {
                                     : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        for (int u = tid; u < 2 * CH * (CH / 4); u += WT)
-            cp_async16(b + KQ + (u / (CH / 4)) * LM + 4 * (u % (CH / 4)), item + 4 * u, true);
+        {
+            const float *src = item + 4 * tid;
+            float *d = b + KQ + (tid / (CH / 4)) * LM + 4 * (tid % (CH / 4));
+#pragma unroll
+            for (int i = 0; i < 2 * CH * (CH / 4) / WT; ++i) cp_async16(d + i * (WT / (CH / 4)) * LM, src + i * 4 * WT, true);
+        }
         if (tid < 48) cp_async16(b + KQ + MM + 4 * tid, item + 2 * CH * CH + 4 * tid, true);
         cp_async_commit();
     }
