@@ -109,17 +109,16 @@ KDA_DEVICE bool page_is_free(const int *sT_index, const int *s0_index, bool same
     return !__syncthreads_or(clash);
 }
 
-// c += A B for an A of 16 x 8 K floats (rows of lda) and a B of 8 K x 8 (rows of ldb), one warp: tf32 products
+// c += A B, k in [k0, k1), for an A of 16 rows (of lda floats) and a B of 8 columns (rows of ldb), one warp: tf32 products
 // of hi and lo parts (hi: the upper 11 bits, exact; lo x lo left out), so good to about 2^-21 of the terms.
 // Lane l has rows l / 4 and l / 4 + 8 of columns 2 (l % 4) and the next.  A 16-byte load from shared memory
 // costs four cycles however many lanes share its address, so products of 16 x 16 blocks on CUDA cores (20
 // loads for 64 FMAs) spent four times the cycles that these fragments do.
-template <int K>
-KDA_DEVICE void mma_block(float (&c)[4], const float *A, int lda, const float *B, int ldb, int lane)
+KDA_DEVICE void mma_block(float (&c)[4], int k0, int k1, const float *A, int lda, const float *B, int ldb, int lane)
 {
     const float *a = A + (lane >> 2) * lda + (lane & 3), *b = B + (lane & 3) * ldb + (lane >> 2);
-#pragma unroll
-    for (int k = 0; k < 8 * K; k += 8) {
+#pragma unroll 2
+    for (int k = k0; k < k1; k += 8) {
         const float x[4] = {a[k], a[8 * lda + k], a[k + 4], a[8 * lda + k + 4]}, y[2] = {b[k * ldb], b[(k + 4) * ldb]};
         uint32_t xh[4], xl[4], yh[2], yl[2];
 #pragma unroll
@@ -189,13 +188,13 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
         const int o = 32 * (w >> 1), n = 8 * (w & 1);
         if (w < 4) {
             float c[4] = {};
-            mma_block<2>(c, A + (o + 16) * LD + o, LD, M + o * LD + o + n, LD, lane);
+            mma_block(c, n, 16, A + (o + 16) * LD + o, LD, M + o * LD + o + n, LD, lane);
             put_block(tmp + (o >> 1) * LD + n, LD, c, 1.0f, lane);
         }
         __syncthreads();
         if (w < 4) {
             float c[4] = {};
-            mma_block<2>(c, M + (o + 16) * LD + o + 16, LD, tmp + (o >> 1) * LD + n, LD, lane);
+            mma_block(c, 0, 16, M + (o + 16) * LD + o + 16, LD, tmp + (o >> 1) * LD + n, LD, lane);
             put_block(M + (o + 16) * LD + o + n, LD, c, -1.0f, lane);
         }
     }
@@ -203,11 +202,11 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
     {   // 32 -> 64: sixteen rows and eight columns a warp
         const int m = 16 * (w >> 2), n = 8 * (w & 3);
         float c[4] = {};
-        mma_block<4>(c, A + (32 + m) * LD, LD, M + n, LD, lane);
+        mma_block(c, n, 32, A + (32 + m) * LD, LD, M + n, LD, lane);           // M is lower
         put_block(tmp + m * LD + n, LD, c, 1.0f, lane);
         __syncthreads();
         float x[4] = {};
-        mma_block<4>(x, M + (32 + m) * LD + 32, LD, tmp + n, LD, lane);
+        mma_block(x, 0, m + 16, M + (32 + m) * LD + 32, LD, tmp + n, LD, lane);
         put_block(M + (32 + m) * LD + n, LD, x, -1.0f, lane);
     }
     __syncthreads();
