@@ -104,6 +104,10 @@ def library():
     return _lib
 
 
+_Tensor, _empty = torch.Tensor, torch.empty
+_cuda_getDevice, _cuda_getCurrentRawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 # The marshalling runs before every launch, and a decode kernel takes 4 us: raw pointers as ints (what the
 # argument types convert), the device and stream of torch's C side, and one look at a well-formed tensor.
 def _ptr(t):
@@ -114,7 +118,7 @@ def _stream(stream):
     if stream is None:
         if not torch.cuda.is_initialized():
             torch.cuda.init()
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _cuda_getCurrentRawStream(_cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -155,12 +159,11 @@ def _need(t, shape, dtype, name, *, allow_none=False):
 
 def _need_all(checks):
     """_need for each (tensor, shape, dtype, name), with one look at those that are well-formed."""
-    cur = torch._C._cuda_getDevice()
-    for c in checks:
-        t = c[0]
-        if not (isinstance(t, torch.Tensor) and t.get_device() == cur and t.shape == c[1] and t.dtype is c[2]
-                and t.is_contiguous()):
-            _need(*c)
+    cur = _cuda_getDevice()
+    for t, shape, dtype, name in checks:
+        if not (t.__class__ is _Tensor and t.shape == shape and t.dtype is dtype and t.is_contiguous()
+                and t.get_device() == cur):
+            _need(t, shape, dtype, name)
 
 
 def kda_forward_chunked(q, k, v, g, beta, initial_state=None, out=None, final_state=None,
@@ -426,30 +429,29 @@ def kda_layer_forward_noalloc(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, g_raw
 def _gdr_shapes(q, k, v, g, beta, cu_seqlens):
     """(N, T_total, Hk, Hv, dk, dv, leading shape) of the head-gated delta rule's inputs: packed
     [T_total, ...] with cu_seqlens, [B, T, ...] without."""
-    if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
-        N = cu_seqlens.shape[0] - 1
-        _need_all(((cu_seqlens, (N + 1,), torch.int32, "cu_seqlens"),))
-        if q.dim() != 3 or v.dim() != 3:
-            raise ValueError("with cu_seqlens, q and v are [T_total, H, d]")
-        lead = (q.shape[0],)
-        Tt = q.shape[0]
-    else:
-        if q.dim() != 4 or v.dim() != 4:
-            raise ValueError("without cu_seqlens, q and v are [B, T, H, d]")
-        lead = (q.shape[0], q.shape[1])
-        N, Tt = q.shape[0], q.shape[0] * q.shape[1]
     sq, sv, io = q.shape, v.shape, q.dtype
-    (Hk, dk), (Hv, dv) = sq[-2:], sv[-2:]
-    gates = lead + (Hv,)
-    _need_all(((q, lead + (Hk, dk), io, "q"), (k, sq, io, "k"), (v, gates + (dv,), io, "v"), (g, gates, io, "g"),
-               (beta, gates, io, "beta")))
+    if cu_seqlens is not None:
+        sc = cu_seqlens.shape
+        if len(sc) != 1 or sc[0] < 2:
+            raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
+        if len(sq) != 3 or len(sv) != 3:
+            raise ValueError("with cu_seqlens, q and v are [T_total, H, d]")
+        Tt, Hk, dk = sq
+        N, lead = sc[0] - 1, (Tt,)
+        _need_all(((cu_seqlens, sc, torch.int32, "cu_seqlens"),))
+    else:
+        if len(sq) != 4 or len(sv) != 4:
+            raise ValueError("without cu_seqlens, q and v are [B, T, H, d]")
+        N, T, Hk, dk = sq
+        Tt, lead = N * T, (N, T)
+    Hv, dv = sv[-2:]
+    gates = (*lead, Hv)
+    _need_all(((q, sq, io, "q"), (k, sq, io, "k"), (v, (*gates, dv), io, "v"), (g, gates, io, "g"), (beta, gates, io, "beta")))
     return N, Tt, Hk, Hv, dk, dv, lead
 
 
 def _workspace(need, device):
-    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    return _empty(need, dtype=torch.uint8, device=device) if need > 0 else None
 
 
 def _ws_bytes(workspace):
@@ -492,9 +494,9 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
     if p0 and p1 and p0 != p1:
         raise ValueError(f"initial_state has {p0} pages, final_state {p1}")
     if out is None:
-        out = torch.empty(lead + (Hv, dv), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(v)
     else:
-        _need_all(((out, lead + (Hv, dv), q.dtype, "out"),))
+        _need_all(((out, v.shape, q.dtype, "out"),))
     if workspace is None:
         workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype), q.device)
     _check(_lib.kda_gdr_forward(
@@ -535,25 +537,32 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
     """One or a few tokens per sequence, states updated in place.  q, k: [N, T, Hk, dk]; v: [N, T, Hv, dv];
     g, beta: [N, T, Hv], or all without T for one token; state: fp32 [N, Hv, dk, dv], or pages
     [P, Hv, dk, dv] with ``index`` int32 [N] (-1: an idle row, whose out is left alone).  Returns out."""
-    one = q.dim() == 3
-    if q.dim() not in (3, 4) or v.dim() != q.dim():
-        raise ValueError("q and v are [N, T, H, d], or [N, H, d] for one token")
     sq, sv, io = q.shape, v.shape, q.dtype
-    lead = sq[:-2]
-    N, T = (lead[0], 1) if one else lead
-    (Hk, dk), (Hv, dv) = sq[-2:], sv[-2:]
-    gates = lead + (Hv,)
-    shape = gates + (dv,)
+    if len(sq) == 4 and len(sv) == 4:
+        N, T, Hk, dk = sq
+        lead = (N, T)
+    elif len(sq) == 3 and len(sv) == 3:
+        N, Hk, dk = sq
+        lead, T = (N,), 1
+    else:
+        raise ValueError("q and v are [N, T, H, d], or [N, H, d] for one token")
+    Hv, dv = sv[-2:]
+    gates = (*lead, Hv)
+    shape = (*gates, dv)
     if out is None:
-        out = torch.empty(shape, dtype=io, device=q.device)
-    P = N if index is None else state.shape[0]
-    _need_all(((q, lead + (Hk, dk), io, "q"), (k, sq, io, "k"), (v, shape, io, "v"), (g, gates, io, "g"),
-               (beta, gates, io, "beta"), (state, (P, Hv, dk, dv), torch.float32, "state"), (out, shape, io, "out")))
-    if index is not None:
+        out = _empty(shape, dtype=io, device=q.device)
+    if index is None:
+        P, idx = N, None
+    else:
+        P = state.shape[0]
         _need_all(((index, (N,), torch.int32, "index"),))
-    _check(_lib.kda_gdr_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(index),
-                               P, _ptr(out), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream)),
-           "kda_gdr_decode")
+        idx = index.data_ptr()
+    _need_all(((q, sq, io, "q"), (k, sq, io, "k"), (v, shape, io, "v"), (g, gates, io, "g"), (beta, gates, io, "beta"),
+               (state, (P, Hv, dk, dv), torch.float32, "state"), (out, shape, io, "out")))
+    st = _lib.kda_gdr_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+                             idx, P, out.data_ptr(), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream))
+    if st:
+        raise KdaError(st, "kda_gdr_decode")
     return out
 
 
