@@ -313,7 +313,7 @@ KDA_DEVICE void st2(__nv_bfloat16 *p, float x, float y) { *(__nv_bfloat162 *)p =
 
 // KEEP: leaves each chunk's start state and U in the workspace for the gradients, and writes no output
 template <typename IO, int DK, int DV, bool KEEP>
-__global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
+KDA_DEVICE void walk_forward(const P &p, unsigned block)
 {
     const GdrArgs &a = p.a;
     extern __shared__ float sm[];
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
     constexpr int NSR = DK == 64 ? 1 : 2;            // state tiles (16 rows, 8 columns) of a warp
     constexpr int NT1 = KEEP ? 1 : 2;                // token tiles: KEEP X's, a warp 16 tokens and 8 columns; else X's and Q S's, 16 columns
     float *S = sm + 2 * T::STAGE, *R = S + DK * L, *Ub = R + CH * L;
-    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
+    const int tid = threadIdx.x, col0 = block % (DV / NS) * NS, hv = blockIdx.y, n = block / (DV / NS), hk = hv / (a.Hv / a.Hk);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
     const int w = tid >> 5, lane = tid & 31, g4 = lane >> 2, c2 = 2 * (lane & 3);
@@ -431,14 +431,14 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
 }
 
 template <typename IO, int DK, int DV>
-__global__ void __launch_bounds__(WT) gdr_reverse_simt_kernel(P p)
+KDA_DEVICE void walk_reverse(const P &p, unsigned block)
 {
     const GdrArgs &a = p.a;
     extern __shared__ float sm[];
     using T = Tiles<IO, DK>;
     constexpr int LK = T::LK, L = LS<DK>, NSR = DK == 64 ? 1 : 2;
     float *S = sm + 2 * T::STAGE, *Yb = S + DK * L, *dO = Yb + CH * L, *W = dO + CH * L;
-    const int tid = threadIdx.x, col0 = blockIdx.x % (DV / NS) * NS, hv = blockIdx.y, n = blockIdx.x / (DV / NS), hk = hv / (a.Hv / a.Hk);
+    const int tid = threadIdx.x, col0 = block % (DV / NS) * NS, hv = blockIdx.y, n = block / (DV / NS), hk = hv / (a.Hv / a.Hk);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
     const int w = tid >> 5, lane = tid & 31, g4 = lane >> 2, c2 = 2 * (lane & 3);
@@ -520,6 +520,19 @@ __global__ void __launch_bounds__(WT) gdr_reverse_simt_kernel(P p)
     }
     if (!a.ds0) return;
     each_state([&](int i, int e, int row, int c) { st2(a.ds0 + st + (size_t)row * DV + c, s[i][e], s[i][e + 1]); });
+}
+
+template <typename IO, int DK, int DV>
+__global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
+{
+    walk_forward<IO, DK, DV, false>(p, blockIdx.x);
+}
+// Both walks of the backward pass at once: neither reads what the other leaves.
+template <typename IO, int DK, int DV>
+__global__ void __launch_bounds__(WT) gdr_walks_simt_kernel(P p)
+{
+    if (blockIdx.x & 1) walk_forward<IO, DK, DV, true>(p, blockIdx.x >> 1);
+    else walk_reverse<IO, DK, DV>(p, blockIdx.x >> 1);
 }
 
 // ---------------------------------------------------------------- gradients of q, k, g, beta, a chunk and value head a block
@@ -792,7 +805,7 @@ static_assert(walk_bytes<128>(3) <= 227 * 1024 && grads_bytes<128, 128>() <= 227
 template <typename IO, int DK, int DV>
 cudaError_t launch_all(const GdrArgs &a, bool backward, cudaStream_t s)
 {
-    struct TagP; struct TagF; struct TagK; struct TagR; struct TagG;
+    struct TagP; struct TagF; struct TagR; struct TagG;
     constexpr int FB = walk_bytes<DK>(2), RB = walk_bytes<DK>(3);
     const long long slots = gdr_slots(a.N, a.T);
     P p{a, carve(a.ws, slots * a.Hv, DK, DV, backward, a.Hv > a.Hk)};
@@ -803,19 +816,14 @@ cudaError_t launch_all(const GdrArgs &a, bool backward, cudaStream_t s)
     }
     const dim3 chain((unsigned)a.N * (DV / NS), a.Hv);
     if (!backward) {
-        auto fn = gdr_forward_simt_kernel<IO, DK, DV, false>;
+        auto fn = gdr_forward_simt_kernel<IO, DK, DV>;
         if ((e = smem_opt_in<TagF>((const void *)fn, FB)) != cudaSuccess) return e;
         fn<<<chain, WT, FB, s>>>(p);
         return cudaGetLastError();
     }
-    if (a.T > 0) {
-        auto fn = gdr_forward_simt_kernel<IO, DK, DV, true>;
-        if ((e = smem_opt_in<TagK>((const void *)fn, FB)) != cudaSuccess) return e;
-        fn<<<chain, WT, FB, s>>>(p);
-    }
-    auto rv = gdr_reverse_simt_kernel<IO, DK, DV>;
-    if ((e = smem_opt_in<TagR>((const void *)rv, RB)) != cudaSuccess) return e;
-    rv<<<chain, WT, RB, s>>>(p);
+    auto fn = gdr_walks_simt_kernel<IO, DK, DV>;
+    if ((e = smem_opt_in<TagR>((const void *)fn, RB)) != cudaSuccess) return e;
+    fn<<<dim3(2 * chain.x, chain.y), WT, RB, s>>>(p);
     if (a.T > 0) {
         auto gr = gdr_grads_simt_kernel<IO, DK, DV>;
         if ((e = smem_opt_in<TagG>((const void *)gr, grads_bytes<DK, DV>())) != cudaSuccess) return e;

@@ -106,9 +106,8 @@ KDA_DEVICE void put_tokens(uint32_t to, const float (&x)[16])
 
 }  // namespace gdr
 
-// Prepares the operand pointers of a call on its workspace; launches prep and the forward walk
-// (keep: of the backward pass).
+// Lays out a call's workspace; makes the maps of q, k and v, and launches prep (nothing of both at T = 0).
 void gdr_tc_plan(const GdrArgs &a, bool backward, gdr::TcP &p);
-cudaError_t launch_gdr_prep_walk_tc(const gdr::TcP &p, bool keep, cudaStream_t s);
+cudaError_t launch_gdr_prep_tc(const gdr::TcP &p, CUtensorMap &mq, CUtensorMap &mk, CUtensorMap &mv, cudaStream_t s);
 
 }  // namespace kda

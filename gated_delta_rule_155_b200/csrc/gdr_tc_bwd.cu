@@ -1,9 +1,9 @@
 // gdr_tc_bwd.cu — gradients of the head-gated delta rule on tcgen05 tensor cores (bf16, dk = dv = 128).
 // The formulas are those of gdr_simt.cu, the operand layouts and the forward sweep those of gdr_tc.cu.
 //
-// Four launches: prep; the forward walk, which leaves each chunk's start state S and U; the reverse walk
-// (below), which leaves the gradient dS of each chunk's end state and H, and writes dv; then the gradients
-// of q, k, g and beta, a block per chunk and key head, which need only their own chunk's S, dS, U and H.
+// Three launches: prep; the forward walk, which leaves each chunk's start state S and U, together with the
+// reverse walk (below), which leaves the gradient dS of each chunk's end state and H, and writes dv; then the
+// gradients of q, k, g and beta, a block per chunk and key head, which need only their own chunk's S, dS, U and H.
 // S, dS, U and H are left as bf16 operand tiles, rounded once: they meet only products whose result is
 // stored in bf16 (the recurrences themselves keep fp32 and hi + lo operands).
 //
@@ -11,7 +11,7 @@
 //     Y^T = dS^T K^T     H^T = (lam Y)^T M + dO^T (P M)     dv = beta H
 //     dS^T <- gamma_C dS^T + (gamma dO)^T Q - (beta gamma H)^T K
 // dO enters the second product as it is; lam Y, gamma dO, beta gamma H, dS, M and P M as hi + lo pairs.
-#include "gdr_tc.cuh"
+#include "gdr_tc_walk.cuh"
 
 namespace kda {
 namespace {
@@ -19,12 +19,9 @@ namespace {
 using namespace gdr;
 
 // tensor memory columns: dS (fp32), dS as an operand (hi, lo), Y then lam Y then beta gamma H, H, gamma dO
-constexpr int TM_S = 0, TM_SHL = 128, TM_Y = 256, TM_H = 320, TM_G = 384;
-
-__global__ void __launch_bounds__(W_THREADS, 1)
-gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_do, TcP p)
+KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_do, const TcP &p, unsigned block)
 {
+    constexpr int TM_S = 0, TM_SHL = 128, TM_Y = 256, TM_H = 320, TM_G = 384;
     const GdrArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -35,8 +32,8 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     uint32_t *tslot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.x % a.Hv, hk = hv / (a.Hv / a.Hk);
-    const int n = p.order ? p.order[blockIdx.x / a.Hv] : blockIdx.x / a.Hv;
+    const int hv = (int)(block % a.Hv), hk = hv / (a.Hv / a.Hk);
+    const int n = p.order ? p.order[block / a.Hv] : (int)(block / a.Hv);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
     const size_t item0 = (size_t)slot_base(span.row0, n);
@@ -310,6 +307,16 @@ gdr_reverse_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Both walks at once: neither reads what the other leaves, and where there are few sequences and heads each
+// alone leaves SMs without work (64 + 64 blocks at 2 sequences of 32 heads: 250 us instead of 201 + 247).
+__global__ void __launch_bounds__(W_THREADS, 1)
+gdr_walks_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, TcP p)
+{
+    if (blockIdx.x & 1) walk_forward<true>(tm_q, tm_k, tm_v, p, blockIdx.x >> 1);
+    else walk_reverse(tm_q, tm_k, tm_do, p, blockIdx.x >> 1);
 }
 
 // ---------------------------------------------------------------- gradients of q, k, g, beta
@@ -734,16 +741,12 @@ cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s)
     struct TagR; struct TagG;
     TcP p;
     gdr_tc_plan(a, true, p);
-    cudaError_t e;
     CUtensorMap mq{}, mk{}, mv{}, mo{};
-    if (a.T > 0) {
-        if ((e = launch_gdr_prep_walk_tc(p, true, s)) != cudaSuccess) return e;
-        if (!make_tile_map(&mq, a.q, 1, a.T, a.Hk, CH) || !make_tile_map(&mk, a.k, 1, a.T, a.Hk, CH) ||
-            !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH) || !make_tile_map(&mo, a.dO, 1, a.T, a.Hv, CH))
-            return cudaErrorInvalidValue;
-    }
-    if ((e = smem_opt_in<TagR>((const void *)gdr_reverse_tc_kernel, W_KEEP_BYTES)) != cudaSuccess) return e;
-    gdr_reverse_tc_kernel<<<(unsigned)(a.N * a.Hv), W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mo, p);
+    cudaError_t e = launch_gdr_prep_tc(p, mq, mk, mv, s);
+    if (e != cudaSuccess) return e;
+    if (a.T > 0 && !make_tile_map(&mo, a.dO, 1, a.T, a.Hv, CH)) return cudaErrorInvalidValue;
+    if ((e = smem_opt_in<TagR>((const void *)gdr_walks_tc_kernel, W_KEEP_BYTES)) != cudaSuccess) return e;
+    gdr_walks_tc_kernel<<<(unsigned)(a.N * a.Hv) * 2, W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mv, mo, p);
     if (a.T > 0) {
         if ((e = smem_opt_in<TagG>((const void *)gdr_grads_tc_kernel, GS_BYTES)) != cudaSuccess) return e;
         int dev = 0, sms = 0;
