@@ -531,8 +531,9 @@ __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
 template <typename IO, int DK, int DV>
 __global__ void __launch_bounds__(WT) gdr_walks_simt_kernel(P p)
 {
-    if (blockIdx.x & 1) walk_forward<IO, DK, DV, true>(p, blockIdx.x >> 1);
-    else walk_reverse<IO, DK, DV>(p, blockIdx.x >> 1);
+    const unsigned half = gridDim.x / 2;
+    if (blockIdx.x >= half) walk_forward<IO, DK, DV, true>(p, blockIdx.x - half);
+    else walk_reverse<IO, DK, DV>(p, blockIdx.x);
 }
 
 // ---------------------------------------------------------------- gradients of q, k, g, beta, a chunk and value head a block

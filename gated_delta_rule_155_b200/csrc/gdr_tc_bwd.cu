@@ -310,13 +310,16 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
 }
 
 // Both walks at once: neither reads what the other leaves, and where there are few sequences and heads each
-// alone leaves SMs without work (64 + 64 blocks at 2 sequences of 32 heads: 250 us instead of 201 + 247).
+// alone leaves SMs without work (64 + 64 blocks at 2 sequences of 32 heads: 261 us instead of 201 + 247).
+// The halves of the grid, not neighbouring blocks, take the two: neighbours share an instruction cache, and
+// with a reverse and a forward walk side by side the same call took 348 us.
 __global__ void __launch_bounds__(W_THREADS, 1)
 gdr_walks_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, TcP p)
 {
-    if (blockIdx.x & 1) walk_forward<true>(tm_q, tm_k, tm_v, p, blockIdx.x >> 1);
-    else walk_reverse(tm_q, tm_k, tm_do, p, blockIdx.x >> 1);
+    const unsigned half = gridDim.x / 2;
+    if (blockIdx.x >= half) walk_forward<true>(tm_q, tm_k, tm_v, p, blockIdx.x - half);
+    else walk_reverse(tm_q, tm_k, tm_do, p, blockIdx.x);
 }
 
 // ---------------------------------------------------------------- gradients of q, k, g, beta
