@@ -477,22 +477,22 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (ok) {
                     tc_fence_after();
                     if (u.r == 0)
-#pragma unroll
+#pragma unroll 2
                         for (int kk = 0; kk < 8; ++kk) {
                             const uint32_t x = kq + (kk >> 2) * TILE + (kk & 3) * 32;
                             mma_ss(tmem + TG_GRAM, sdesc(x, 16, 1024), sdesc(x, 16, 1024), id_gram, kk);
                         }
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < 8; ++kk)
                         mma_ss(tmem + TG_DP, sdesc(ho + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024),
                                sdesc(uu + kk * 2048, TILE / 2, 1024), id_dp, kk);
                     mma_commit(m_p);
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < 8; ++kk)
                         mma_ss(tmem + TG_ST, sdesc(ho + (kk >> 2) * TILE + (kk & 3) * 32, 16, 1024),
                                sdesc(ss + kk * 2048, TILE, 1024), id_st, kk);
                     mma_commit(m_st);
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < 8; ++kk)   // rows 64.. of A are whatever follows U: their lanes are not read
                         mma_ss(tmem + TG_UD, sdesc(uu + kk * 2048, TILE, 1024), sdesc(ds + kk * 2048, TILE, 1024), id_ud, kk);
                     mma_commit(m_ud);
@@ -501,10 +501,10 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (ok && (ok = wait(b_dot, u.i)) && (ok = wait(m_ud, u.i)) && v.w < nwork) load(v);
                 if (ok && (ok = wait(b_n, u.i)) && (u.r > 0 || u.wi == 0 || (ok = wait(b_out, u.wi - 1)))) {
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < 4; ++kk)   // [N; dPD] K
                         mma_ss(tmem + TG_ACC, sdesc(nn + kk * 32, 16, 1024), sdesc(kq + kk * 2048, TILE, 1024), id_st, u.r | kk);
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < 8; ++kk)   // rows 0..63 += N^T K, dPD^T Q; rows 64..: zeros
                         mma_ss(tmem + TG_ACC, sdesc(nn + kk * 2048, zero - nn - (kk >> 2) * (TILE / 2), 1024),
                                sdesc(kq + (kk >> 2) * (TILE / 2) + (kk & 3) * 2048, TILE, 1024), id_ud, 1);
@@ -614,16 +614,18 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_n);
-            // [H; dO] S^T
-            if (!wait_all(m_st, u.i)) return false;
-            tc_fence_after();
-            {
-                const float sc = krow ? -bt * gm : gm;
+            // [H; dO] S^T, then U dS^T (k rows): one piece of code for the two
+#pragma unroll 1
+            for (int ud = 0; ud < 2; ++ud) {
+                if (!wait_all(ud ? m_ud : m_st, u.i)) return false;
+                if (ud && !krow) break;
+                tc_fence_after();
+                const float sc = ud ? lm : krow ? -bt * gm : gm;
                 float d = 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t x[32];
-                    tmem_ld32(at + TG_ST + 64 * half + 32 * hf, x);
+                    tmem_ld32(at + (ud ? TG_UD : TG_ST) + 64 * half + 32 * hf, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -638,34 +640,13 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         }
                     }
                 }
-                row += sc * d;
-                if (krow) db -= gm * d;
-            }
-            // U dS^T
-            float kud = 0.0f;
-            if (!wait_all(m_ud, u.i)) return false;
-            tc_fence_after();
-            if (krow) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t x[32];
-                    tmem_ld32(at + TG_UD + 64 * half + 32 * hf, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 k4 = *(const uint4 *)(own + swz(L, 4 * hf + j));
-                        const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x0 = lm * __uint_as_float(x[8 * j + 2 * i]), x1 = lm * __uint_as_float(x[8 * j + 2 * i + 1]);
-                            kud += x0 * bf_lo(kw[i]) + x1 * bf_hi(kw[i]);
-                            acc[32 * hf + 8 * j + 2 * i] += x0;
-                            acc[32 * hf + 8 * j + 2 * i + 1] += x1;
-                        }
-                    }
+                if (ud) {
+                    s_kud[half * 64 + t] = lm * d;
+                    s_db[half * 64 + t] = db;
+                } else {
+                    row += sc * d;
+                    if (krow) db -= gm * d;
                 }
-                s_kud[half * 64 + t] = kud;
-                s_db[half * 64 + t] = db;
             }
             s_row[half * 128 + L] = row;
             tc_fence_before();
