@@ -89,11 +89,11 @@ KDA_DEVICE int page_of(const int *index, int n, int pages, int *err)
 {
     if (!index) return n;
     const int p = index[n];
-    if (p >= pages) {
+    if (p >= pages || p < -1) {
         raise_error(err, ERR_PAGE_INDEX);
         return -1;
     }
-    return p < 0 ? -1 : p;
+    return p;
 }
 
 // Whether sequence n may write its final state to `page`: no earlier sequence writes there and, in

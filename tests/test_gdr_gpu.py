@@ -581,3 +581,197 @@ def test_no_tokens_pass_the_state_through(kda):
     kda.kda_gdr_backward(*x, z(2, 0, 2, 128), None, s0, s0, d_initial_state=d0)
     kda.kda_check_device_error()
     assert out.shape == (2, 0, 2, 128) and torch.equal(sT, s0) and torch.equal(d0, s0)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64), ("bf16", 64)])
+def test_many_sequences(kda, io, dk):
+    """More sequences than a warp looks at in one round of the slot search, lengths from zero on."""
+    rng = np.random.default_rng(50)
+    lens = [int(n) for n in rng.integers(0, 90, size=70)] + [0, 200, 0]
+    cu, Hk, Hv = cu_of(lens), 1, 2
+    d = make(cu[-1], Hk, Hv, dk, dk, io, 51, len(lens))
+    cug = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    sT, d0 = torch.empty_like(d["s0"], device="cuda"), torch.empty_like(d["s0"], device="cuda")
+    out, _ = kda.kda_gdr_forward(*to(d, *NAMES), cug, d["s0"].cuda(), final_state=sT)
+    gr = kda.kda_gdr_backward(*to(d, *NAMES, "dO"), cug, d["s0"].cuda(), d["dS"].cuda(), d_initial_state=d0)
+    kda.kda_check_device_error()
+    a = [f64(d[n]) for n in NAMES]
+    ro, rs = gdr.forward(*a, cu, f64(d["s0"]))
+    ref = gdr.backward(*a, cu, f64(d["dO"]), f64(d["s0"]), f64(d["dS"]))
+    ex = not tc(io, dk, dk)
+    near(out, ro, io, ex, "out")
+    near(sT, rs, io, ex, "final state", stored=False)
+    near(d0, ref["d_initial_state"], io, ex, "d_initial_state", stored=False)
+    near(gr["dv"], ref["dv"], io, ex, "dv")
+    for n in ("dq", "dk", "dg", "dbeta"):
+        near_grad(gr[n], ref[n], io, ex, n)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 128)])
+def test_a_batch_is_its_parts(kda, io, dk):
+    """1100 sequences (two rounds of the slot search; more chunks than the GPU has SMs, so blocks take several):
+    outputs and gradients are bit for bit those of the batch's two halves, called apart."""
+    rng = np.random.default_rng(60)
+    lens = [int(n) for n in rng.integers(0, 20, size=1100)]
+    lens[37], lens[900] = 700, 500
+    cu, N, Hk, Hv = cu_of(lens), 1100, 1, 2
+    d = make(cu[-1], Hk, Hv, dk, dk, io, 61)
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    s0, dS = (0.3 * torch.randn(N, Hv, dk, dk, generator=gen, device="cuda") for _ in range(2))
+    x = dict(zip(NAMES + ("dO",), to(d, *NAMES, "dO")))
+
+    def run(a, b):
+        rows, offs = slice(cu[a], cu[b]), torch.tensor([c - cu[a] for c in cu[a:b + 1]], dtype=torch.int32, device="cuda")
+        y = {n: t[rows].clone() for n, t in x.items()}      # (a view would not start on 16 bytes)
+        sT, d0 = torch.empty_like(s0[a:b]), torch.empty_like(s0[a:b])
+        out, _ = kda.kda_gdr_forward(*(y[n] for n in NAMES), offs, s0[a:b].contiguous(), final_state=sT)
+        gr = kda.kda_gdr_backward(*(y[n] for n in NAMES), y["dO"], offs, s0[a:b].contiguous(), dS[a:b].contiguous(),
+                                  d_initial_state=d0)
+        return [out, sT, *(gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "d_initial_state"))]
+
+    whole, parts = run(0, N), [run(0, 470), run(470, N)]
+    kda.kda_check_device_error()
+    for i, t in enumerate(whole):
+        assert torch.equal(t, torch.cat([p[i] for p in parts])), i
+
+
+@pytest.mark.parametrize("chunk", [0, 1, 2])
+@pytest.mark.parametrize("direction", ["forward", "backward"])
+def test_a_wait_that_runs_out_is_reported(kda, chunk, direction):
+    """A tile load that is never issued: the bounded wait for it runs out after 1 ms, the blocks let finish what
+    they issued and return, the error is reported once, and the next call on the same context is right."""
+    lens, Hk, Hv = [200, 10, 130], 1, 2
+    cu = cu_of(lens)
+    d = make(cu[-1], Hk, Hv, 128, 128, "bf16", 70, 3)
+    cug = torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def run():
+        if direction == "forward":
+            out = kda.kda_gdr_forward(*to(d, *NAMES), cug, d["s0"].cuda())[0]
+        else:
+            out = kda.kda_gdr_backward(*to(d, *NAMES, "dO"), cug, d["s0"].cuda(), d["dS"].cuda())["dv"]
+        kda.kda_check_device_error()
+        return out
+
+    kda.kda_set_wait_test_hooks(1_000_000, chunk)
+    try:
+        with pytest.raises(kda.KdaError) as e:
+            run()
+        assert e.value.status == 5
+    finally:
+        kda.kda_set_wait_test_hooks(0, -1)
+    kda.kda_check_device_error()
+    got = run()
+    a = [f64(d[n]) for n in NAMES]
+    if direction == "forward":
+        near(got, gdr.forward(*a, cu, f64(d["s0"]))[0], "bf16", False, "out")
+    else:
+        near(got, gdr.backward(*a, cu, f64(d["dO"]), f64(d["s0"]), f64(d["dS"]))["dv"], "bf16", False, "dv")
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_two_calls_at_once(kda, io, dk):
+    """Calls on two streams, each with its own workspace, beside one another and in another order: the same bits."""
+    sets = []
+    for seed in (80, 81):
+        d = make(900, 1, 3, dk, dk, io, seed, 2)
+        sets.append((to(d, *NAMES, "dO"), d["s0"].cuda()))
+    cug = torch.tensor([0, 610, 900], dtype=torch.int32, device="cuda")
+
+    def call(i):
+        x, s0 = sets[i]
+        sT = torch.empty_like(s0)
+        out, _ = kda.kda_gdr_forward(*x[:5], cug, s0, final_state=sT)
+        gr = kda.kda_gdr_backward(*x, cug, s0)
+        return [out, sT, *(gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta"))]
+
+    alone = [call(i) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for order in ((0, 1), (1, 0)):
+        got = {}
+        for i in order:
+            with torch.cuda.stream(streams[i]):
+                got[i] = [call(i) for _ in range(3)]
+        torch.cuda.synchronize()
+        kda.kda_check_device_error()
+        for i in (0, 1):
+            for run in got[i]:
+                assert all(torch.equal(a, b) for a, b in zip(run, alone[i]))
+
+
+def test_far_pages(kda):
+    """Pages behind 2^32 bytes and 2^31 elements of the cache: states read, written, copied and packed there."""
+    Hv, dk, P = 32, 128, 4200                                  # 2 MB a page, 8.8 GB
+    pages = torch.empty(P, Hv, dk, dk, device="cuda")
+    far, N = torch.tensor([4199, 2060, 4100], dtype=torch.int32), 3
+    d = make(N * 2, 16, Hv, dk, dk, "bf16", 90, N)
+    pages[far.long().cuda()] = d["s0"].cuda()
+    x = [t.view(N, 2, *t.shape[1:]) for t in to(d, *NAMES)]
+    got = kda.kda_gdr_decode(*x, pages, far.cuda())
+    ro, rs = gdr.decode(*(f64(t) for t in x), f64(d["s0"]))
+    near(got, ro, "bf16", True, "decode")
+    near(pages[far.long().cuda()], rs, "bf16", True, "states", stored=False)
+    pages[far.long().cuda()] = d["s0"].cuda()
+    cu = [0, 1, 1, 6]
+    start, end = far.cuda(), torch.tensor([4198, 4196, 3000], dtype=torch.int32, device="cuda")
+    out, _ = kda.kda_gdr_forward(*to(d, *NAMES), torch.tensor(cu, dtype=torch.int32, device="cuda"), pages,
+                                 final_state=pages, initial_index=start, final_index=end)
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), cu, f64(d["s0"]))
+    near(out, ro, "bf16", False, "forward")
+    near(pages[end.long()], rs, "bf16", False, "final states", stored=False)
+    cache = pages.view(1, P, Hv, dk, dk)
+    kept = pages[end.long()].clone()
+    kda.kda_pages_copy(cache, end, torch.tensor([4000, 1, 4195], dtype=torch.int32, device="cuda"))
+    assert torch.equal(pages[[4000, 1, 4195]], kept)
+    refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    refs[end.long()] = 1
+    table = end.clone()
+    assert int(kda.kda_pages_compact(cache, refs, table)) == 3
+    kda.kda_check_device_error()
+    assert sorted(table.tolist()) == [0, 1, 2] and torch.equal(pages[table.long()], kept)
+
+
+def test_indices_below_minus_one_are_refused(kda):
+    d = make(4, 1, 1, 128, 128, "bf16", 91, 4)
+    state, i32 = d["s0"].cuda(), lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    out = torch.full((4, 1, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    kda.kda_gdr_decode(*to(d, *NAMES), state, i32(0, -2, -1, 3), out)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_check_device_error()
+    assert e.value.status == 7
+    assert bool((out[1:3] == 7.0).all()) and not bool((out[[0, 3]] == 7.0).any())
+    assert torch.equal(state[1:3].cpu(), d["s0"][1:3])
+
+
+def test_inputs_on_another_stream_and_strided_inputs(kda):
+    """A call made on the stream that its inputs are made on; inputs that are not contiguous are refused."""
+    s = torch.cuda.Stream()
+    d = make(130, 1, 2, 128, 128, "bf16", 92)
+    x = to(d, *NAMES)
+    with torch.cuda.stream(s):
+        y = [t.clone()[None] for t in x]
+        out, _ = kda.kda_gdr_forward(*y)
+        explicit, _ = kda.kda_gdr_forward(*y, stream=s)
+    s.synchronize()
+    ro, _ = gdr.forward(*(f64(d[n]) for n in NAMES), [0, 130])
+    near(out[0], ro, "bf16", False, "out")
+    assert torch.equal(out, explicit)
+    wide = torch.zeros(1, 130, 2, 256, dtype=torch.bfloat16, device="cuda")[..., :128]
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.kda_gdr_forward(y[0], y[1], wide, y[3], y[4])
+
+
+def test_exponents_far_apart(kda):
+    """Keys, queries and values of very different sizes in one chunk; the state's small entries keep their bits."""
+    d = make(200, 1, 2, 128, 128, "bf16", 93)
+    scale = 2.0 ** torch.randint(-6, 7, (200, 1, 1), generator=torch.Generator().manual_seed(1)).float()
+    d["v"] = (d["v"].float() * scale).bfloat16()
+    d["q"] = (d["q"].float() * scale.flip(0)).bfloat16()
+    x = [t[None] for t in to(d, *NAMES)]
+    sT = torch.empty_like(d["s0"], device="cuda")
+    out, _ = kda.kda_gdr_forward(*x, None, d["s0"].cuda(), final_state=sT)
+    kda.kda_check_device_error()
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), [0, 200], f64(d["s0"]))
+    near(out[0], ro, "bf16", False, "out")
+    near(sT, rs, "bf16", False, "state", stored=False)
