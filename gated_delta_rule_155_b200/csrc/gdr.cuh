@@ -148,17 +148,19 @@ KDA_DEVICE void put_block(float *dst, int ld, const float (&c)[4], float sign, i
     *(float2 *)(d + 8 * ld) = make_float2(sign * c[2], sign * c[3]);
 }
 
-// M <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats: the 16 x 16 diagonal blocks
-// by forward substitution (one column a thread: a product form such as (I - A)(I + A^2)... would cancel
-// where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64)
-// with mma_block's products.  A's upper right quarter is scratch.  256 threads; M's upper triangle is written
-// as zeros.  Ends with a barrier.
-template <int LD>
-KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
+// A <- (I + A)^-1 for the strictly lower A, 64 x 64 in rows of LD floats, in place: the 16 x 16 diagonal
+// blocks by forward substitution (one column a thread: a product form such as (I - A)(I + A^2)... would
+// cancel where keys repeat), then twice [[X, 0], [B, Y]]^-1 = [[X^-1, 0], [-Y^-1 B X^-1, Y^-1]] (16 -> 32 -> 64)
+// with mma_block's products.  Rows 0..31 of columns 32.. are scratch, and hold no zeros behind it.  W warps,
+// at least four.  Ends with a barrier.
+template <int LD, int W>
+KDA_DEVICE void unit_lower_inverse(float *A, int tid)
 {
+    const int w = tid >> 5, lane = tid & 31;
     float *tmp = A + 32;   // rows 0..31, columns 32..63
     if (tid < 64) {
         const int b = tid >> 4, c = tid & 15;
+        float *D = A + 16 * b * (LD + 1);
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -166,48 +168,48 @@ KDA_DEVICE void unit_lower_inverse(float *A, float *M, int tid)
 #pragma unroll
             for (int m = 0; m < r; m += 4) {
                 float a[4];
-                ld4(A + (16 * b + r) * LD + 16 * b + m, a);
+                ld4(D + r * LD + m, a);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (m + e < r) s[e] -= a[e] * x[m + e];
             }
             x[r] = (s[0] + s[1]) + (s[2] + s[3]);
         }
+        __syncwarp();      // both blocks of the warp have been read
 #pragma unroll
-        for (int r = 0; r < 16; ++r) M[(16 * b + r) * LD + 16 * b + c] = x[r];
-    } else {
-        const float z[4] = {};
-        for (int u = tid - 64; u < 6 * 64; u += 192) {   // blocks (0,1) (0,2) (0,3) (1,2) (1,3) (2,3)
-            const int b = u >> 6, I = b < 3 ? 0 : b < 5 ? 1 : 2, J = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
-            st4(M + (16 * I + ((u & 63) >> 2)) * LD + 16 * J + 4 * (u & 3), z);
-        }
+        for (int r = 0; r < 16; ++r) D[r * LD + c] = x[r];
     }
     __syncthreads();
-    const int w = tid >> 5, lane = tid & 31;
     {   // 16 -> 32: two pairs of blocks, eight columns a warp
         const int o = 32 * (w >> 1), n = 8 * (w & 1);
         if (w < 4) {
             float c[4] = {};
-            mma_block(c, n, 16, A + (o + 16) * LD + o, LD, M + o * LD + o + n, LD, lane);
+            mma_block(c, n, 16, A + (o + 16) * LD + o, LD, A + o * LD + o + n, LD, lane);
             put_block(tmp + (o >> 1) * LD + n, LD, c, 1.0f, lane);
         }
         __syncthreads();
         if (w < 4) {
             float c[4] = {};
-            mma_block(c, 0, 16, M + (o + 16) * LD + o + 16, LD, tmp + (o >> 1) * LD + n, LD, lane);
-            put_block(M + (o + 16) * LD + o + n, LD, c, -1.0f, lane);
+            mma_block(c, 0, 16, A + (o + 16) * LD + o + 16, LD, tmp + (o >> 1) * LD + n, LD, lane);
+            put_block(A + (o + 16) * LD + o + n, LD, c, -1.0f, lane);
         }
     }
     __syncthreads();
-    {   // 32 -> 64: sixteen rows and eight columns a warp
-        const int m = 16 * (w >> 2), n = 8 * (w & 3);
+    // 32 -> 64: eight tiles of sixteen rows and eight columns
+#pragma unroll
+    for (int i = w; i < 8; i += W) {
+        const int m = 16 * (i >> 2), n = 8 * (i & 3);
         float c[4] = {};
-        mma_block(c, n, 32, A + (32 + m) * LD, LD, M + n, LD, lane);           // M is lower
+        mma_block(c, n, 32, A + (32 + m) * LD, LD, A + n, LD, lane);            // lower
         put_block(tmp + m * LD + n, LD, c, 1.0f, lane);
-        __syncthreads();
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = w; i < 8; i += W) {
+        const int m = 16 * (i >> 2), n = 8 * (i & 3);
         float x[4] = {};
-        mma_block(x, 0, m + 16, M + (32 + m) * LD + 32, LD, tmp + n, LD, lane);
-        put_block(M + (32 + m) * LD + n, LD, x, -1.0f, lane);
+        mma_block(x, 0, m + 16, A + (32 + m) * LD + 32, LD, tmp + n, LD, lane);
+        put_block(A + (32 + m) * LD + n, LD, x, -1.0f, lane);
     }
     __syncthreads();
 }

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
     extern __shared__ float sm[];
     constexpr int LK = DK + 4;
     float *K = sm, *Q = K + CH * LK, *A = Q + CH * LK, *Pm = A + CH * LM;
-    float *M = K;             // K and Q are read only by the Gram products
+    float *M = A;             // the inverse takes A's place
     __shared__ Gates gs;
     const int tid = threadIdx.x, hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
     const size_t row0 = (size_t)span.row0 + c * CH;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
             }
     }
     __syncthreads();
-    unit_lower_inverse<LM>(A, M, tid);
+    unit_lower_inverse<LM, NT / 32>(A, tid);
     const size_t item = (size_t)blockIdx.x * a.Hv + hv;
     float *dst = p.w.I + item * ITEM;
     float pm[4][4] = {};
@@ -225,7 +225,10 @@ __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
 #pragma unroll
         for (int e = 0; e < 4; e += 2)
             *(float2 *)(dst + CH * CH + (m + g4 + 4 * e) * CH + h + 8 * i + c2) = make_float2(pm[i][e], pm[i][e + 1]);
-    for (int u = tid; u < CH * CH / 4; u += NT) *(float4 *)(dst + 4 * u) = *(const float4 *)(M + (u >> 4) * LM + 4 * (u & 15));
+    for (int u = tid; u < CH * CH / 4; u += NT) {
+        const int t = u >> 4, s = 4 * (u & 15);
+        *(float4 *)(dst + 4 * u) = t < 32 && s >= 32 ? make_float4(0.f, 0.f, 0.f, 0.f) : *(const float4 *)(M + t * LM + s);
+    }
     if (tid < CH) {
         float *g = p.w.I + item * ITEM + 2 * CH * CH + tid;
         g[0] = gs.gam[tid];

@@ -14,12 +14,13 @@ namespace {
 using namespace gdr;
 
 // ---------------------------------------------------------------- prep
-// Shared memory: K; Q tiles; once their product is done, P (hi, lo; later P M) and M (fp32) in their
-// place.  A (fp32), later M (hi, lo).  53 KB, so that four blocks share an SM.
-constexpr int LM = 68;
-constexpr int PR_KQ = 0, PR_P = 0, PR_M = TILE, PR_A = 33 * 1024, PR_MHL = PR_A, PR_G = PR_A + 64 * LM * 4;
+// Shared memory: K; Q tiles; once their product is done, P (hi, lo; later P M) and A (fp32; its inverse M in
+// place; later M's hi, lo) in their place.  36 KB and 128 threads, so that six blocks share an SM: a block is a
+// chain of short steps with a barrier behind each, and what one leaves idle the others use.
+constexpr int LM = 68, PR_T = 128;
+constexpr int PR_KQ = 0, PR_P = 0, PR_A = TILE, PR_MHL = PR_A, PR_G = 33 * 1024 + 512;
 constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
-static_assert(PR_M + 64 * LM * 4 <= PR_A && PR_MHL + TILE <= PR_G && PR_BYTES <= 57344, "regions");
+static_assert(PR_A + 64 * LM * 4 <= PR_G && PR_MHL + TILE <= PR_G && 2 * TILE <= PR_G && PR_BYTES + 1024 <= 228 * 1024 / 6, "regions");
 
 // order[r] <- the sequence whose length is the r-th longest: the walks start with the longest.  A warp a sequence.
 KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
@@ -37,12 +38,12 @@ KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
     }
 }
 
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(PR_T, 6)
 gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
 {
     const GdrArgs &a = p.a;
     if (p.order && blockIdx.y == gridDim.y - 1) {       // the blocks behind the heads: the sequences' order
-        order_sequences(p, blockIdx.x * (256 / 32) + (threadIdx.x >> 5), gridDim.x * (256 / 32), threadIdx.x & 31);
+        order_sequences(p, blockIdx.x * (PR_T / 32) + (threadIdx.x >> 5), gridDim.x * (PR_T / 32), threadIdx.x & 31);
         return;
     }
     int n, c;
@@ -50,7 +51,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *A = (float *)(sm + PR_A), *M = (float *)(sm + PR_M);
+    float *A = (float *)(sm + PR_A);
     float *graw = (float *)(sm + PR_G), *ghi = graw + 64, *glo = ghi + 64, *beta = glo + 64;
     uint64_t *bars = (uint64_t *)(sm + PR_G + 4 * 256);   // tiles, [K; Q] K^T, P M
     uint32_t *tslot = (uint32_t *)(bars + 3);
@@ -74,7 +75,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_alloc(tslot, 64);
         tmem_relinquish();
     }
-    if (tid >= 64 && tid < 128) {
+    if (tid >= 64) {
         const int t = tid - 64;
         const size_t at = (size_t)(row0 + t) * a.Hv + hv;
         graw[t] = t < valid ? clamp_gate(__bfloat162float(((const __nv_bfloat16 *)a.g)[at])) : 0.0f;
@@ -114,20 +115,19 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0 && !*abort_flag) mbar_wait_bounded(&bars[1], 0, abort_flag, a.err, p.wait_ns);
     __syncthreads();
     bool ok = !*abort_flag;
-    const int lq = warp & 3, r = 32 * lq + lane, half = warp >> 2, s0 = 32 * half;   // lane of tensor memory, 32 of its columns
-    const uint32_t at = tmem + ((uint32_t)(32 * lq) << 16) + s0;
+    const int t = tid & 63;                    // row of [K; Q] K^T in the thread's lane of tensor memory
+    const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
     if (ok) {
         tc_fence_after();
-        const int t = r & 63;
-        const int last = t >= valid ? -1 : r < 64 ? t - 1 : t;   // A is strictly lower; rows behind the end may hold NaN
-        const float gh = ghi[t], gl = glo[t], scale = r < 64 ? beta[t] : 1.0f;
+        const bool krow = tid < 64;
+        const int last = t >= valid ? -1 : krow ? t - 1 : t;     // A is strictly lower; rows behind the end may hold NaN
+        const float gh = ghi[t], gl = glo[t], scale = krow ? beta[t] : 1.0f;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {          // eight columns at a time: the instruction cache bounds this kernel
-            const int c0 = s0 + 8 * c;
+        for (int c0 = 0; c0 < 64; c0 += 8) {   // eight columns at a time: the instruction cache bounds this kernel
             float y[8] = {};
-            if (c0 <= 32 * (lq & 1) + 31) {    // else the warp's rows all end before these columns
+            if (c0 <= 32 * (warp & 1) + 31) {  // else the warp's rows all end before these columns
                 uint32_t x[8];
-                tmem_ld8(at + 8 * c, x);
+                tmem_ld8(at + c0, x);
                 float h[8], l[8];
                 ld4(ghi + c0, *(float(*)[4])h);
                 ld4(ghi + c0 + 4, *(float(*)[4])(h + 4));
@@ -139,7 +139,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = c0 + e <= last ? h[e] * __uint_as_float(x[e]) : 0.0f;
             }
-            if (r < 64) {
+            if (krow) {
                 st4(A + t * LM + c0, *(const float(*)[4])y);
                 st4(A + t * LM + c0 + 4, *(const float(*)[4])(y + 4));
             } else {
@@ -151,18 +151,23 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     __syncthreads();
     if (ok) {
-        unit_lower_inverse<LM>(A, M, tid);
-        {                                      // M as hi + lo
-            const int t = tid >> 2;
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-                float y[8];
-                const int q8 = (tid & 3) + 4 * j;      // a quarter of a warp reads 8 different bank groups
-                ld4(M + t * LM + 8 * q8, *(float(*)[4])y);
-                ld4(M + t * LM + 8 * q8 + 4, *(float(*)[4])(y + 4));
-                put_split(sm + PR_MHL, sm + PR_MHL + TILE / 2, t, q8, y);
-            }
+        unit_lower_inverse<LM, PR_T / 32>(A, tid);
+        // M as hi + lo over itself: a thread has half a row
+        const int q = 4 * (tid >> 6);
+        float y[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ld4(A + t * LM + 8 * (q + j), *(float(*)[4])y[j]);
+            ld4(A + t * LM + 8 * (q + j) + 4, *(float(*)[4])(y[j] + 4));
         }
+        __syncthreads();
+        if (t < 32 && q)                       // scratch of the inverse
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[j][e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put_split(sm + PR_MHL, sm + PR_MHL + TILE / 2, t, q + j, y[j]);
         fence_proxy_async();
     }
     tc_fence_before();
@@ -186,16 +191,16 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     ok = ok && !*abort_flag;
     if (ok) {
         tc_fence_after();
-        if (r < 64) {
+        if (tid < 64) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {      // over P, which has been read
+            for (int c0 = 0; c0 < 64; c0 += 8) {      // over P, which has been read
                 uint32_t x[8];
-                tmem_ld8(at + 8 * c, x);
+                tmem_ld8(at + c0, x);
                 tmem_wait_ld();
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[e]);
-                put_split(sm + PR_P, sm + PR_P + TILE / 2, r, 4 * half + c, y);
+                put_split(sm + PR_P, sm + PR_P + TILE / 2, t, c0 / 8, y);
             }
             fence_proxy_async();
         }
@@ -270,7 +275,7 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        gdr_prep_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), 256, PR_BYTES, s>>>(mq, mk, p);
+        gdr_prep_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), PR_T, PR_BYTES, s>>>(mq, mk, p);
     }
     return cudaGetLastError();
 }
