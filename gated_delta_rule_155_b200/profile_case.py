@@ -6,6 +6,9 @@
     python -m gated_delta_rule_155_b200.profile_case varlen  --T 8192 --H 96 --launches 3
     python -m gated_delta_rule_155_b200.profile_case backward --B 1 --T 1024 --H 148 --launches 2
     python -m gated_delta_rule_155_b200.profile_case layer_decode --B 64 --H 96 --launches 3
+    python -m gated_delta_rule_155_b200.profile_case gdr          --B 2 --T 4096 --H 32 --Hk 16 --launches 3
+    python -m gated_delta_rule_155_b200.profile_case gdr_backward --B 2 --T 4096 --H 32 --Hk 16 --launches 3
+    python -m gated_delta_rule_155_b200.profile_case gdr_decode   --B 64 --H 32 --Hk 16 --launches 3
 
 Inputs come from the seeded generators; nothing is checked or timed here (use the
 tests for parity and bench.py for timing).  Sizes should keep the inputs larger than
@@ -21,10 +24,12 @@ import torch
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("kind", choices=["prefill", "decode", "layer", "varlen", "backward", "layer_decode"])
+    ap.add_argument("kind", choices=["prefill", "decode", "layer", "varlen", "backward", "layer_decode", "gdr", "gdr_backward",
+                                     "gdr_decode"])
     ap.add_argument("--B", type=int, default=2)
     ap.add_argument("--T", type=int, default=4096)
     ap.add_argument("--H", type=int, default=96)
+    ap.add_argument("--Hk", type=int, default=0, help="key heads of the head-gated rule (0: as many as H)")
     ap.add_argument("--d", type=int, default=128)
     ap.add_argument("--launches", type=int, default=3)
     a = ap.parse_args(argv)
@@ -34,6 +39,24 @@ def main(argv=None):
     from gated_delta_rule_155_b200 import kda
 
     dev = torch.device("cuda", 0)
+    if a.kind.startswith("gdr"):
+        gen, Hk = torch.Generator(device=dev).manual_seed(7), a.Hk or a.H
+        T = 1 if a.kind == "gdr_decode" else a.T
+        rn = lambda *s: torch.randn(*s, generator=gen, device=dev)  # noqa: E731
+        unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).bfloat16()  # noqa: E731
+        args = [unit(rn(a.B, T, Hk, a.d)), unit(rn(a.B, T, Hk, a.d)), rn(a.B, T, a.H, a.d).bfloat16(),
+                -torch.nn.functional.softplus(rn(a.B, T, a.H) - 2.0).bfloat16(), torch.sigmoid(rn(a.B, T, a.H)).bfloat16()]
+        args[3] = args[3].contiguous()
+        extra = rn(a.B, T, a.H, a.d).bfloat16() if a.kind == "gdr_backward" else rn(a.B, a.H, a.d, a.d)
+        for _ in range(a.launches):
+            if a.kind == "gdr":
+                kda.kda_gdr_forward(*args, final_state=extra)
+            elif a.kind == "gdr_backward":
+                kda.kda_gdr_backward(*args, extra)
+            else:
+                kda.kda_gdr_decode(*args, extra)
+        kda.kda_check_device_error()
+        return
     if a.kind == "prefill":
         d = inputs.prefill_inputs(a.B, a.T, a.H, a.d, a.d, io="bf16", seed=2)
         args = [d[n].to(dev) for n in ("q", "k", "v", "g", "beta")]
