@@ -51,8 +51,12 @@ KDA_DEVICE void mbar_arrive(uint64_t *bar)
 KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
 {
     hi = pack_bf16x2(x0, x1);
-    const float2 h = unpack_bf16x2(hi);
-    lo = pack_bf16x2(x0 - h.x, x1 - h.y);
+    float l0, l1;
+    asm("{\n\t.reg .b64 x, h, m;\n\t.reg .b32 a, b;\n\t"
+        "mov.b64 x, {%2, %3};\n\tshl.b32 a, %4, 16;\n\tand.b32 b, %4, 0xffff0000;\n\tmov.b64 h, {a, b};\n\t"
+        "mov.b64 m, {%5, %5};\n\tfma.rn.f32x2 x, h, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(l0), "=f"(l1) : "f"(x0), "f"(x1), "r"(hi), "f"(-1.0f));
+    lo = pack_bf16x2(l0, l1);
 }
 
 // find_slot for a chunk's first row and its rows: {row, rows}, rows 0 for a slot that no chunk has (out of
