@@ -224,8 +224,9 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (!(ok = wait_full(i))) break;
             {                                        // dS decayed, in the shadow of the product
                 const float gC = gates[GA_GAM + CH - 1];
+                float *x = (float *)S;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = __float_as_uint(gC * __uint_as_float(S[e]));
+                for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], gC, gC);
                 tmem_st32(at + TM_S + r0, S);
             }
             float r[16], w[16];
@@ -237,11 +238,15 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                     float g4[4];
                     ld4(gates + GA_GAM + t0 + e, g4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float f = __bfloat162float(*(const __nv_bfloat16 *)(dy + (e + k) * 128 + ((j ^ ((e + k) & 7)) << 4)));
-                        r[e + k] = t0 + e + k < valid ? g4[k] * f : 0.0f;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        r[e + k] = __bfloat162float(*(const __nv_bfloat16 *)(dy + (e + k) * 128 + ((j ^ ((e + k) & 7)) << 4)));
+                    mul2(r[e], r[e + 1], r[e], r[e + 1], g4[0], g4[1]);
+                    mul2(r[e + 2], r[e + 3], r[e + 2], r[e + 3], g4[2], g4[3]);
                 }
+                if (valid < CH)                      // rows behind the end may hold NaN
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (t0 + e >= valid) r[e] = 0.0f;
                 put_tokens(at + TM_G + t0, r);
             }
 #pragma unroll
@@ -253,7 +258,8 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                 tmem_ld16(at + TM_Y + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = w[e] * __uint_as_float(x[e]);
+                for (int e = 0; e < 16; e += 2)
+                    mul2(r[e], r[e + 1], w[e], w[e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 put_tokens(at + TM_Y + t0, r);
             }
             arrive(b_y);
@@ -266,7 +272,8 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                 tmem_ld16(at + TM_H + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = -w[e] * __uint_as_float(x[e]);
+                for (int e = 0; e < 16; e += 2)
+                    mul2(r[e], r[e + 1], -w[e], -w[e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 put_tokens(at + TM_Y + t0, r);       // lam Y has been read: H's product is done
                 arrive(b_w);
                 // H as an operand tile [token][dv], and dv = beta H

@@ -221,8 +221,9 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (!(ok = wait_full(ch))) break;
             {                                        // the state decayed, in the shadow of the product
                 const float gC = gates[GA_GAM + CH - 1];
+                float *x = (float *)S;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = __float_as_uint(gC * __uint_as_float(S[e]));
+                for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], gC, gC);
                 tmem_st32(at + TM_S + r0, S);
             }
             // beta V^T: column dv of the thread's tokens
@@ -237,11 +238,16 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                     ld4(gates + GA_BG + t0 + e, c4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float f = __bfloat162float(*(const __nv_bfloat16 *)(vt + (e + i) * 128 + ((j ^ ((e + i) & 7)) << 4)));
-                        r[e + i] = t0 + e + i < valid ? b4[i] * f : 0.0f;
-                        w[e + i] = c4[i];
+                        r[e + i] = __bfloat162float(*(const __nv_bfloat16 *)(vt + (e + i) * 128 + ((j ^ ((e + i) & 7)) << 4)));
+                        w[e + i] = -c4[i];
                     }
+                    mul2(r[e], r[e + 1], r[e], r[e + 1], b4[0], b4[1]);
+                    mul2(r[e + 2], r[e + 3], r[e + 2], r[e + 3], b4[2], b4[3]);
                 }
+                if (valid < CH)                      // rows behind the end may hold NaN
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (t0 + e >= valid) r[e] = 0.0f;
             }
             if (!(ok = wait_all(m_x, ch))) break;
             tc_fence_after();
@@ -250,7 +256,8 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                 tmem_ld16(at + TM_X + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] -= w[e] * __uint_as_float(x[e]);
+                for (int e = 0; e < 16; e += 2)
+                    fma2(r[e], r[e + 1], w[e], w[e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), r[e], r[e + 1]);
                 put_tokens(at + TM_X + t0, r);
             }
             arrive(b_r);
@@ -263,7 +270,8 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                 tmem_ld16(at + TM_U + t0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = w[e] * __uint_as_float(x[e]);
+                for (int e = 0; e < 16; e += 2)
+                    mul2(r[e], r[e + 1], w[e], w[e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 put_tokens(at + TM_X + t0, r);       // R has been read: U's product is done
                 arrive(b_u);
                 if (KEEP) {                          // [dv][token]
@@ -289,11 +297,14 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                 for (int e = 0; e < 16; e += 4) {
                     float g4[4];
                     ld4(gates + GA_GAM + t0 + e, g4);
+                    float o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        fma2(o[i], o[i + 1], g4[i], g4[i + 1], __uint_as_float(x[e + i]), __uint_as_float(x[e + i + 1]),
+                             __uint_as_float(y[e + i]), __uint_as_float(y[e + i + 1]));
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (t0 + e + i < valid)
-                            dst[(size_t)((e + i) * a.Hv) * D] =
-                                __float2bfloat16_rn(g4[i] * __uint_as_float(x[e + i]) + __uint_as_float(y[e + i]));
+                        if (t0 + e + i < valid) dst[(size_t)((e + i) * a.Hv) * D] = __float2bfloat16_rn(o[i]);
                 }
             }
             __syncwarp();
