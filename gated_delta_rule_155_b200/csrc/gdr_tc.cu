@@ -134,10 +134,21 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ld4(glo + c0, *(float(*)[4])l);
                 ld4(glo + c0 + 4, *(float(*)[4])(l + 4));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = scale * __expf((gh - h[e]) + (gl - l[e]));
+                for (int e = 0; e < 8; e += 2) {       // e^((gh - h) + (gl - l))
+                    fma2(h[e], h[e + 1], h[e], h[e + 1], -1.0f, -1.0f, gh, gh);
+                    fma2(l[e], l[e + 1], l[e], l[e + 1], -1.0f, -1.0f, gl, gl);
+                    fma2(h[e], h[e + 1], h[e], h[e + 1], 1.0f, 1.0f, l[e], l[e + 1]);
+                    h[e] = __expf(h[e]);
+                    h[e + 1] = __expf(h[e + 1]);
+                    mul2(h[e], h[e + 1], h[e], h[e + 1], scale, scale);
+                }
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = c0 + e <= last ? h[e] * __uint_as_float(x[e]) : 0.0f;
+                for (int e = 0; e < 8; e += 2) {
+                    mul2(y[e], y[e + 1], h[e], h[e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    if (c0 + e > last) y[e] = 0.0f;
+                    if (c0 + e + 1 > last) y[e + 1] = 0.0f;
+                }
             }
             if (krow) {
                 st4(A + t * LM + c0, *(const float(*)[4])y);

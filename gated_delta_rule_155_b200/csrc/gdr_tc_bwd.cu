@@ -355,10 +355,13 @@ constexpr int TG_GRAM = 0, TG_DP = 64, TG_ST = 128, TG_UD = 256, TG_ACC = 384;
 
 KDA_DEVICE float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 KDA_DEVICE float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-KDA_DEVICE float dot8(const uint4 &a, const uint4 &b)
+// d0 + d1 += the products of eight pairs of bf16
+KDA_DEVICE void dot8(float &d0, float &d1, const uint4 &a, const uint4 &b)
 {
-    return (bf_lo(a.x) * bf_lo(b.x) + bf_hi(a.x) * bf_hi(b.x)) + (bf_lo(a.y) * bf_lo(b.y) + bf_hi(a.y) * bf_hi(b.y)) +
-           (bf_lo(a.z) * bf_lo(b.z) + bf_hi(a.z) * bf_hi(b.z)) + (bf_lo(a.w) * bf_lo(b.w) + bf_hi(a.w) * bf_hi(b.w));
+    fma2(d0, d1, bf_lo(a.x), bf_hi(a.x), bf_lo(b.x), bf_hi(b.x), d0, d1);
+    fma2(d0, d1, bf_lo(a.y), bf_hi(a.y), bf_lo(b.y), bf_hi(b.y), d0, d1);
+    fma2(d0, d1, bf_lo(a.z), bf_hi(a.z), bf_lo(b.z), bf_hi(b.z), d0, d1);
+    fma2(d0, d1, bf_lo(a.w), bf_hi(a.w), bf_lo(b.w), bf_hi(b.w), d0, d1);
 }
 
 __global__ void __launch_bounds__(G_THREADS, 1)
@@ -549,18 +552,21 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             const float ghi = gates[GA_HI + t], glo = gates[GA_LO + t];
             // <S, dS> of the block, H.V of the row
             {
-                float x = 0.0f;
+                float x = 0.0f, y = 0.0f;
 #pragma unroll 2
                 for (int i = 0; i < 8; ++i)
-                    x += dot8(*(const uint4 *)(sm + GS_S + 16 * (tid + i * G_VT)), *(const uint4 *)(sm + GS_DS + 16 * (tid + i * G_VT)));
-                x = warp_sum(x);
+                    dot8(x, y, *(const uint4 *)(sm + GS_S + 16 * (tid + i * G_VT)), *(const uint4 *)(sm + GS_DS + 16 * (tid + i * G_VT)));
+                x = warp_sum(x + y);
                 if (lane == 0) s_sum[warp] = x;
             }
             float db = 0.0f, row = 0.0f;
-            if (krow)
+            if (krow) {
+                float x = 0.0f;
 #pragma unroll 2
                 for (int j = 0; j < 8; ++j)
-                    db += dot8(*(const uint4 *)(sm + GS_HO + half * TILE + swz(t, j)), *(const uint4 *)(sm + GS_V + half * (TILE / 2) + swz(t, j)));
+                    dot8(db, x, *(const uint4 *)(sm + GS_HO + half * TILE + swz(t, j)), *(const uint4 *)(sm + GS_V + half * (TILE / 2) + swz(t, j)));
+                db += x;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(b_dot);
             // [K; Q] K^T and [H; dO] U^T, columns s = 32 half ..
@@ -588,7 +594,13 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     ld4(gates + GA_LO + c0, *(float(*)[4])l);
                     ld4(gates + GA_LO + c0 + 4, *(float(*)[4])(l + 4));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[e] = __expf((ghi - h[e]) + (glo - l[e]));
+                    for (int e = 0; e < 8; e += 2) {     // e^((ghi - h) + (glo - l))
+                        fma2(h[e], h[e + 1], h[e], h[e + 1], -1.0f, -1.0f, ghi, ghi);
+                        fma2(l[e], l[e + 1], l[e], l[e + 1], -1.0f, -1.0f, glo, glo);
+                        fma2(h[e], h[e + 1], h[e], h[e + 1], 1.0f, 1.0f, l[e], l[e + 1]);
+                        h[e] = __expf(h[e]);
+                        h[e + 1] = __expf(h[e + 1]);
+                    }
                     tmem_wait_ld();
                     float y[8];
 #pragma unroll
@@ -628,7 +640,7 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (ud && !krow) break;
                 tc_fence_after();
                 const float sc = ud ? lm : krow ? -bt * gm : gm;
-                float d = 0.0f;
+                float d = 0.0f, d1 = 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t x[32];
@@ -641,12 +653,13 @@ gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float x0 = __uint_as_float(x[8 * j + 2 * i]), x1 = __uint_as_float(x[8 * j + 2 * i + 1]);
-                            d += x0 * bf_lo(kw[i]) + x1 * bf_hi(kw[i]);
-                            acc[32 * hf + 8 * j + 2 * i] += sc * x0;
-                            acc[32 * hf + 8 * j + 2 * i + 1] += sc * x1;
+                            float *c = acc + 32 * hf + 8 * j + 2 * i;
+                            fma2(d, d1, x0, x1, bf_lo(kw[i]), bf_hi(kw[i]), d, d1);
+                            fma2(c[0], c[1], x0, x1, sc, sc, c[0], c[1]);
                         }
                     }
                 }
+                d += d1;
                 if (ud) {
                     s_kud[half * 64 + t] = lm * d;
                     s_db[half * 64 + t] = db;
