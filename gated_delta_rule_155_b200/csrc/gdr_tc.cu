@@ -159,9 +159,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         fence_proxy_async();
         tc_fence_before();
-    }
-    __syncthreads();
-    if (ok) {
+        if (krow) named_bar_sync(1, 64);       // A is there: the inverse's diagonal blocks (these warps) need no P
         unit_lower_inverse<LM, PR_T / 32>(A, tid);
         // M as hi + lo over itself: a thread has half a row
         const int q = 4 * (tid >> 6);
