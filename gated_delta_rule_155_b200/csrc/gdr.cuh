@@ -15,6 +15,19 @@ constexpr int ERR_PAGE_INDEX = kErrPageIndex;
 // where a gate is -inf.  NaN stays NaN.
 KDA_DEVICE float clamp_gate(float g) { return g < -128.0f ? -128.0f : g; }
 
+// Two fp32 operations an instruction (kernels that are short of issue slots, not of arithmetic).
+KDA_DEVICE void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1)
+{
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+KDA_DEVICE void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // Rows of sequence n (offsets clamped into [0, T]; cu == null: N sequences of T / N tokens).
 KDA_DEVICE SeqSpan span_of(const int *cu, int n, int N, int T)
 {

@@ -80,16 +80,17 @@ gdr_decode_kernel(GdrDecodeArgs a)
     }
     for (int t = 0;;) {
         const float alpha = __expf(clamp_gate(g));
-        float x[9] = {};                      // S^T k, S^T q of four columns, q.k
+        float x[9] = {}, kq = 0.0f;           // S^T k, S^T q of four columns, q.k
 #pragma unroll
-        for (int p = 0; p < R; ++p) {
+        for (int p = 0; p < R; ++p)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] += k[p] * s[p][j];
-                x[4 + j] += q[p] * s[p][j];
+            for (int j = 0; j < 4; j += 2) {
+                fma2(x[j], x[j + 1], k[p], k[p], s[p][j], s[p][j + 1], x[j], x[j + 1]);
+                fma2(x[4 + j], x[5 + j], q[p], q[p], s[p][j], s[p][j + 1], x[4 + j], x[5 + j]);
             }
-            x[8] += k[p] * q[p];
-        }
+#pragma unroll
+        for (int p = 0; p < R; p += 2) fma2(x[8], kq, k[p], k[p + 1], q[p], q[p + 1], x[8], kq);
+        x[8] += kq;
 #pragma unroll
         for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -104,7 +105,10 @@ gdr_decode_kernel(GdrDecodeArgs a)
 #pragma unroll
         for (int p = 0; p < R; ++p)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[p][j] = alpha * s[p][j] + k[p] * u[j];
+            for (int j = 0; j < 4; j += 2) {
+                mul2(s[p][j], s[p][j + 1], alpha, alpha, s[p][j], s[p][j + 1]);
+                fma2(s[p][j], s[p][j + 1], k[p], k[p], u[j], u[j + 1], s[p][j], s[p][j + 1]);
+            }
         if (++t == a.T) break;
         load_token(t);
     }

@@ -47,19 +47,6 @@ KDA_DEVICE void mbar_arrive(uint64_t *bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Two fp32 operations an instruction: the walks are short of issue slots, not of arithmetic.
-KDA_DEVICE void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1)
-{
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-KDA_DEVICE void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
-{
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 // x -> bf16 hi and lo, two values a word
 KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
 {
