@@ -4,7 +4,8 @@
 // prep, a block per chunk and value head: [K; Q] K^T in one M = 128 MMA (exact bf16 operands, fp32
 //   sums), the decays, M = (I + A)^-1 and P M in fp32 on CUDA cores; M and P M go to the workspace as
 //   one 128 x 64 operand [M; P M], split into bf16 hi + lo, in the 128-byte swizzle of the MMA's
-//   operand tiles, so the walk brings it in with one bulk copy.
+//   operand tiles, so the walk brings it in with one bulk copy.  765 us for 49152 chunks and heads (4 x 8192
+//   tokens of 96 heads), 75 us for 4224; shared memory bounds it (its data pipe is busy 78 % of the time).
 // walk, a block per sequence and value head: gdr_tc_walk.cuh.
 #include "gdr_tc_walk.cuh"
 

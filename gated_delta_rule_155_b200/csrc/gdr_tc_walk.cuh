@@ -14,6 +14,9 @@
 // the outputs under the state's product; one thread issues the MMAs, one the copies of the chunks to
 // come.  An M = 128 MMA takes about max(54, N / 2) cycles, so X and Q S, and U and P U, are one product
 // of N = 128 each: 36 MMAs a chunk.
+// A chunk takes about 5900 cycles: the MMAs 3560, the vector phases 1500, six hand-offs 850.  4 x 8192 tokens of
+// 96 heads (384 chains on 148 SMs): 1.20 ms; 8192 packed tokens of 32 heads, the longest 3001: 155 us.  A product
+// of two narrower halves that overlapped the state's split, with 60 MMAs a chunk, took 1.42 ms against 1.29.
 #pragma once
 
 #include "gdr_tc.cuh"
