@@ -775,3 +775,88 @@ def test_exponents_far_apart(kda):
     ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), [0, 200], f64(d["s0"]))
     near(out[0], ro, "bf16", False, "out")
     near(sT, rs, "bf16", False, "state", stored=False)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_a_batch_of_equal_lengths_is_the_packed_call(kda, io, dk):
+    """[B, T, ...] inputs, given buffers and a given workspace, gradients in place of d_final_state: the same bits
+    as the packed call with allocated ones."""
+    B, T, Hk, Hv = 3, 150, 2, 4
+    d = make(B * T, Hk, Hv, dk, dk, io, 100, B)
+    x = to(d, *NAMES, "dO")
+    s0, dS = d["s0"].cuda(), d["dS"].cuda()
+    cu = torch.tensor(cu_of([T] * B), dtype=torch.int32, device="cuda")
+    sT, d0 = torch.empty_like(s0), torch.empty_like(s0)
+    out, _ = kda.kda_gdr_forward(*x[:5], cu, s0, final_state=sT)
+    gr = kda.kda_gdr_backward(*x, cu, s0, dS, d_initial_state=d0)
+    y = [t.view(B, T, *t.shape[1:]) for t in x]
+    ws = [torch.empty(kda.kda_gdr_workspace_size(B, B * T, Hk, Hv, dk, dk, DT[io], backward=b), dtype=torch.uint8,
+                      device="cuda") for b in (False, True)]
+    out2, sT2 = torch.empty_like(y[2]), torch.empty_like(s0)
+    kda.kda_gdr_forward(*y[:5], None, s0, out2, sT2, workspace=ws[0])
+    both = dS.clone()
+    gr2 = kda.kda_gdr_backward(*y, None, s0, both, d_initial_state=both, workspace=ws[1])
+    kda.kda_check_device_error()
+    assert torch.equal(out, out2.view_as(out)) and torch.equal(sT, sT2) and torch.equal(both, d0)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(gr[n], gr2[n].view_as(gr[n])), n
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_gdr_forward(*y[:5], None, s0, out2, sT2, workspace=ws[0][:-1])
+    assert e.value.status == 6
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_gdr_backward(*y, None, s0, workspace=ws[1][16:])
+    assert e.value.status in (3, 6)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_decode_of_many_tokens_is_the_forward_pass(kda, io, dk):
+    N, T, Hk, Hv = 2, 70, 1, 2
+    d = make(N * T, Hk, Hv, dk, dk, io, 101, N)
+    x = [t.view(N, T, *t.shape[1:]) for t in to(d, *NAMES)]
+    state = d["s0"].cuda()
+    out = kda.kda_gdr_decode(*x, state)
+    sT = torch.empty_like(state)
+    fwd, _ = kda.kda_gdr_forward(*x, None, d["s0"].cuda(), final_state=sT)
+    kda.kda_check_device_error()
+    ro, rs = gdr.decode(*(f64(t) for t in x), f64(d["s0"]))
+    near(out, ro, io, True, "decode")
+    near(state, rs, io, True, "state", stored=False)
+    near(fwd, ro, io, io == "f32", "forward")
+    near(sT, rs, io, io == "f32", "forward's state", stored=False)
+
+
+def test_pages_with_nothing_to_do(kda):
+    """No ids, no table, no free page, no live page, a cache of one page: calls that change nothing, or only refs."""
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = torch.randn(2, 1, 8, device="cuda")
+    was = cache.clone()
+    none = i32()
+    refs = i32(0)
+    assert kda.kda_pages_fork(cache, refs, none).numel() == 0
+    kda.kda_pages_copy(cache, none, none)
+    kda.kda_pages_free(refs, none)
+    assert int(kda.kda_pages_compact(cache, refs)) == 0 and torch.equal(cache, was) and refs.tolist() == [0]
+    assert kda.kda_pages_fork(cache, refs, i32(-1, -1)).tolist() == [0, -1]
+    assert not bool(cache.any()) and refs.tolist() == [1]
+    assert kda.kda_pages_fork(cache, refs, i32(0)).tolist() == [-1]           # no page left: no error
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    assert int(kda.kda_pages_compact(cache, refs, table)) == 1 and bool((table == -1).all())
+    kda.kda_check_device_error()
+
+
+def test_many_key_heads(kda):
+    """More heads than SMs, one token each, and a group of five value heads."""
+    d = make(3, 150, 150, 128, 128, "bf16", 102, 3)
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    sT = torch.empty_like(d["s0"], device="cuda")
+    out, _ = kda.kda_gdr_forward(*to(d, *NAMES), cu, d["s0"].cuda(), final_state=sT)
+    ro, rs = gdr.forward(*(f64(d[n]) for n in NAMES), [0, 1, 2, 3], f64(d["s0"]))
+    near(out, ro, "bf16", False, "out")
+    near(sT, rs, "bf16", False, "state", stored=False)
+    for io, dk in (("bf16", 128), ("f32", 64)):
+        d = make(90, 1, 5, dk, dk, io, 103)
+        gr = kda.kda_gdr_backward(*(t[None] for t in to(d, *NAMES, "dO")))
+        ref = gdr.backward(*(f64(d[n]) for n in NAMES), [0, 90], f64(d["dO"]))
+        for n in ("dq", "dk", "dg", "dbeta"):
+            near_grad(gr[n][0], ref[n], io, io == "f32", n)
+    kda.kda_check_device_error()
