@@ -5,8 +5,9 @@
 Each ``csrc/*.cu`` is compiled separately (in parallel) with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` and linked into
 ``gated_delta_rule_155_b200/libkda.so`` (CUDA runtime linked statically).
-Objects go to ``_build/`` at the repository root.  A rebuild happens only when a
-source or header is newer than the library.
+Objects go to ``_build/`` at the repository root.  ``csrc/calls.cpp``, the binding's short
+calls, is compiled with g++ against torch's headers into the extension module ``_calls.so``.
+A rebuild happens only when a source or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -53,7 +55,35 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _newer(lib, deps) -> bool:
+    return os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps)
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and _newer(CALLS, [src, os.path.join(INCLUDE, "kda.h")]):
+        return CALLS
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(root, "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, jobs: int = 0, verbose: bool = False, extra=()) -> str:
+    build_calls(force, verbose)
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)

@@ -3,7 +3,9 @@
 Every function here has the name of the C entry point it calls (``include/kda.h``)
 and takes torch tensors that live on the GPU; each one checks shapes, dtypes and
 contiguity, passes raw device pointers and the current CUDA stream, and raises
-:class:`KdaError` on a non-OK status.  All computation happens in the library's
+:class:`KdaError` on a non-OK status.  The calls whose kernels take a few microseconds go
+through ``_calls.so`` (``csrc/calls.cpp``), which does the same for well-formed arguments in
+C++; every other argument comes back here to be named in an error.  All computation happens in the library's
 CUDA kernels.  There is no fallback: if ``libkda.so`` is missing or fails to load,
 importing this module raises.
 """
@@ -88,6 +90,22 @@ def _load():
 
 _lib = _load()
 
+
+def _load_calls():
+    try:
+        from gated_delta_rule_155_b200 import _calls
+    except ImportError as e:
+        raise ImportError(f"_calls.so does not load ({e}); build it with `python -m gated_delta_rule_155_b200.build`") from e
+    names = ("kda_gdr_decode", "kda_gdr_workspace_size", "kda_gdr_forward", "kda_pages_fork", "kda_pages_free",
+             "kda_pages_workspace_size", "kda_pages_compact")
+    _calls.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names))
+    return _calls
+
+
+# The calls whose kernels take a few microseconds, in C++: None where an argument is not well-formed (the
+# Python function then checks them one by one and raises), a status where the library refuses.
+_calls = _load_calls()
+
 EXPORTED_SYMBOLS = ("kda_status_string", "kda_abi_version", "kda_forward_chunked",
                     "kda_decode_step", "kda_layer_workspace_size", "kda_layer_forward",
                     "kda_layer_forward_noalloc", "kda_layer_decode_step", "kda_forward_chunked_varlen",
@@ -130,6 +148,20 @@ def _io_code(dtype):
     if code is None:
         raise TypeError(f"unsupported io dtype {dtype}")
     return code
+
+
+def _taken(r, where):
+    if r.__class__ is int:
+        raise KdaError(r, where)
+    return r
+
+
+def _on(stream, *tensors):
+    """What was allocated on the current stream and is used on `stream` is kept until that use is over."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _check(status, where):
@@ -488,6 +520,10 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
     [P, Hv, dk, dv] with an int32 index [N] (initial: -1 starts from zeros; final: -1 is not kept; the
     two buffers have the same number of pages).  ``workspace`` (a uint8 CUDA tensor of
     kda_gdr_workspace_size bytes) is allocated with torch when not given.  Returns (out, final_state)."""
+    if stream is None and workspace is None:
+        r = _calls.gdr_forward(q, k, v, g, beta, cu_seqlens, initial_state, out, final_state, initial_index, final_index)
+        if r is not None:
+            return _taken(r, "kda_gdr_forward"), final_state
     N, Tt, Hk, Hv, dk, dv, lead = _gdr_shapes(q, k, v, g, beta, cu_seqlens)
     p0 = _paged_state(initial_state, initial_index, N, (Hv, dk, dv), "initial")
     p1 = _paged_state(final_state, final_index, N, (Hv, dk, dv), "final")
@@ -503,6 +539,7 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(initial_index), _ptr(out),
         _ptr(final_state), _ptr(final_index), max(p0, p1), _ptr(cu_seqlens), _ptr(workspace), _ws_bytes(workspace),
         N, Tt, Hk, Hv, dk, dv, _io_code(q.dtype), _stream(stream)), "kda_gdr_forward")
+    _on(stream, out, workspace)
     return out, final_state
 
 
@@ -529,6 +566,7 @@ def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=Non
         _ptr(d_final_state), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]), _ptr(gr["dg"]), _ptr(gr["dbeta"]),
         _ptr(d_initial_state), _ptr(workspace), _ws_bytes(workspace), N, Tt, Hk, Hv, dk, dv, _io_code(q.dtype),
         _stream(stream)), "kda_gdr_backward")
+    _on(stream, workspace, *gr.values())
     gr["d_initial_state"] = d_initial_state
     return gr
 
@@ -537,6 +575,10 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
     """One or a few tokens per sequence, states updated in place.  q, k: [N, T, Hk, dk]; v: [N, T, Hv, dv];
     g, beta: [N, T, Hv], or all without T for one token; state: fp32 [N, Hv, dk, dv], or pages
     [P, Hv, dk, dv] with ``index`` int32 [N] (-1: an idle row, whose out is left alone).  Returns out."""
+    if stream is None:
+        r = _calls.gdr_decode(q, k, v, g, beta, state, index, out)
+        if r is not None:
+            return _taken(r, "kda_gdr_decode")
     sq, sv, io = q.shape, v.shape, q.dtype
     if len(sq) == 4 and len(sv) == 4:
         N, T, Hk, dk = sq
@@ -563,6 +605,7 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
                              idx, P, out.data_ptr(), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream))
     if st:
         raise KdaError(st, "kda_gdr_decode")
+    _on(stream, out)
     return out
 
 
@@ -586,6 +629,10 @@ def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
     """A free page for each of ``parents`` (int32 [n]), lowest first, with the parent's contents in every
     layer of ``cache`` [L, P, ...] (zeros for -1); ``refs`` (int32 [P]) of the new pages become 1.
     Returns their numbers, int32 [n]: -1 where no page is left or the parent is not live."""
+    if stream is None and children is None:
+        r = _calls.pages_fork(cache, refs, parents)
+        if r is not None:
+            return _taken(r, "kda_pages_fork")
     L, P, nbytes = _cache(cache)
     n = _ids(parents, "parents")
     if children is None:
@@ -593,6 +640,7 @@ def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
     _need_all(((refs, (P,), torch.int32, "refs"), (children, (n,), torch.int32, "children")))
     _check(_lib.kda_pages_fork(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(parents), _ptr(children), n, _stream(stream)),
            "kda_pages_fork")
+    _on(stream, children)
     return children
 
 
@@ -606,6 +654,11 @@ def kda_pages_copy(cache, src, dst, *, stream=None):
 
 def kda_pages_free(refs, ids, *, stream=None):
     """One holder less for each page of ``ids`` (int32 [n], -1: nothing); a page is free at refs 0."""
+    if stream is None:
+        r = _calls.pages_free(refs, ids)
+        if r is not None:
+            _taken(r, "kda_pages_free")
+            return
     n = _ids(ids, "ids")
     P = _ids(refs, "refs")
     _check(_lib.kda_pages_free(_ptr(refs), P, _ptr(ids), n, _stream(stream)), "kda_pages_free")
@@ -621,6 +674,10 @@ def kda_pages_workspace_size(pages):
 def kda_pages_compact(cache, refs, table=None, live=None, *, workspace=None, stream=None):
     """Moves the live pages of ``cache`` [L, P, ...] to the lowest numbers, ``refs`` (int32 [P]) with them,
     and renumbers ``table`` (int32, any page numbers, -1 stays) in place.  Returns their count, int32 [1]."""
+    if stream is None and live is None and workspace is None:
+        r = _calls.pages_compact(cache, refs, table)
+        if r is not None:
+            return _taken(r, "kda_pages_compact")
     L, P, nbytes = _cache(cache)
     _need_all(((refs, (P,), torch.int32, "refs"),))
     n = 0
@@ -635,6 +692,7 @@ def kda_pages_compact(cache, refs, table=None, live=None, *, workspace=None, str
         workspace = _workspace(kda_pages_workspace_size(P), cache.device)
     _check(_lib.kda_pages_compact(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(table), n, _ptr(live), _ptr(workspace),
                                   _ws_bytes(workspace), _stream(stream)), "kda_pages_compact")
+    _on(stream, live, workspace)
     return live
 
 

@@ -860,3 +860,60 @@ def test_many_key_heads(kda):
         for n in ("dq", "dk", "dg", "dbeta"):
             near_grad(gr[n][0], ref[n], io, io == "f32", n)
     kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_a_call_on_a_given_stream_keeps_what_it_allocated(kda, io, dk):
+    """The workspace and outputs of a call on another stream are not handed out again while it runs."""
+    d = make(6000, 1, 2, dk, dk, io, 110)
+    x = [t[None] for t in to(d, *NAMES, "dO")]
+    want = kda.kda_gdr_forward(*x[:5])[0]
+    grads = kda.kda_gdr_backward(*x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sizes = [kda.kda_gdr_workspace_size(1, 6000, 1, 2, dk, dk, DT[io], backward=b) for b in (False, True)]
+    torch.cuda.synchronize()
+    out = kda.kda_gdr_forward(*x[:5], stream=s)[0]
+    gr = kda.kda_gdr_backward(*x, stream=s)
+    for _ in range(20):
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    kda.kda_check_device_error()
+    assert torch.equal(out, want)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(gr[n], grads[n]), n
+
+
+def test_short_calls_answer_as_the_checked_ones(kda):
+    """The marshalling in C++ takes what the Python checks take and nothing else: its results and its refusals."""
+    d = make(12, 2, 4, 64, 64, "f32", 111, 3)
+    x = to(d, *NAMES)
+    cu = torch.tensor([0, 5, 5, 12], dtype=torch.int32, device="cuda")
+    s0 = d["s0"].cuda()
+    cur = torch.cuda.current_stream()
+    for init, ii, fi in ((None, None, None), (s0, None, None), (s0, cu[:3].contiguous(), None)):
+        ii = None if ii is None else torch.tensor([2, 0, -1], dtype=torch.int32, device="cuda")
+        sT = torch.empty_like(s0)
+        a, _ = kda.kda_gdr_forward(*x, cu, init, None, sT, initial_index=ii)
+        tT = torch.empty_like(s0)
+        b, _ = kda.kda_gdr_forward(*x, cu, init, None, tT, initial_index=ii, stream=cur)
+        assert torch.equal(a, b) and torch.equal(sT, tT)
+    y = [t[:3].clone() for t in x]
+    st = [s0.clone() for _ in range(2)]
+    assert torch.equal(kda.kda_gdr_decode(*y, st[0]), kda.kda_gdr_decode(*y, st[1], stream=cur)) and torch.equal(*st)
+    for bad in (x[:1] + x[:1] + x[1:4], [x[0], x[1], x[2], x[3][:, :3], x[4]], [x[0], x[1], x[2].bfloat16(), x[3], x[4]],
+                [x[0].cpu(), *x[1:]], [x[0], x[1], x[2].transpose(0, 1).contiguous().transpose(0, 1), x[3], x[4]]):
+        with pytest.raises((ValueError, TypeError)):
+            kda.kda_gdr_forward(*bad, cu)
+        with pytest.raises((ValueError, TypeError)):
+            kda.kda_gdr_decode(*(t[:3] for t in bad), s0)
+    with pytest.raises(TypeError):
+        kda.kda_gdr_decode(*(t[:3].half() for t in x), s0)
+    with pytest.raises(kda.KdaError):                       # 48 channels: the library's own refusal
+        kda.kda_gdr_decode(*(t[:3, :, :48].clone() for t in x[:3]), *(t[:3].clone() for t in x[3:]),
+                           torch.zeros(3, 4, 48, 48, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.kda_pages_free(cu.long(), cu)
+    with pytest.raises(ValueError):
+        kda.kda_pages_compact(torch.zeros(1, 4, 4, device="cuda"), cu, cu.float())
