@@ -59,6 +59,19 @@ kda_status_t check_pages(const void *cache, size_t page_bytes, int layers, int p
     if ((uintptr_t)cache & 15u) return KDA_ERR_MISALIGNED;
     return KDA_OK;
 }
+// whether a buffer that is written is also one that is read, or is written twice
+bool shared(std::initializer_list<const void *> written, std::initializer_list<const void *> read)
+{
+    for (auto w = written.begin(); w != written.end(); ++w) {
+        if (!*w) continue;
+        for (const void *r : read)
+            if (*w == r) return true;
+        for (auto x = written.begin(); x != w; ++x)
+            if (*w == *x) return true;
+    }
+    return false;
+}
+bool meet(const int *a, const int *b, int n) { return a < b + n && b < a + n; }
 bool misaligned4(std::initializer_list<const void *> ptrs)
 {
     for (const void *p : ptrs)
@@ -97,6 +110,7 @@ kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const 
         return KDA_ERR_MISALIGNED;
     st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, false));
     if (st != KDA_OK) return st;
+    if (T_total > 0 && shared({out}, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, initial_index, out, final_state, final_index, pages, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word()};
     if (on_tensor_cores(dk, dv, io)) {
@@ -121,6 +135,7 @@ kda_status_t kda_gdr_backward(const void *q, const void *k, const void *v, const
         return KDA_ERR_MISALIGNED;
     st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, true));
     if (st != KDA_OK) return st;
+    if (T_total > 0 && shared({d_q, d_k, d_v, d_g, d_beta}, {q, k, v, g, beta, d_out})) return KDA_ERR_INVALID_ARG;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, nullptr, nullptr, nullptr, nullptr, 0, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word(),
                    d_out, d_final_state, d_q, d_k, d_v, d_g, d_beta, d_initial_state};
@@ -141,6 +156,7 @@ kda_status_t kda_gdr_decode(const void *q, const void *k, const void *v, const v
     if (T < 1 || any_null({q, k, v, g, beta, state, out})) return KDA_ERR_INVALID_ARG;
     if (index && pages < 1) return KDA_ERR_INVALID_ARG;
     if (misaligned({q, k, v, g, beta, state, out}) || misaligned4({index})) return KDA_ERR_MISALIGNED;
+    if (shared({out}, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
     kda::GdrDecodeArgs a{q, k, v, g, beta, state, index, pages, out, N, T, Hk, Hv, dk, dv, io_of(io),
                          kda::device_error_word()};
     return cuda_status(kda::launch_gdr_decode(a, (cudaStream_t)stream));
@@ -154,6 +170,7 @@ kda_status_t kda_pages_fork(void *cache, size_t page_bytes, int layers, int page
     if (!refs || (n > 0 && any_null({parents, children}))) return KDA_ERR_INVALID_ARG;
     if (misaligned4({refs, parents, children})) return KDA_ERR_MISALIGNED;
     if (n == 0) return KDA_OK;
+    if (meet(children, parents, n)) return KDA_ERR_INVALID_ARG;   // written before the copies read the parents
     kda::PagesArgs a{cache, page_bytes, layers, pages, kda::device_error_word()};
     return cuda_status(kda::launch_pages_fork(a, refs, parents, children, n, (cudaStream_t)stream));
 }

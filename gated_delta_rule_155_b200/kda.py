@@ -487,7 +487,10 @@ def _workspace(need, device):
 
 
 def _ws_bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is None:
+        return 0
+    _need_all(((workspace, workspace.shape, torch.uint8, "workspace"),))
+    return workspace.numel()
 
 
 def _paged_state(state, index, N, tail, name):

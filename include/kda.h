@@ -315,6 +315,8 @@ kda_status_t kda_layer_decode_step(const void *q_raw, const void *k_raw, const v
  * fp32 sums, so states and out carry about 2^-16 relative error before out's own rounding.
  * The other shapes run exact fp32 CUDA-core kernels.  A g below -128 (-inf among them) acts as
  * a full reset, which exp(g) = 0 is; NaN inputs reach their own head's values and no other's.
+ * A buffer that is written shares no memory with another argument unless it says so here (the
+ * same pointer is refused: KDA_ERR_INVALID_ARG).
  */
 
 /*
@@ -392,7 +394,7 @@ kda_status_t kda_gdr_decode(const void *q, const void *k, const void *v, const v
  * kda_pages_fork: for each i < n a free page, lowest first, with the contents of page
  * parents[i] in every layer (zeros for parents[i] = -1); children[i] receives its number and its
  * refs becomes 1.  children[i] = -1 where parents[i] is not a live page (its free page stays
- * free), and, without an error, where no free page is left.
+ * free), and, without an error, where no free page is left.  children may not overlap parents.
  */
 kda_status_t kda_pages_fork(void *cache, size_t page_bytes, int layers, int pages, int *refs, const int *parents,
                             int *children, int n, kda_stream_t stream);

@@ -143,3 +143,28 @@ def test_workspace_sizes(lib):
 
 def test_status_string_of_bad_pages(lib):
     assert b"page" in lib.kda_status_string(7)
+
+
+def test_shared_buffers_are_refused(lib):
+    """Written buffers that are inputs, or two of which are one."""
+    other = [P(0x200000 + 0x10000 * i) for i in range(12)]
+
+    def forward(out):
+        return lib.kda_gdr_forward(*other[:5], None, None, out, None, None, 0, None, A, 1 << 50, 2, 64, 2, 4, 128, 128, 0, None)
+
+    def backward(outs):
+        return lib.kda_gdr_backward(*other[:5], None, None, other[5], None, *outs, None, A, 1 << 50, 2, 64, 2, 4, 128, 128, 1, None)
+
+    def decode(out):
+        return lib.kda_gdr_decode(*other[:5], A, None, 0, out, 2, 1, 2, 4, 128, 128, 1, None)
+    for i in range(5):
+        assert forward(other[i]) == INVALID and decode(other[i]) == INVALID
+        for j in range(6):
+            outs = other[6:11]
+            outs[i] = other[j]
+            assert backward(outs) == INVALID
+        outs = other[6:11]
+        outs[i] = other[6 + (i + 1) % 5]
+        assert backward(outs) == INVALID
+    for at in (0x300000, 0x300008, 0x2ffff8):           # the same ids, or some of them
+        assert lib.kda_pages_fork(A, 64, 2, 5, A, P(0x300000), P(at), 3, None) == INVALID

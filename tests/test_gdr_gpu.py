@@ -917,3 +917,20 @@ def test_short_calls_answer_as_the_checked_ones(kda):
         kda.kda_pages_free(cu.long(), cu)
     with pytest.raises(ValueError):
         kda.kda_pages_compact(torch.zeros(1, 4, 4, device="cuda"), cu, cu.float())
+
+
+def test_workspaces_that_are_none(kda):
+    """A workspace on the host, of another type or of strided bytes is refused before a kernel sees it."""
+    d = make(10, 2, 2, 64, 64, "f32", 43)
+    x = to(d, *NAMES)
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    need = kda.kda_gdr_workspace_size(1, 10, 2, 2, 64, 64, torch.float32, backward=True)
+    cache, refs = torch.zeros(2, 3, 4, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.float32, device="cuda"),
+               torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            kda.kda_gdr_forward(*x, cu, workspace=ws)
+        with pytest.raises(ValueError):
+            kda.kda_gdr_backward(*x, torch.ones_like(x[2]), cu, workspace=ws)
+        with pytest.raises(ValueError):
+            kda.kda_pages_compact(cache, refs, workspace=ws)
