@@ -7,6 +7,23 @@
 namespace kda {
 namespace gdr {
 
+// Launches fn behind what is on the stream, its blocks brought up while that ends (see follow).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*fn)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, const Args &...args)
+{
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 constexpr int CH = 64;              // chunk length
 constexpr int ERR_PAGE_INDEX = kErrPageIndex;
 
@@ -14,6 +31,13 @@ constexpr int ERR_PAGE_INDEX = kErrPageIndex;
 // every decay that contains it, so the clamp changes no result; it keeps differences of sums finite
 // where a gate is -inf.  NaN stays NaN.
 KDA_DEVICE float clamp_gate(float g) { return g < -128.0f ? -128.0f : g; }
+
+// The first words of every kernel here, launched by launch_after: it may be on the GPU before the kernel it follows
+// has ended, and goes no further until that one's writes can be seen.  Every block waits, those with nothing
+// to do too, so that the end of a kernel is the end of all before it.  No kernel lets its follower come before its
+// own end (griddepcontrol.launch_dependents): blocks placed among those of a running kernel end up unevenly, and
+// the walks lost more by that than the earlier start gave (8192 tokens backward 529 us against 513).
+KDA_DEVICE void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Two fp32 operations an instruction (kernels that are short of issue slots, not of arithmetic).
 KDA_DEVICE void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1)

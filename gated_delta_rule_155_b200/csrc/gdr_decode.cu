@@ -48,6 +48,7 @@ template <typename IO, int DK>
 __global__ void __launch_bounds__(NT, MINB)
 gdr_decode_kernel(GdrDecodeArgs a)
 {
+    follow();
     constexpr int R = DK * LPR / 32;                // rows of a lane
     const int slices = a.dv / COLS;
     const int n = blockIdx.x / slices, hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
@@ -121,12 +122,9 @@ gdr_decode_kernel(GdrDecodeArgs a)
 cudaError_t launch_gdr_decode(const GdrDecodeArgs &a, cudaStream_t s)
 {
     const dim3 grid((unsigned)a.N * (a.dv / COLS), a.Hv);
-    if (a.io == IO_BF16)
-        a.dk == 128 ? gdr_decode_kernel<__nv_bfloat16, 128><<<grid, NT, 0, s>>>(a)
-                    : gdr_decode_kernel<__nv_bfloat16, 64><<<grid, NT, 0, s>>>(a);
-    else
-        a.dk == 128 ? gdr_decode_kernel<float, 128><<<grid, NT, 0, s>>>(a) : gdr_decode_kernel<float, 64><<<grid, NT, 0, s>>>(a);
-    return cudaGetLastError();
+    const auto fn = a.io == IO_BF16 ? (a.dk == 128 ? gdr_decode_kernel<__nv_bfloat16, 128> : gdr_decode_kernel<__nv_bfloat16, 64>)
+                                    : (a.dk == 128 ? gdr_decode_kernel<float, 128> : gdr_decode_kernel<float, 64>);
+    return launch_after(fn, grid, NT, 0, s, a);
 }
 
 }  // namespace kda

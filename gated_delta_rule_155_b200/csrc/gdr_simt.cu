@@ -177,6 +177,7 @@ KDA_DEVICE void mm(float (&acc)[NTL][4], int k0, int k1, const float *A, int ar,
 template <typename IO, int DK>
 __global__ void __launch_bounds__(NT) gdr_prep_simt_kernel(P p)
 {
+    follow();
     const GdrArgs &a = p.a;
     int n, c;
     SeqSpan span;
@@ -530,12 +531,14 @@ KDA_DEVICE void walk_reverse(const P &p, unsigned block)
 template <typename IO, int DK, int DV>
 __global__ void __launch_bounds__(WT) gdr_forward_simt_kernel(P p)
 {
+    follow();
     walk_forward<IO, DK, DV, false>(p, blockIdx.x);
 }
 // Both walks of the backward pass at once: neither reads what the other leaves.
 template <typename IO, int DK, int DV>
 __global__ void __launch_bounds__(WT) gdr_walks_simt_kernel(P p)
 {
+    follow();
     const unsigned half = gridDim.x / 2;
     if (blockIdx.x >= half) walk_forward<IO, DK, DV, true>(p, blockIdx.x - half);
     else walk_reverse<IO, DK, DV>(p, blockIdx.x);
@@ -554,6 +557,7 @@ KDA_DEVICE void load_item(float *dst, int ld, const float *src, int tid)   // 64
 template <typename IO, int DK, int DV>
 __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
 {
+    follow();
     const GdrArgs &a = p.a;
     int n, c;
     SeqSpan span;
@@ -775,6 +779,7 @@ __global__ void __launch_bounds__(NT) gdr_grads_simt_kernel(P p)
 template <typename IO, int DK>
 __global__ void __launch_bounds__(NT) gdr_group_sum_kernel(P p)
 {
+    follow();
     const GdrArgs &a = p.a;
     int n, c;
     SeqSpan span;
@@ -818,25 +823,25 @@ cudaError_t launch_all(const GdrArgs &a, bool backward, cudaStream_t s)
     cudaError_t e;
     if (a.T > 0) {
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_simt_kernel<IO, DK>, prep_bytes<DK>())) != cudaSuccess) return e;
-        gdr_prep_simt_kernel<IO, DK><<<dim3((unsigned)slots, a.Hv), NT, prep_bytes<DK>(), s>>>(p);
+        e = launch_after(gdr_prep_simt_kernel<IO, DK>, dim3((unsigned)slots, a.Hv), NT, prep_bytes<DK>(), s, p);
+        if (e != cudaSuccess) return e;
     }
     const dim3 chain((unsigned)a.N * (DV / NS), a.Hv);
     if (!backward) {
         auto fn = gdr_forward_simt_kernel<IO, DK, DV>;
         if ((e = smem_opt_in<TagF>((const void *)fn, FB)) != cudaSuccess) return e;
-        fn<<<chain, WT, FB, s>>>(p);
-        return cudaGetLastError();
+        return launch_after(fn, chain, WT, FB, s, p);
     }
     auto fn = gdr_walks_simt_kernel<IO, DK, DV>;
     if ((e = smem_opt_in<TagR>((const void *)fn, RB)) != cudaSuccess) return e;
-    fn<<<dim3(2 * chain.x, chain.y), WT, RB, s>>>(p);
+    if ((e = launch_after(fn, dim3(2 * chain.x, chain.y), WT, RB, s, p)) != cudaSuccess) return e;
     if (a.T > 0) {
         auto gr = gdr_grads_simt_kernel<IO, DK, DV>;
         if ((e = smem_opt_in<TagG>((const void *)gr, grads_bytes<DK, DV>())) != cudaSuccess) return e;
-        gr<<<dim3((unsigned)slots, a.Hv), NT, grads_bytes<DK, DV>(), s>>>(p);
-        if (a.Hv > a.Hk) gdr_group_sum_kernel<IO, DK><<<dim3((unsigned)slots, a.Hk), NT, 0, s>>>(p);
+        if ((e = launch_after(gr, dim3((unsigned)slots, a.Hv), NT, grads_bytes<DK, DV>(), s, p)) != cudaSuccess) return e;
+        if (a.Hv > a.Hk) return launch_after(gdr_group_sum_kernel<IO, DK>, dim3((unsigned)slots, a.Hk), NT, 0, s, p);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 template <typename IO>

@@ -42,6 +42,7 @@ KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
 __global__ void __launch_bounds__(PR_T, 6)
 gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
 {
+    follow();
     const GdrArgs &a = p.a;
     if (p.order && blockIdx.y == gridDim.y - 1) {       // the blocks behind the heads: the sequences' order
         order_sequences(p, blockIdx.x * (PR_T / 32) + (threadIdx.x >> 5), gridDim.x * (PR_T / 32), threadIdx.x & 31);
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, TcP p)
 {
+    follow();
     walk_forward<false>(tm_q, tm_k, tm_v, p, blockIdx.x);
 }
 
@@ -285,9 +287,9 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        gdr_prep_tc_kernel<<<dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), PR_T, PR_BYTES, s>>>(mq, mk, p);
+        return launch_after(gdr_prep_tc_kernel, dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), PR_T, PR_BYTES, s, mq, mk, p);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
@@ -299,8 +301,7 @@ cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
     cudaError_t e = launch_gdr_prep_tc(p, mq, mk, mv, s);
     if (e != cudaSuccess) return e;
     if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel, W_BYTES)) != cudaSuccess) return e;
-    gdr_walk_tc_kernel<<<(unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s>>>(mq, mk, mv, p);
-    return cudaGetLastError();
+    return launch_after(gdr_walk_tc_kernel, (unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s, mq, mk, mv, p);
 }
 
 }  // namespace kda

@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 gdr_walks_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, TcP p)
 {
+    follow();
     const unsigned half = gridDim.x / 2;
     if (blockIdx.x >= half) walk_forward<true>(tm_q, tm_k, tm_v, p, blockIdx.x - half);
     else walk_reverse(tm_q, tm_k, tm_do, p, blockIdx.x);
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 gdr_grads_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, TcP p)
 {
+    follow();
     const GdrArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -752,16 +754,17 @@ cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (a.T > 0 && !make_tile_map(&mo, a.dO, 1, a.T, a.Hv, CH)) return cudaErrorInvalidValue;
     if ((e = smem_opt_in<TagR>((const void *)gdr_walks_tc_kernel, W_KEEP_BYTES)) != cudaSuccess) return e;
-    gdr_walks_tc_kernel<<<(unsigned)(a.N * a.Hv) * 2, W_THREADS, W_KEEP_BYTES, s>>>(mq, mk, mv, mo, p);
+    if ((e = launch_after(gdr_walks_tc_kernel, (unsigned)(a.N * a.Hv) * 2, W_THREADS, W_KEEP_BYTES, s, mq, mk, mv, mo, p)) != cudaSuccess)
+        return e;
     if (a.T > 0) {
         if ((e = smem_opt_in<TagG>((const void *)gdr_grads_tc_kernel, GS_BYTES)) != cudaSuccess) return e;
         int dev = 0, sms = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         const long long work = gdr_slots(a.N, a.T) * a.Hk;
-        gdr_grads_tc_kernel<<<(unsigned)(work < sms ? work : sms), G_THREADS, GS_BYTES, s>>>(mq, mk, mv, mo, p);
+        return launch_after(gdr_grads_tc_kernel, (unsigned)(work < sms ? work : sms), G_THREADS, GS_BYTES, s, mq, mk, mv, mo, p);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace kda

@@ -10,7 +10,7 @@
 namespace kda {
 namespace {
 
-using gdr::ERR_PAGE_INDEX;
+using namespace gdr;
 
 constexpr int PT = 1024;            // plan block
 constexpr int CT = 256;             // copy block
@@ -46,6 +46,7 @@ KDA_DEVICE int block_prefix(int x, int &sum, int tid)
 __global__ void __launch_bounds__(PT) pages_fork_plan_kernel(int *refs, int pages, const int *parents, int *children, int n,
                                                              int *err)
 {
+    follow();
     const int tid = threadIdx.x;
     for (int i = tid; i < n; i += PT) {
         const int p = parents[i];
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(PT) pages_fork_plan_kernel(int *refs, int page
 __global__ void __launch_bounds__(PT) pages_compact_plan_kernel(int *refs, int pages, int *table, int n, int *live, int *map,
                                                                 int *from, int *to, int *count, int *err)
 {
+    follow();
     const int tid = threadIdx.x;
     int mine = 0, m;
     for (int p = tid; p < pages; p += PT) mine += refs[p] > 0;
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(PT) pages_compact_plan_kernel(int *refs, int p
 template <bool CHECK>
 __global__ void __launch_bounds__(CT) pages_copy_kernel(PagesArgs a, const int *src, const int *dst, int n, const int *count)
 {
+    follow();
     const int tid = threadIdx.x;
     if (count) n = min(n, *count);
     const long long pieces = (long long)((a.page_bytes + PIECE - 1) / PIECE);
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(CT) pages_copy_kernel(PagesArgs a, const int *
 
 __global__ void pages_free_kernel(int *refs, int pages, const int *ids, int n, int *err)
 {
+    follow();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
     const int p = ids[i];
@@ -194,22 +198,20 @@ unsigned copy_blocks(const PagesArgs &a, long long moves)
 
 cudaError_t launch_pages_fork(const PagesArgs &a, int *refs, const int *parents, int *children, int n, cudaStream_t s)
 {
-    pages_fork_plan_kernel<<<1, PT, 0, s>>>(refs, a.pages, parents, children, n, a.err);
+    const cudaError_t e = launch_after(pages_fork_plan_kernel, 1, PT, 0, s, refs, a.pages, parents, children, n, a.err);
+    if (e != cudaSuccess) return e;
     // every child is a page that was free, every parent one that was not: the pairs cannot meet
-    pages_copy_kernel<false><<<copy_blocks(a, n), CT, 0, s>>>(a, parents, children, n, nullptr);
-    return cudaGetLastError();
+    return launch_after(pages_copy_kernel<false>, copy_blocks(a, n), CT, 0, s, a, parents, children, n, nullptr);
 }
 
 cudaError_t launch_pages_copy(const PagesArgs &a, const int *src, const int *dst, int n, cudaStream_t s)
 {
-    pages_copy_kernel<true><<<copy_blocks(a, n), CT, 0, s>>>(a, src, dst, n, nullptr);
-    return cudaGetLastError();
+    return launch_after(pages_copy_kernel<true>, copy_blocks(a, n), CT, 0, s, a, src, dst, n, nullptr);
 }
 
 cudaError_t launch_pages_free(int *refs, int pages, const int *ids, int n, int *err, cudaStream_t s)
 {
-    pages_free_kernel<<<(n + 255) / 256, 256, 0, s>>>(refs, pages, ids, n, err);
-    return cudaGetLastError();
+    return launch_after(pages_free_kernel, (n + 255) / 256, 256, 0, s, refs, pages, ids, n, err);
 }
 
 // map [pages], from [pages / 2], to [pages / 2], count
@@ -218,10 +220,9 @@ size_t pages_compact_workspace(int pages) { return 4 * ((size_t)pages + 2 * (siz
 cudaError_t launch_pages_compact(const PagesArgs &a, int *refs, int *table, int n, int *live, void *ws, cudaStream_t s)
 {
     int *map = (int *)ws, *from = map + a.pages, *to = from + a.pages / 2, *count = to + a.pages / 2;
-    pages_compact_plan_kernel<<<1, PT, 0, s>>>(refs, a.pages, table, n, live, map, from, to, count, a.err);
-    if (a.pages >= 2)
-        pages_copy_kernel<false><<<copy_blocks(a, a.pages / 2), CT, 0, s>>>(a, from, to, a.pages / 2, count);
-    return cudaGetLastError();
+    const cudaError_t e = launch_after(pages_compact_plan_kernel, 1, PT, 0, s, refs, a.pages, table, n, live, map, from, to, count, a.err);
+    if (e != cudaSuccess || a.pages < 2) return e;
+    return launch_after(pages_copy_kernel<false>, copy_blocks(a, a.pages / 2), CT, 0, s, a, from, to, a.pages / 2, count);
 }
 
 }  // namespace kda

@@ -934,3 +934,55 @@ def test_workspaces_that_are_none(kda):
             kda.kda_gdr_backward(*x, torch.ones_like(x[2]), cu, workspace=ws)
         with pytest.raises(ValueError):
             kda.kda_pages_compact(cache, refs, workspace=ws)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_in_a_row_follow_one_another(kda, io, dk, captured):
+    """Each call's kernels are brought up while what is before them on the stream ends: a run of calls whose inputs
+    are written just before them, by torch and by each other, gives the bits of the run with a wait behind each step."""
+    N, T, Hk, Hv, R = 3, 70, 2, 4, 4
+    d = make(R * N * T, Hk, Hv, dk, dk, io, 95, N)
+    src = [t.view(R, N, T, *t.shape[1:]) for t in to(d, *NAMES)]
+    first, ids = d["s0"].cuda(), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    x, outs = [t[0].clone() for t in src], [torch.empty_like(src[2]) for _ in range(2)]
+    grads = [torch.empty_like(src[0]) for _ in range(2)]
+    pages, refs = torch.empty(1, 2 * N, Hv, dk, dk, device="cuda"), torch.empty(2 * N, dtype=torch.int32, device="cuda")
+
+    def run(step):
+        pages[0, :N].copy_(first)
+        refs.fill_(0)[:N].fill_(1)
+        kids = kda.kda_pages_fork(pages, refs, ids)
+        step()
+        for r in range(R):
+            for a, b in zip(x, src):
+                a.copy_(b[r])
+            step()
+            kda.kda_gdr_forward(*x, None, pages[0], outs[0][r], pages[0], initial_index=kids, final_index=kids)
+            step()
+            kda.kda_gdr_decode(*x, pages[0], kids, outs[1][r])
+            step()
+            gr = kda.kda_gdr_backward(*x, outs[1][r], None, pages[0, N:])
+            step()
+            grads[0][r].copy_(gr["dq"])
+            grads[1][r].copy_(gr["dk"])
+        return kids
+
+    def answer():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (*outs, *grads, pages)]
+    assert run(torch.cuda.synchronize).tolist() == [3, 4, 5]
+    want = answer()
+    for t in (*outs, *grads, pages):
+        t.zero_()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(lambda: None)
+        for _ in range(3):
+            graph.replay()
+    else:
+        for _ in range(3):
+            run(lambda: None)
+    assert all(torch.equal(a, b) for a, b in zip(answer(), want))
+    kda.kda_check_device_error()
