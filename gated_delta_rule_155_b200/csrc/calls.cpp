@@ -24,6 +24,7 @@ struct Entries {
     decltype(&kda_gdr_decode) decode;
     decltype(&kda_gdr_workspace_size) gdr_bytes;
     decltype(&kda_gdr_forward) forward;
+    decltype(&kda_gdr_backward) backward;
     decltype(&kda_pages_fork) fork;
     decltype(&kda_pages_free) free_;
     decltype(&kda_pages_workspace_size) pages_bytes;
@@ -112,6 +113,32 @@ PyObject *gdr_decode(PyObject *, PyObject *const *o, Py_ssize_t n)
     });
 }
 
+// The sizes of q, k, v, g, beta (a[0..4]), packed where cu is given; false where they do not fit together.
+struct Shape {
+    int64_t N, T, Hk, Hv, dk, dv;
+    kda_dtype_t io;
+    bool of(const Arg *a, const Arg &cu)
+    {
+        const at::Tensor &q = *a[0].t, &v = *a[2].t;
+        const bool packed = !cu.none;
+        const int64_t d = packed ? 3 : 4;
+        if (q.dim() != d || v.dim() != d || !io_type(q.scalar_type(), io)) return false;
+        const auto type = q.scalar_type();
+        N = T = q.size(0);
+        if (packed) {
+            if (cu.t->dim() != 1 || cu.t->size(0) < 2 || cu.t->scalar_type() != at::kInt) return false;
+            N = cu.t->size(0) - 1;
+        } else {
+            if (q.size(1) > 0x7fffffff) return false;
+            T = N * q.size(1);
+        }
+        Hk = q.size(d - 2), dk = q.size(d - 1), Hv = v.size(d - 2), dv = v.size(d - 1);
+        const int64_t s4[4] = {q.size(0), packed ? 0 : q.size(1), Hv, dv}, s3[3] = {q.size(0), Hv, dv}, g3[3] = {s4[0], s4[1], Hv}, g2[2] = {s4[0], Hv};
+        const at::IntArrayRef sv = packed ? at::IntArrayRef(s3) : at::IntArrayRef(s4), sg = packed ? at::IntArrayRef(g2) : at::IntArrayRef(g3);
+        return has(a[1], type, q.sizes()) && has(a[2], type, sv) && has(a[3], type, sg) && has(a[4], type, sg) && fits_int({N, T, Hk, Hv, dk, dv});
+    }
+};
+
 // q, k, v, g, beta, cu_seqlens, initial_state, out, final_state, initial_index, final_index -> out
 PyObject *gdr_forward(PyObject *, PyObject *const *o, Py_ssize_t n)
 {
@@ -121,25 +148,12 @@ PyObject *gdr_forward(PyObject *, PyObject *const *o, Py_ssize_t n)
         Arg a[11];
         for (int i = 0; i < 11; ++i)
             if (!take(o[i], dev, a[i]) || (i < 5 && a[i].none)) Py_RETURN_NONE;
-        const at::Tensor &q = *a[0].t, &v = *a[2].t;
-        const bool packed = !a[5].none;
-        const int64_t d = packed ? 3 : 4;
-        kda_dtype_t io;
-        if (q.dim() != d || v.dim() != d || !io_type(q.scalar_type(), io)) Py_RETURN_NONE;
-        const auto type = q.scalar_type();
-        int64_t N = q.size(0), T = N;
-        if (packed) {
-            if (a[5].t->dim() != 1 || a[5].t->size(0) < 2 || a[5].t->scalar_type() != at::kInt) Py_RETURN_NONE;
-            N = a[5].t->size(0) - 1;
-        } else {
-            if (q.size(1) > 0x7fffffff) Py_RETURN_NONE;
-            T = N * q.size(1);
-        }
-        const int64_t Hk = q.size(d - 2), dk = q.size(d - 1), Hv = v.size(d - 2), dv = v.size(d - 1);
-        const int64_t s4[4] = {q.size(0), packed ? 0 : q.size(1), Hv, dv}, s3[3] = {q.size(0), Hv, dv}, g3[3] = {s4[0], s4[1], Hv}, g2[2] = {s4[0], Hv};
-        const at::IntArrayRef sv = packed ? at::IntArrayRef(s3) : at::IntArrayRef(s4), sg = packed ? at::IntArrayRef(g2) : at::IntArrayRef(g3);
-        if (!has(a[1], type, q.sizes()) || !has(a[2], type, sv) || !has(a[3], type, sg) || !has(a[4], type, sg)) Py_RETURN_NONE;
-        if (!a[7].none && !has(a[7], type, sv)) Py_RETURN_NONE;
+        Shape x;
+        if (!x.of(a, a[5])) Py_RETURN_NONE;
+        const int64_t N = x.N, T = x.T, Hk = x.Hk, Hv = x.Hv, dk = x.dk, dv = x.dv;
+        const kda_dtype_t io = x.io;
+        const at::Tensor &v = *a[2].t;
+        if (!a[7].none && !has(a[7], v.scalar_type(), v.sizes())) Py_RETURN_NONE;
         int64_t pages = 0;
         for (int i = 0; i < 2; ++i) {          // initial, final: the state and its index
             const Arg &s = a[i ? 8 : 6], &x = a[i ? 10 : 9];
@@ -155,7 +169,7 @@ PyObject *gdr_forward(PyObject *, PyObject *const *o, Py_ssize_t n)
                 pages = P;
             }
         }
-        if (!fits_int({N, T, Hk, Hv, dk, dv, pages})) Py_RETURN_NONE;
+        if (!fits_int({pages})) Py_RETURN_NONE;
         size_t bytes = 0;
         if (lib.gdr_bytes((int)N, (int)T, (int)Hk, (int)Hv, (int)dk, (int)dv, io, 0, &bytes) != KDA_OK) Py_RETURN_NONE;
         at::Tensor out = a[7].none ? at::empty_like(v) : *a[7].t, ws;
@@ -169,6 +183,44 @@ PyObject *gdr_forward(PyObject *, PyObject *const *o, Py_ssize_t n)
             return o[7];
         }
         return THPVariable_Wrap(out);
+    });
+}
+
+// q, k, v, g, beta, d_out, cu_seqlens, initial_state, d_final_state, d_initial_state -> (dq, dk, dv, dg, dbeta)
+PyObject *gdr_backward(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    if (n != 10) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject * {
+        const int dev = c10::cuda::current_device();
+        Arg a[10];
+        for (int i = 0; i < 10; ++i)
+            if (!take(o[i], dev, a[i]) || (i < 6 && a[i].none)) Py_RETURN_NONE;
+        Shape x;
+        if (!x.of(a, a[6])) Py_RETURN_NONE;
+        const at::Tensor &v = *a[2].t;
+        if (!has(a[5], v.scalar_type(), v.sizes())) Py_RETURN_NONE;
+        for (int i = 7; i < 10; ++i)
+            if (!a[i].none && !has(a[i], at::kFloat, {x.N, x.Hv, x.dk, x.dv})) Py_RETURN_NONE;
+        const int N = (int)x.N, T = (int)x.T, Hk = (int)x.Hk, Hv = (int)x.Hv, dk = (int)x.dk, dv = (int)x.dv;
+        size_t bytes = 0;
+        if (lib.gdr_bytes(N, T, Hk, Hv, dk, dv, x.io, 1, &bytes) != KDA_OK) Py_RETURN_NONE;
+        at::Tensor d[5], ws;
+        for (int i = 0; i < 5; ++i) d[i] = at::empty_like(*a[i].t);
+        if (bytes) ws = at::empty({(int64_t)bytes}, v.options().dtype(at::kByte));
+        const kda_status_t st = lib.backward(ptr(a[0]), ptr(a[1]), ptr(a[2]), ptr(a[3]), ptr(a[4]), ptr<float>(a[7]), ptr<int>(a[6]), ptr(a[5]),
+                                             ptr<float>(a[8]), d[0].data_ptr(), d[1].data_ptr(), d[2].data_ptr(), d[3].data_ptr(), d[4].data_ptr(),
+                                             ptr<float>(a[9]), bytes ? ws.data_ptr() : nullptr, bytes, N, T, Hk, Hv, dk, dv, x.io, stream_of(dev));
+        if (st != KDA_OK) return PyLong_FromLong(st);
+        PyObject *r = PyTuple_New(5);
+        for (int i = 0; r && i < 5; ++i) {
+            PyObject *t = THPVariable_Wrap(d[i]);
+            if (!t) {
+                Py_DECREF(r);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(r, i, t);
+        }
+        return r;
     });
 }
 
@@ -261,7 +313,7 @@ PyObject *init(PyObject *, PyObject *const *o, Py_ssize_t n)
 }
 
 #define KDA_CALL(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {KDA_CALL(init),       KDA_CALL(gdr_decode), KDA_CALL(gdr_forward),   KDA_CALL(pages_fork),
+PyMethodDef methods[] = {KDA_CALL(init),       KDA_CALL(gdr_decode), KDA_CALL(gdr_forward), KDA_CALL(gdr_backward), KDA_CALL(pages_fork),
                          KDA_CALL(pages_free), KDA_CALL(pages_compact), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Short calls of the kda binding", -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -96,8 +96,8 @@ def _load_calls():
         from gated_delta_rule_155_b200 import _calls
     except ImportError as e:
         raise ImportError(f"_calls.so does not load ({e}); build it with `python -m gated_delta_rule_155_b200.build`") from e
-    names = ("kda_gdr_decode", "kda_gdr_workspace_size", "kda_gdr_forward", "kda_pages_fork", "kda_pages_free",
-             "kda_pages_workspace_size", "kda_pages_compact")
+    names = ("kda_gdr_decode", "kda_gdr_workspace_size", "kda_gdr_forward", "kda_gdr_backward", "kda_pages_fork",
+             "kda_pages_free", "kda_pages_workspace_size", "kda_pages_compact")
     _calls.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names))
     return _calls
 
@@ -551,6 +551,11 @@ def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=Non
     """Gradients of kda_gdr_forward (dense states).  Returns a dict dq, dk, dv, dg, dbeta (io dtype,
     shaped as the inputs) and d_initial_state (fp32, None unless a buffer is passed).  ``grads`` may
     hold preallocated outputs; ``workspace`` is allocated with torch when not given."""
+    if grads is None and stream is None and workspace is None:
+        r = _calls.gdr_backward(q, k, v, g, beta, d_out, cu_seqlens, initial_state, d_final_state, d_initial_state)
+        if r is not None:
+            dq, dk, dv, dg, db = _taken(r, "kda_gdr_backward")
+            return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": db, "d_initial_state": d_initial_state}
     N, Tt, Hk, Hv, dk, dv, lead = _gdr_shapes(q, k, v, g, beta, cu_seqlens)
     _need(d_out, lead + (Hv, dv), q.dtype, "d_out")
     for t, n in ((initial_state, "initial_state"), (d_final_state, "d_final_state"),

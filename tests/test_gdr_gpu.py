@@ -986,3 +986,29 @@ def test_calls_in_a_row_follow_one_another(kda, io, dk, captured):
             run(lambda: None)
     assert all(torch.equal(a, b) for a, b in zip(answer(), want))
     kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_short_backward_calls_answer_as_the_checked_ones(kda, io, dk):
+    """Packed and batched, with states and without, an empty sequence among them; and what both refuse."""
+    d = make(150, 1, 3, dk, dk, io, 112, 3)
+    x, do, s0, dT = to(d, *NAMES), d["v"].cuda().flip(0), d["s0"].cuda(), d["s0"].cuda().flip(0)
+    cu = torch.tensor([0, 80, 80, 150], dtype=torch.int32, device="cuda")
+    cur = torch.cuda.current_stream()
+    batch = [t.view(3, 50, *t.shape[1:]) for t in (*x, do)]
+    for ins, c in (([*x, do], cu), (batch, None)):
+        for states in ((None, None), (s0, None), (s0, dT)):
+            got = []
+            for stream in (None, cur):
+                first = torch.empty_like(s0) if states[0] is not None else None
+                got.append(kda.kda_gdr_backward(*ins, c, *states, d_initial_state=first, stream=stream))
+            assert list(got[0]) == list(got[1])
+            assert all(torch.equal(p, q) for p, q in zip(got[0].values(), got[1].values()) if p is not None)
+            assert got[0]["dq"].shape == ins[0].shape and got[0]["dg"].shape == ins[3].shape
+    for bad in ([*x, do[:-1]], [*x, do.cpu()], [*x[:3], x[3][:, :2], x[4], do], [x[0][:, :, :32], *x[1:], do]):
+        with pytest.raises(ValueError):
+            kda.kda_gdr_backward(*bad, cu)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_backward(*x, do, cu, s0[:2])
+    with pytest.raises(kda.KdaError):                       # 48 channels: the library's own refusal
+        kda.kda_gdr_backward(*(t[..., :48].clone() if t.dim() == 3 else t for t in x), do[..., :48].clone(), cu)
