@@ -22,6 +22,7 @@ constexpr int LM = 68, PR_T = 128;
 constexpr int PR_KQ = 0, PR_P = 0, PR_A = TILE, PR_MHL = PR_A, PR_G = 33 * 1024 + 512;
 constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
 static_assert(PR_A + 64 * LM * 4 <= PR_G && PR_MHL + TILE <= PR_G && 2 * TILE <= PR_G && PR_BYTES + 1024 <= 228 * 1024 / 6, "regions");
+static_assert(W_ALONE_BYTES + PR_BYTES > 228 * 1024 && W_ALONE_BYTES >= W_BYTES, "no prep beside a leading walk");
 
 // order[r] <- the sequence whose length is the r-th longest: the walks start with the longest.  A warp a sequence.
 KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
@@ -42,8 +43,12 @@ KDA_DEVICE void order_sequences(const TcP &p, int first, int step, int lane)
 __global__ void __launch_bounds__(PR_T, 6)
 gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TcP p)
 {
-    follow();
+    if (!p.beside) follow();
     const GdrArgs &a = p.a;
+    if (p.beside && blockIdx.y == gridDim.y - 1) {      // the end of this kernel is the end of all before it
+        if (blockIdx.x == 0) follow();
+        return;
+    }
     if (p.order && blockIdx.y == gridDim.y - 1) {       // the blocks behind the heads: the sequences' order
         order_sequences(p, blockIdx.x * (PR_T / 32) + (threadIdx.x >> 5), gridDim.x * (PR_T / 32), threadIdx.x & 31);
         return;
@@ -59,7 +64,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint32_t *tslot = (uint32_t *)(bars + 3);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.y, hk = hv / (a.Hv / a.Hk);
+    const int hv = p.head0 + blockIdx.y, hk = hv / (a.Hv / a.Hk);
     const int row0 = span.row0 + c * CH, valid = min(CH, span.len - c * CH);
     if (tid == 0) {
         mbar_init(&bars[0], 1);
@@ -237,11 +242,13 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // ---------------------------------------------------------------- the walk
+template <bool LEADS>
 __global__ void __launch_bounds__(W_THREADS, 1)
 gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, TcP p)
 {
     follow();
+    if (LEADS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the next prep's blocks may come
     walk_forward<false>(tm_q, tm_k, tm_v, p, blockIdx.x);
 }
 
@@ -264,6 +271,7 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
     const size_t items = (size_t)gdr_slots(a.N, a.T) * a.Hv;
     p = TcP{};
     p.a = a;
+    p.heads = a.Hv;
     p.items = (uint8_t *)a.ws;
     uint8_t *at = p.items + items * IT_BYTES;
     if (backward) {
@@ -287,21 +295,48 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        return launch_after(gdr_prep_tc_kernel, dim3((unsigned)gdr_slots(a.N, a.T), a.Hv + (p.order ? 1 : 0)), PR_T, PR_BYTES, s, mq, mk, p);
+        return launch_after(gdr_prep_tc_kernel, dim3((unsigned)gdr_slots(a.N, a.T), p.heads + (p.order || p.beside ? 1 : 0)), PR_T, PR_BYTES, s, mq, mk, p);
     }
     return cudaSuccess;
 }
 
+// Sequences of one length whose walks fill the SMs more than once but not evenly: the value heads that walk first,
+// few enough to leave SMs idle, so many that the others' walks fill the SMs evenly.  The others' prep runs beside them
+// on the idle SMs (not before, and not on the idle SMs of the last round, when nothing is left to do).  4 x 8192
+// tokens of 96 heads 1833 us (1955 in one prep and one walk), 2 x 4096 of 96 heads 459 (603), 2 x 512 of 96 heads 79
+// (93); where the idle SMs have fewer than 400 chunks' time, two launches more cost what it gives (2 x 128 of 96
+// heads 36.5 against 35.9).  0: all heads in one prep and one walk.
+static int leading_heads(const GdrArgs &a)
+{
+    int dev = 0, sms = 0;
+    if (a.cu || cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    const long long walks = (long long)a.N * a.Hv;
+    if (walks <= sms || walks % sms == 0) return 0;
+    const long long lead = (walks % sms + a.N - 1) / a.N, idle = sms - lead * a.N, chunks = (a.T / a.N + CH - 1) / CH;
+    return lead < a.Hv && idle > 0 && chunks * idle >= 400 ? (int)lead : 0;
+}
+
 cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
 {
-    struct TagW;
+    struct TagW; struct TagL;
     TcP p;
     CUtensorMap mq{}, mk{}, mv{};
     gdr_tc_plan(a, false, p);
-    cudaError_t e = launch_gdr_prep_tc(p, mq, mk, mv, s);
-    if (e != cudaSuccess) return e;
-    if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel, W_BYTES)) != cudaSuccess) return e;
-    return launch_after(gdr_walk_tc_kernel, (unsigned)(a.N * a.Hv), W_THREADS, W_BYTES, s, mq, mk, mv, p);
+    cudaError_t e;
+    if (const int lead = leading_heads(a)) {
+        p.heads = lead;
+        if ((e = launch_gdr_prep_tc(p, mq, mk, mv, s)) != cudaSuccess) return e;
+        if ((e = smem_opt_in<TagL>((const void *)gdr_walk_tc_kernel<true>, W_ALONE_BYTES)) != cudaSuccess) return e;
+        e = launch_after(gdr_walk_tc_kernel<true>, (unsigned)(a.N * lead), W_THREADS, W_ALONE_BYTES, s, mq, mk, mv, p);
+        if (e != cudaSuccess) return e;
+        p.head0 = lead;
+        p.heads = a.Hv - lead;
+        p.beside = true;
+    }
+    if ((e = launch_gdr_prep_tc(p, mq, mk, mv, s)) != cudaSuccess) return e;
+    if ((e = smem_opt_in<TagW>((const void *)gdr_walk_tc_kernel<false>, W_BYTES)) != cudaSuccess) return e;
+    return launch_after(gdr_walk_tc_kernel<false>, (unsigned)(a.N * p.heads), W_THREADS, W_BYTES, s, mq, mk, mv, p);
 }
 
 }  // namespace kda

@@ -27,6 +27,8 @@ struct TcP {
     uint8_t *items;
     int *order;              // sequences by length, longest first (null: as they are)
     uint8_t *S, *U, *dS, *H; // kept for the gradients, operand tiles of 2, 1, 2 and 1 TILE bytes an item
+    int head0, heads;        // the value heads of a launch of prep and forward walk
+    bool beside;             // prep: beside the walk before it in the stream
     unsigned long long wait_ns;
     int skip_load_chunk;
 };
@@ -88,6 +90,7 @@ constexpr unsigned long long DRAIN_NS = 2000000000ull;
 constexpr int ST_KQ = 0, ST_V = 2 * TILE, ST_MM = ST_V + TILE, ST_G = ST_MM + IT_GATES, ST_BYTES = ST_G + 1024;
 constexpr int STAGES = 2;
 constexpr int W_BAR = STAGES * ST_BYTES, W_BYTES = W_BAR + 256 + 1024;
+constexpr int W_ALONE_BYTES = 200 * 1024;   // of a walk that no block of prep fits beside (it would wait for tensor memory)
 // and, in the backward pass, what goes to the workspace: the state's tile (32 KB) and U's or H's (16 KB), each
 // stored by one bulk copy (as 16-byte pieces of 128-byte rows from the registers the walks took a fifth longer)
 constexpr int W_KEEP_S = W_BAR + 1024, W_KEEP_U = W_KEEP_S + 2 * TILE, W_KEEP_BYTES = W_KEEP_U + TILE + 1024;

@@ -40,8 +40,8 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
     uint32_t *tslot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = (int)(block % a.Hv), hk = hv / (a.Hv / a.Hk);
-    const int n = p.order ? p.order[block / a.Hv] : (int)(block / a.Hv);
+    const int hv = p.head0 + (int)(block % p.heads), hk = hv / (a.Hv / a.Hk);
+    const int n = p.order ? p.order[block / p.heads] : (int)(block / p.heads);
     const SeqSpan span = span_of(a.cu, n, a.N, a.T);
     const int nchunks = (span.len + CH - 1) / CH;
     const size_t item0 = (size_t)slot_base(span.row0, n);

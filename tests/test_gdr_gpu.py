@@ -1012,3 +1012,36 @@ def test_short_backward_calls_answer_as_the_checked_ones(kda, io, dk):
         kda.kda_gdr_backward(*x, do, cu, s0[:2])
     with pytest.raises(kda.KdaError):                       # 48 channels: the library's own refusal
         kda.kda_gdr_backward(*(t[..., :48].clone() if t.dim() == 3 else t for t in x), do[..., :48].clone(), cu)
+
+
+@pytest.mark.parametrize("N,T,Hk,Hv", [(2, 420, 16, 96), (3, 321, 50, 100), (1, 200, 1, 150), (5, 1024, 8, 32)])
+def test_a_batch_whose_heads_walk_in_two_parts(kda, N, T, Hk, Hv):
+    """More walks than SMs, of one length: some heads walk before the others' chunks are prepared.  The packed call,
+    which takes all heads at once, gives the same bits; states in pages, in place; twice over the same workspace."""
+    torch.manual_seed(113)
+    unit = torch.nn.functional.normalize
+    x = [unit(torch.randn(N, T, Hk, 128, device="cuda"), dim=-1).bfloat16() for _ in range(2)]
+    x += [torch.randn(N, T, Hv, 128, device="cuda").bfloat16(), -torch.rand(N, T, Hv, device="cuda").bfloat16(),
+          torch.rand(N, T, Hv, device="cuda").bfloat16()]
+    pages = torch.randn(N + 2, Hv, 128, 128, device="cuda")
+    start = torch.arange(N, 0, -1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kda.kda_gdr_workspace_size(N, N * T, Hk, Hv, 128, 128, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    cu = torch.arange(0, N * T + 1, T, dtype=torch.int32, device="cuda")
+    answers = []
+    for packed in (True, False, False):
+        p = pages.clone()
+        y = [t.flatten(0, 1) for t in x] if packed else x
+        ws.fill_(255)                              # NaN, were it read
+        out, _ = kda.kda_gdr_forward(*y, cu if packed else None, p, None, p, initial_index=start, final_index=start, workspace=ws)
+        answers.append((out.flatten(), p))
+    graph = torch.cuda.CUDAGraph()
+    p, out = pages.clone(), torch.empty_like(x[2])
+    with torch.cuda.graph(graph):
+        kda.kda_gdr_forward(*x, None, p, out, p, initial_index=start, final_index=start, workspace=ws)
+        out.add_(0)                                # a kernel behind, which reads all of it
+    p.copy_(pages)
+    graph.replay()
+    answers.append((out.flatten(), p))
+    kda.kda_check_device_error()
+    for a in answers[1:]:
+        assert torch.equal(a[0], answers[0][0]) and torch.equal(a[1], answers[0][1])
