@@ -7,6 +7,9 @@
 //   operand tiles, so the walk brings it in with one bulk copy.  765 us for 49152 chunks and heads (4 x 8192
 //   tokens of 96 heads), 75 us for 4224; shared memory bounds it (its data pipe is busy 78 % of the time).
 // walk, a block per sequence and value head: gdr_tc_walk.cuh.
+#include <algorithm>
+#include <climits>
+
 #include "gdr_tc_walk.cuh"
 
 namespace kda {
@@ -19,6 +22,7 @@ using namespace gdr;
 // place; later M's hi, lo) in their place.  36 KB and 128 threads, so that six blocks share an SM: a block is a
 // chain of short steps with a barrier behind each, and what one leaves idle the others use.
 constexpr int LM = 68, PR_T = 128;
+constexpr int SMS = 148;
 constexpr int PR_KQ = 0, PR_P = 0, PR_A = TILE, PR_MHL = PR_A, PR_G = 33 * 1024 + 512;
 constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
 static_assert(PR_A + 64 * LM * 4 <= PR_G && PR_MHL + TILE <= PR_G && 2 * TILE <= PR_G && PR_BYTES + 1024 <= 228 * 1024 / 6, "regions");
@@ -53,9 +57,18 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         order_sequences(p, blockIdx.x * (PR_T / 32) + (threadIdx.x >> 5), gridDim.x * (PR_T / 32), threadIdx.x & 31);
         return;
     }
-    int n, c;
+    int n, c, slot = blockIdx.x;
     SeqSpan span;
-    if (!find_slot(a.cu, a.N, a.T, blockIdx.x, n, c, span)) return;
+    if (!a.cu || a.N == 1) {                            // a sequence's chunks side by side
+        const int per = gridDim.x / a.N;
+        n = blockIdx.x / per;
+        c = p.chunk0 + (int)(blockIdx.x % per);
+        span = span_of(a.cu, n, a.N, a.T);
+        slot = slot_base(span.row0, n) + c;
+        if (c * CH >= span.len) return;
+    } else if (!find_slot(a.cu, a.N, a.T, slot, n, c, span) || c < p.chunk0 || c >= p.chunk1) {
+        return;
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     float *A = (float *)(sm + PR_A);
@@ -104,7 +117,7 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit(&bars[1]);
         }
     }
-    uint8_t *item = p.items + ((size_t)blockIdx.x * a.Hv + hv) * IT_BYTES;
+    uint8_t *item = p.items + ((size_t)slot * a.Hv + hv) * IT_BYTES;
     float *gates = (float *)(item + IT_GATES);
     if (warp == 1) {
         gate_sums(graw, ghi, glo, lane);
@@ -257,12 +270,28 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 bool gdr_tc_shape(int dk, int dv, IoType io) { return io == IO_BF16 && dk == D && dv == D; }
 bool gdr_tc_available() { return device_is_sm100() && tensor_maps_available(); }
 
-// items; then 1 KB aligned: for the gradients S, U, dS, H; the sequences' order
+// Walks that leave SMs idle: how many chunks of every sequence (of the mean length) to walk before the others are
+// prepared, which then runs beside them on the idle SMs; that takes about as long as those walks if prep costs
+// 1 / 205 of a walk's step a chunk and head on all SMs (15.6 ns, 3.2 us).  2 x 4096 tokens of 32 heads 238 us (267
+// in one prep and one walk), 32768 of 32 heads 1583 (1764), 4096 of 16 heads 208 (214); fewer than 600 chunks and
+// heads to prepare beside are not worth two launches more (512 tokens of 64 heads, 320: 46 us against 43; 1024 of 32
+// heads, 416: 67 against 66).  The states in between are fp32, so the parts give the bits of the whole.  0: all
+// chunks in one prep and one walk.
+static int early_chunks(int N, int T, int Hv)
+{
+    const long long walks = (long long)N * Hv, idle = SMS - walks, chunks = (T / N + CH - 1) / CH;
+    if (idle <= 0) return 0;
+    const long long early = (chunks * walks * SMS) / (205 * idle + walks * SMS) + 1;
+    return (chunks - early) * walks >= 600 ? (int)early : 0;
+}
+
+// items; then 1 KB aligned: for the gradients S, U, dS, H, or the states between two walks; the sequences' order
 size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
 {
     (void)Hk;
     const size_t items = (size_t)gdr_slots(N, T) * Hv;
-    return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + 4 * (size_t)N;
+    const size_t carry = !backward && early_chunks(N, T, Hv) ? (size_t)N * Hv * D * D * 4 : 0;
+    return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + carry + 4 * (size_t)N;
 }
 
 void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
@@ -272,6 +301,9 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
     p = TcP{};
     p.a = a;
     p.heads = a.Hv;
+    p.chunk1 = INT_MAX;
+    p.start = a.s0;
+    p.start_index = a.s0_index;
     p.items = (uint8_t *)a.ws;
     uint8_t *at = p.items + items * IT_BYTES;
     if (backward) {
@@ -279,6 +311,9 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
         p.dS = at; at += items * 2 * TILE;
         p.U = at; at += items * TILE;
         p.H = at; at += items * TILE;
+    } else if (early_chunks(a.N, a.T, a.Hv)) {
+        p.carry = (float *)at;
+        at += (size_t)a.N * a.Hv * D * D * 4;
     }
     if (a.T > 0 && a.cu && a.N > 1) p.order = (int *)at;
     p.wait_ns = hk.wait_ns;
@@ -295,7 +330,9 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
             !make_tile_map(&mv, a.v, 1, a.T, a.Hv, CH))
             return cudaErrorInvalidValue;
         if ((e = smem_opt_in<TagP>((const void *)gdr_prep_tc_kernel, PR_BYTES)) != cudaSuccess) return e;
-        return launch_after(gdr_prep_tc_kernel, dim3((unsigned)gdr_slots(a.N, a.T), p.heads + (p.order || p.beside ? 1 : 0)), PR_T, PR_BYTES, s, mq, mk, p);
+        const long long per = std::min<long long>(p.chunk1, ((a.cu ? a.T : a.T / a.N) + CH - 1) / CH) - p.chunk0;
+        const unsigned slots = (unsigned)(!a.cu || a.N == 1 ? a.N * per : gdr_slots(a.N, a.T));
+        return launch_after(gdr_prep_tc_kernel, dim3(slots, p.heads + (p.order || p.beside ? 1 : 0)), PR_T, PR_BYTES, s, mq, mk, p);
     }
     return cudaSuccess;
 }
@@ -308,12 +345,9 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
 // heads 36.5 against 35.9).  0: all heads in one prep and one walk.
 static int leading_heads(const GdrArgs &a)
 {
-    int dev = 0, sms = 0;
-    if (a.cu || cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
     const long long walks = (long long)a.N * a.Hv;
-    if (walks <= sms || walks % sms == 0) return 0;
-    const long long lead = (walks % sms + a.N - 1) / a.N, idle = sms - lead * a.N, chunks = (a.T / a.N + CH - 1) / CH;
+    if (a.cu || walks <= SMS || walks % SMS == 0) return 0;
+    const long long lead = (walks % SMS + a.N - 1) / a.N, idle = SMS - lead * a.N, chunks = (a.T / a.N + CH - 1) / CH;
     return lead < a.Hv && idle > 0 && chunks * idle >= 400 ? (int)lead : 0;
 }
 
@@ -324,14 +358,31 @@ cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s)
     CUtensorMap mq{}, mk{}, mv{};
     gdr_tc_plan(a, false, p);
     cudaError_t e;
-    if (const int lead = leading_heads(a)) {
-        p.heads = lead;
+    const int lead = leading_heads(a), early = early_chunks(a.N, a.T, a.Hv);
+    if (lead || early) {
+        if (lead) p.heads = lead;
+        if (early) {
+            p.chunk1 = early;
+            p.a.sT = p.carry;
+            p.a.sT_index = nullptr;
+            p.start = nullptr;
+        }
         if ((e = launch_gdr_prep_tc(p, mq, mk, mv, s)) != cudaSuccess) return e;
         if ((e = smem_opt_in<TagL>((const void *)gdr_walk_tc_kernel<true>, W_ALONE_BYTES)) != cudaSuccess) return e;
-        e = launch_after(gdr_walk_tc_kernel<true>, (unsigned)(a.N * lead), W_THREADS, W_ALONE_BYTES, s, mq, mk, mv, p);
+        e = launch_after(gdr_walk_tc_kernel<true>, (unsigned)(a.N * p.heads), W_THREADS, W_ALONE_BYTES, s, mq, mk, mv, p);
         if (e != cudaSuccess) return e;
-        p.head0 = lead;
-        p.heads = a.Hv - lead;
+        if (lead) {
+            p.head0 = lead;
+            p.heads = a.Hv - lead;
+        }
+        if (early) {
+            p.a = a;
+            p.a.s0 = p.carry;
+            p.a.s0_index = nullptr;
+            p.start = a.s0;
+            p.chunk0 = early;
+            p.chunk1 = INT_MAX;
+        }
         p.beside = true;
     }
     if ((e = launch_gdr_prep_tc(p, mq, mk, mv, s)) != cudaSuccess) return e;

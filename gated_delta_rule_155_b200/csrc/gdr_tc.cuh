@@ -26,8 +26,12 @@ struct TcP {
     GdrArgs a;
     uint8_t *items;
     int *order;              // sequences by length, longest first (null: as they are)
+    float *carry;            // the states between two walks of the forward pass
     uint8_t *S, *U, *dS, *H; // kept for the gradients, operand tiles of 2, 1, 2 and 1 TILE bytes an item
     int head0, heads;        // the value heads of a launch of prep and forward walk
+    int chunk0, chunk1;      // and its chunks of every sequence
+    const float *start;      // what the caller's sequences start from, for a walk that starts from another's states
+    const int *start_index;
     bool beside;             // prep: beside the walk before it in the stream
     unsigned long long wait_ns;
     int skip_load_chunk;

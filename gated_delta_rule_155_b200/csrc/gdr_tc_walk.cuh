@@ -42,9 +42,11 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hv = p.head0 + (int)(block % p.heads), hk = hv / (a.Hv / a.Hk);
     const int n = p.order ? p.order[block / p.heads] : (int)(block / p.heads);
-    const SeqSpan span = span_of(a.cu, n, a.N, a.T);
-    const int nchunks = (span.len + CH - 1) / CH;
-    const size_t item0 = (size_t)slot_base(span.row0, n);
+    SeqSpan span = span_of(a.cu, n, a.N, a.T);
+    const int all = (span.len + CH - 1) / CH, first = min(p.chunk0, all), nchunks = min(p.chunk1, all) - first;
+    const size_t item0 = (size_t)slot_base(span.row0, n) + first;
+    span.row0 += first * CH;
+    span.len -= first * CH;
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -318,11 +320,11 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             const int page = page_of(a.sT_index, n, a.pages, a.err);
             bool keep = page >= 0 && ok;
-            if (page >= 0 && (a.sT_index || (a.s0_index && a.sT == a.s0))) {
+            if (page >= 0 && (a.sT_index || (p.start_index && a.sT == p.start))) {
                 bool clash = false;       // as page_is_free, a warp at a time
                 for (int j = lane; j < a.N; j += 32) {
                     if (a.sT_index && j < n && a.sT_index[j] == page) clash = true;
-                    if (a.sT == a.s0 && j != n && (a.s0_index ? a.s0_index[j] : j) == page) clash = true;
+                    if (a.sT == p.start && j != n && (p.start_index ? p.start_index[j] : j) == page) clash = true;
                 }
                 if (__any_sync(0xffffffffu, clash)) {
                     keep = false;

@@ -1045,3 +1045,89 @@ def test_a_batch_whose_heads_walk_in_two_parts(kda, N, T, Hk, Hv):
     kda.kda_check_device_error()
     for a in answers[1:]:
         assert torch.equal(a[0], answers[0][0]) and torch.equal(a[1], answers[0][1])
+
+
+def _few_long(lens, Hk, Hv, seed):
+    """bf16 inputs of packed sequences whose walks leave SMs idle, and those with one-token sequences behind them,
+    so many that the call takes all chunks at once."""
+    torch.manual_seed(seed)
+    more = 148 // Hv + 1
+    T, unit = sum(lens) + more, torch.nn.functional.normalize
+    x = [unit(torch.randn(T, Hk, 128, device="cuda"), dim=-1).bfloat16() for _ in range(2)]
+    x += [torch.randn(T, Hv, 128, device="cuda").bfloat16(), -0.1 * torch.rand(T, Hv, device="cuda"), torch.rand(T, Hv, device="cuda")]
+    x = [t.bfloat16() for t in x]
+    offs = torch.tensor([0, *lens, *[1] * more], dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    return x, offs, sum(lens)
+
+
+@pytest.mark.parametrize("lens,Hk,Hv", [((3000, 0, 456), 4, 16), ((4100,), 1, 32), ((64 * 40, 64 * 60 + 1, 250, 64 * 52), 3, 30),
+                                        ((12345,), 2, 4)])
+def test_few_long_sequences_walk_in_two_parts(kda, lens, Hk, Hv):
+    """A part of every sequence's chunks walks before the others are prepared: the bits of the call that takes all at
+    once; with dense states, with pages in place, without states, replayed from a graph."""
+    x, offs, T = _few_long(lens, Hk, Hv, 114)
+    N, M = len(lens), offs.numel() - 1
+    s0 = torch.randn(M, Hv, 128, 128, device="cuda")
+    sT = torch.empty_like(s0)
+    want, _ = kda.kda_gdr_forward(*x, offs, s0, None, sT)
+    zero, _ = kda.kda_gdr_forward(*x, offs)
+    y, cu = [t[:T].clone() for t in x], offs[:N + 1].clone()
+    ws = torch.empty(kda.kda_gdr_workspace_size(N, T, Hk, Hv, 128, 128, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        ws.fill_(255)
+        got = torch.empty_like(sT[:N])
+        out, _ = kda.kda_gdr_forward(*y, cu, s0[:N].clone(), None, got, workspace=ws)
+        assert torch.equal(out, want[:T]) and torch.equal(got, sT[:N])
+        ws.fill_(255)
+        out, _ = kda.kda_gdr_forward(*y, cu, workspace=ws)
+        assert torch.equal(out, zero[:T])
+    if N == 1:
+        out, _ = kda.kda_gdr_forward(*(t[None] for t in y), None, s0[:1].clone(), None, got)
+        assert torch.equal(out[0], want[:T]) and torch.equal(got, sT[:1])
+    at = torch.randperm(N + 2, device="cuda")[:N].to(torch.int32)
+    pages, kept = torch.randn(N + 2, Hv, 128, 128, device="cuda"), None
+    pages[at.long()] = s0[:N]
+    first = pages.clone()
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(y[2])
+    with torch.cuda.graph(graph):
+        kda.kda_gdr_forward(*y, cu, pages, out, pages, initial_index=at, final_index=at, workspace=ws)
+        kept = pages.clone()                       # a kernel behind, which reads all of them
+    for _ in range(2):
+        pages.copy_(first)
+        graph.replay()
+        assert torch.equal(out, want[:T]) and torch.equal(kept[at.long()], sT[:N])
+        rest = [i for i in range(N + 2) if i not in at.tolist()]
+        assert torch.equal(kept[rest], first[rest])
+    kda.kda_check_device_error()
+
+
+def test_bad_pages_of_few_long_sequences(kda):
+    """In two parts as in one: a page that another sequence starts from is not written, of two that end on one page
+    the first does, indices out of range count as none; each is reported."""
+    lens, Hk, Hv = (3000, 80, 456), 4, 16
+    x, offs, T = _few_long(lens, Hk, Hv, 115)
+    y, cu = [t[:T].clone() for t in x], offs[:4].clone()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    first = torch.randn(6, Hv, 128, 128, device="cuda")
+
+    def call(start, end):
+        p = first.clone()
+        kda.kda_gdr_forward(*y, cu, p, None, p, initial_index=start, final_index=end)
+        return p
+    good = call(i32(0, 1, 2), i32(3, 4, 5))
+    kda.kda_check_device_error()
+    for start, end, written in ((i32(0, 1, 2), i32(1, 4, 5), (4, 5)), (i32(0, 1, 2), i32(3, 3, 5), (3, 5)),
+                                (i32(0, 1, 2), i32(6, 4, -7), (4,))):
+        got = call(start, end)
+        with pytest.raises(kda.KdaError):
+            kda.kda_check_device_error()
+        for p in range(6):
+            assert torch.equal(got[p], good[p] if p in written else first[p]), p
+    with pytest.raises(kda.KdaError):
+        call(i32(9, 1, 2), i32(3, 4, 5))
+        kda.kda_check_device_error()
+    none = call(i32(-1, 1, 2), i32(3, 4, 5))
+    got = call(i32(9, 1, 2), i32(3, 4, 5))
+    assert torch.equal(got, none)
+    with pytest.raises(kda.KdaError):
+        kda.kda_check_device_error()
