@@ -342,11 +342,13 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
 // on the idle SMs (not before, and not on the idle SMs of the last round, when nothing is left to do).  4 x 8192
 // tokens of 96 heads 1833 us (1955 in one prep and one walk), 2 x 4096 of 96 heads 459 (603), 2 x 512 of 96 heads 79
 // (93); where the idle SMs have fewer than 400 chunks' time, two launches more cost what it gives (2 x 128 of 96
-// heads 36.5 against 35.9).  0: all heads in one prep and one walk.
+// heads 36.5 against 35.9).  Packed sequences: their lengths are on the device only; launches that decide there which
+// of them has work gave 4 x 8192 packed tokens of 96 heads 1 % and cost lengths that differ 5 %.  0: all heads in
+// one prep and one walk.
 static int leading_heads(const GdrArgs &a)
 {
     const long long walks = (long long)a.N * a.Hv;
-    if (a.cu || walks <= SMS || walks % SMS == 0) return 0;
+    if ((a.cu && a.N > 1) || walks <= SMS || walks % SMS == 0) return 0;
     const long long lead = (walks % SMS + a.N - 1) / a.N, idle = SMS - lead * a.N, chunks = (a.T / a.N + CH - 1) / CH;
     return lead < a.Hv && idle > 0 && chunks * idle >= 400 ? (int)lead : 0;
 }
