@@ -34,10 +34,12 @@ KDA_DEVICE float clamp_gate(float g) { return g < -128.0f ? -128.0f : g; }
 
 // The first words of every kernel here, launched by launch_after: it may be on the GPU before the kernel it follows
 // has ended, and goes no further until that one's writes can be seen.  Every block waits, those with nothing
-// to do too, so that the end of a kernel is the end of all before it.  No kernel lets its follower come before its
-// own end (griddepcontrol.launch_dependents): blocks placed among those of a running kernel end up unevenly, and
-// the walks lost more by that than the earlier start gave (8192 tokens backward 529 us against 513).
+// to do too, so that the end of a kernel is the end of all before it.
 KDA_DEVICE void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel come before this one's end; only for work that is to run beside it: blocks placed among those
+// of a running kernel end up unevenly, and the walks lost more by that than an earlier start gave (8192 tokens
+// backward 529 us against 513).
+KDA_DEVICE void come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Two fp32 operations an instruction (kernels that are short of issue slots, not of arithmetic).
 KDA_DEVICE void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1)

@@ -261,7 +261,7 @@ gdr_walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_v, TcP p)
 {
     follow();
-    if (LEADS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the next prep's blocks may come
+    if (LEADS) come();                       // the next prep's blocks may
     walk_forward<false>(tm_q, tm_k, tm_v, p, blockIdx.x);
 }
 
@@ -344,7 +344,8 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
 // (93); where the idle SMs have fewer than 400 chunks' time, two launches more cost what it gives (2 x 128 of 96
 // heads 36.5 against 35.9).  Packed sequences: their lengths are on the device only; launches that decide there which
 // of them has work gave 4 x 8192 packed tokens of 96 heads 1 % and cost lengths that differ 5 %.  0: all heads in
-// one prep and one walk.
+// one prep and one walk, as in the backward pass, whose longer reverse and shorter forward walks fill the SMs better
+// (2 x 4096 tokens of 48 heads 775 us, 813 in two parts).
 static int leading_heads(const GdrArgs &a)
 {
     const long long walks = (long long)a.N * a.Hv;
