@@ -290,7 +290,8 @@ size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
 {
     (void)Hk;
     const size_t items = (size_t)gdr_slots(N, T) * Hv;
-    const size_t carry = !backward && early_chunks(N, T, Hv) ? (size_t)N * Hv * D * D * 4 : 0;
+    // whether they are used or not, so that a workspace of the most sequences and tokens does for fewer
+    const size_t carry = backward ? 0 : (size_t)std::min<long long>((long long)N * Hv, SMS) * D * D * 4;
     return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + carry + 4 * (size_t)N;
 }
 

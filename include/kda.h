@@ -322,9 +322,11 @@ kda_status_t kda_layer_decode_step(const void *q_raw, const void *k_raw, const v
 /*
  * Bytes of device workspace of kda_gdr_forward (backward = 0) or kda_gdr_backward
  * (backward = 1): per 64-token chunk and value head, the chunk's matrices M and P M (32 KiB),
- * for the backward pass also the chunk's states, corrections and their gradients, for a forward
- * pass of few long sequences also a state of each.  A call needs it only while it runs; calls
- * that overlap on the GPU need one each (two captured graphs that may run at once among them).
+ * for the backward pass also the chunk's states, corrections and their gradients, for the
+ * forward pass also the states of up to 148 sequences and heads.  More sequences, tokens or value
+ * heads never need less, so a workspace of the largest call does for all.  A call needs it only
+ * while it runs; calls that overlap on the GPU need one each (two captured graphs that may run
+ * at once among them).
  */
 kda_status_t kda_gdr_workspace_size(int N, int T_total, int Hk, int Hv, int dk, int dv, kda_dtype_t io,
                                     int backward, size_t *bytes);

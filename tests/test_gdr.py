@@ -168,3 +168,20 @@ def test_shared_buffers_are_refused(lib):
         assert backward(outs) == INVALID
     for at in (0x300000, 0x300008, 0x2ffff8):           # the same ids, or some of them
         assert lib.kda_pages_fork(A, 64, 2, 5, A, P(0x300000), P(at), 3, None) == INVALID
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("io,dk", [(1, 128), (0, 64)])
+def test_a_workspace_of_the_largest_call_does_for_all(lib, io, dk, backward):
+    """The size never falls with the sequences, the tokens or the value heads."""
+    n = ctypes.c_size_t(0)
+
+    def size(N, T, Hv):
+        assert lib.kda_gdr_workspace_size(N, T, 1, Hv, dk, dk, io, backward, ctypes.byref(n)) == 0
+        return n.value
+    Ns, Ts, Hs = [1, 2, 3, 4, 5, 8, 16, 100, 148, 149], [0, 1, 63, 64, 500, 1200, 4096, 8192, 65536], [1, 4, 8, 30, 32, 33, 96, 148, 160]
+    for N in Ns:
+        for T in Ts:
+            for H in Hs:
+                here = size(N, T, H)
+                assert all(size(N + 1, T, H) >= here and size(N, T + d, H) >= here and size(N, T, H + d) >= here for d in (1, 64, 100))
