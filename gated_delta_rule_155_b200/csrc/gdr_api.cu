@@ -110,7 +110,12 @@ kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const 
         return KDA_ERR_MISALIGNED;
     st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, false));
     if (st != KDA_OK) return st;
-    if (T_total > 0 && shared({out}, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
+    // what no kernel touches may be anything: at T_total = 0 the tensors of tokens and the workspace
+    const bool tokens = T_total > 0;
+    const void *o = tokens ? out : nullptr, *ws = tokens ? workspace : nullptr;
+    if (shared({o, final_state, ws}, {initial_index, final_index, cu_seqlens}) || shared({o, ws}, {initial_state}) ||
+        (tokens && shared({out, final_state, workspace}, {q, k, v, g, beta})))
+        return KDA_ERR_INVALID_ARG;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, initial_index, out, final_state, final_index, pages, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word()};
     if (on_tensor_cores(dk, dv, io)) {
@@ -135,7 +140,13 @@ kda_status_t kda_gdr_backward(const void *q, const void *k, const void *v, const
         return KDA_ERR_MISALIGNED;
     st = check_workspace(workspace, workspace_bytes, workspace_bytes_of(N, T_total, Hk, Hv, dk, dv, io, true));
     if (st != KDA_OK) return st;
-    if (T_total > 0 && shared({d_q, d_k, d_v, d_g, d_beta}, {q, k, v, g, beta, d_out})) return KDA_ERR_INVALID_ARG;
+    // d_initial_state may be d_final_state: a block reads its columns of the one before it writes them to the other.
+    // It may not be initial_state, which other blocks may not have read yet.
+    if (shared({d_initial_state}, {initial_state, cu_seqlens})) return KDA_ERR_INVALID_ARG;
+    if (T_total > 0 && (shared({d_q, d_k, d_v, d_g, d_beta, d_initial_state, workspace},
+                               {q, k, v, g, beta, d_out, initial_state, cu_seqlens}) ||
+                        shared({d_q, d_k, d_v, d_g, d_beta, workspace}, {d_final_state})))
+        return KDA_ERR_INVALID_ARG;
     kda::GdrArgs a{q, k, v, g, beta, initial_state, nullptr, nullptr, nullptr, nullptr, 0, cu_seqlens,
                    workspace, N, T_total, Hk, Hv, dk, dv, io_of(io), kda::device_error_word(),
                    d_out, d_final_state, d_q, d_k, d_v, d_g, d_beta, d_initial_state};
@@ -156,7 +167,7 @@ kda_status_t kda_gdr_decode(const void *q, const void *k, const void *v, const v
     if (T < 1 || any_null({q, k, v, g, beta, state, out})) return KDA_ERR_INVALID_ARG;
     if (index && pages < 1) return KDA_ERR_INVALID_ARG;
     if (misaligned({q, k, v, g, beta, state, out}) || misaligned4({index})) return KDA_ERR_MISALIGNED;
-    if (shared({out}, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
+    if (shared({out, state}, {q, k, v, g, beta, index})) return KDA_ERR_INVALID_ARG;
     kda::GdrDecodeArgs a{q, k, v, g, beta, state, index, pages, out, N, T, Hk, Hv, dk, dv, io_of(io),
                          kda::device_error_word()};
     return cuda_status(kda::launch_gdr_decode(a, (cudaStream_t)stream));
@@ -170,6 +181,7 @@ kda_status_t kda_pages_fork(void *cache, size_t page_bytes, int layers, int page
     if (!refs || (n > 0 && any_null({parents, children}))) return KDA_ERR_INVALID_ARG;
     if (misaligned4({refs, parents, children})) return KDA_ERR_MISALIGNED;
     if (n == 0) return KDA_OK;
+    if (shared({cache, refs, children}, {parents})) return KDA_ERR_INVALID_ARG;
     if (meet(children, parents, n)) return KDA_ERR_INVALID_ARG;   // written before the copies read the parents
     kda::PagesArgs a{cache, page_bytes, layers, pages, kda::device_error_word()};
     return cuda_status(kda::launch_pages_fork(a, refs, parents, children, n, (cudaStream_t)stream));
@@ -183,6 +195,7 @@ kda_status_t kda_pages_copy(void *cache, size_t page_bytes, int layers, int page
     if (n > 0 && any_null({src, dst})) return KDA_ERR_INVALID_ARG;
     if (misaligned4({src, dst})) return KDA_ERR_MISALIGNED;
     if (n == 0) return KDA_OK;
+    if (shared({cache}, {src, dst})) return KDA_ERR_INVALID_ARG;
     kda::PagesArgs a{cache, page_bytes, layers, pages, kda::device_error_word()};
     return cuda_status(kda::launch_pages_copy(a, src, dst, n, (cudaStream_t)stream));
 }
@@ -192,6 +205,7 @@ kda_status_t kda_pages_free(int *refs, int pages, const int *ids, int n, kda_str
     if (!refs || pages < 1 || n < 0 || (n > 0 && !ids)) return KDA_ERR_INVALID_ARG;
     if (misaligned4({refs, ids})) return KDA_ERR_MISALIGNED;
     if (n == 0) return KDA_OK;
+    if (shared({refs}, {ids})) return KDA_ERR_INVALID_ARG;
     return cuda_status(kda::launch_pages_free(refs, pages, ids, n, kda::device_error_word(), (cudaStream_t)stream));
 }
 
@@ -210,6 +224,7 @@ kda_status_t kda_pages_compact(void *cache, size_t page_bytes, int layers, int p
     if (!refs || (n > 0 && !table)) return KDA_ERR_INVALID_ARG;
     if (misaligned4({refs, table, live, workspace})) return KDA_ERR_MISALIGNED;
     if (!workspace || workspace_bytes < kda::pages_compact_workspace(pages)) return KDA_ERR_WORKSPACE;
+    if (shared({cache, refs, n > 0 ? table : nullptr, live, workspace}, {})) return KDA_ERR_INVALID_ARG;
     kda::PagesArgs a{cache, page_bytes, layers, pages, kda::device_error_word()};
     return cuda_status(kda::launch_pages_compact(a, refs, table, n, live, workspace, (cudaStream_t)stream));
 }

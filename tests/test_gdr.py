@@ -185,3 +185,46 @@ def test_a_workspace_of_the_largest_call_does_for_all(lib, io, dk, backward):
             for H in Hs:
                 here = size(N, T, H)
                 assert all(size(N + 1, T, H) >= here and size(N, T + d, H) >= here and size(N, T, H + d) >= here for d in (1, 64, 100))
+
+
+def test_a_written_buffer_is_no_other_argument(lib):
+    """Every pair of a written argument and another one, given as one pointer, is refused before any launch, but for
+    the pairs that are documented (final_state over initial_state, d_initial_state over d_final_state)."""
+    def pairs(call, written, read, allowed=()):
+        at = {n: P(0x1000000 + 0x10000 * i) for i, n in enumerate((*written, *read))}
+        for i, w in enumerate(written):
+            for other in (*written[:i], *read):
+                if (w, other) not in allowed:
+                    assert call({**at, w: at[other]}) == INVALID, (w, other)
+    io = ("q", "k", "v", "g", "beta")
+
+    def forward(x):
+        return lib.kda_gdr_forward(*(x[n] for n in io), x["s0"], x["i0"], x["out"], x["sT"], x["i1"], 4, x["cu"], x["ws"],
+                                   1 << 50, 2, 64, 2, 4, 128, 128, 0, None)
+    pairs(forward, ("out", "sT", "ws"), (*io, "s0", "i0", "i1", "cu"), {("sT", "s0")})
+
+    def backward(dk, T, x):
+        return lib.kda_gdr_backward(*(x[n] for n in io), x["s0"], x["cu"], x["do"], x["dT"], x["dq"], x["dk"], x["dv"], x["dg"],
+                                    x["db"], x["d0"], x["ws"], 1 << 50, 2, T, 2, 4, dk, dk, 1, None)
+    for dk in (64, 128):
+        pairs(lambda x: backward(dk, 64, x), ("dq", "dk", "dv", "dg", "db", "d0", "ws"), (*io, "do", "s0", "dT", "cu"),
+              {("d0", "dT")})
+    pairs(lambda x: backward(128, 0, {n: x.get(n) for n in (*io, "do", "dT", "dq", "dk", "dv", "dg", "db", "ws", *x)}),
+          ("d0",), ("s0", "cu"))                       # no tokens: the states are still read and written
+
+    def decode(x):
+        return lib.kda_gdr_decode(*(x[n] for n in io), x["state"], x["index"], 4, x["out"], 2, 1, 2, 4, 128, 128, 1, None)
+    pairs(decode, ("out", "state"), (*io, "index"))
+
+    def fork(x):
+        return lib.kda_pages_fork(x["cache"], 64, 2, 5, x["refs"], x["parents"], x["children"], 3, None)
+    pairs(fork, ("cache", "refs", "children"), ("parents",))
+
+    def copy(x):
+        return lib.kda_pages_copy(x["cache"], 64, 2, 5, x["src"], x["dst"], 3, None)
+    pairs(copy, ("cache",), ("src", "dst"))
+    pairs(lambda x: lib.kda_pages_free(x["refs"], 5, x["ids"], 3, None), ("refs",), ("ids",))
+
+    def compact(x):
+        return lib.kda_pages_compact(x["cache"], 64, 2, 5, x["refs"], x["table"], 3, x["live"], x["ws"], 1 << 20, None)
+    pairs(compact, ("cache", "refs", "table", "live", "ws"), ())
