@@ -3,7 +3,9 @@
 Every function here has the name of the C entry point it calls (``include/kda.h``)
 and takes torch tensors that live on the GPU; each one checks shapes, dtypes and
 contiguity, passes raw device pointers and the current CUDA stream, and raises
-:class:`KdaError` on a non-OK status.  The calls whose kernels take a few microseconds go
+:class:`KdaError` on a non-OK status.  With ``stream=`` a call runs on that stream, its inputs must be
+ready there, and what it allocates comes out of that stream's memory; the caller orders the
+streams before it reads the results on another.  The calls whose kernels take a few microseconds go
 through ``_calls.so`` (``csrc/calls.cpp``), which does the same for well-formed arguments in
 C++; every other argument comes back here to be named in an error.  All computation happens in the library's
 CUDA kernels.  There is no fallback: if ``libkda.so`` is missing or fails to load,
@@ -156,9 +158,37 @@ def _taken(r, where):
     return r
 
 
+def _torch_stream(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _new(stream, make, *args, **kw):
+    """make(*args, **kw), which a call on `stream` writes and the caller gets.  Out of that stream's memory: a block of
+    the current stream's may have a last user that still runs there, and nothing orders `stream` behind it.  The
+    caller may drop it while the current stream works on it, so it is kept until that is over."""
+    if stream is None:
+        return make(*args, **kw)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = make(*args, **kw)
+    t.record_stream(current)
+    return t
+
+
+def _workspace(stream, need, device):
+    """A workspace of `need` bytes for a call on `stream`, out of that stream's memory (as _new); no other uses it."""
+    if need == 0:
+        return None
+    if stream is None:
+        return _empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return _empty(need, dtype=torch.uint8, device=device)
+
+
 def _on(stream, *tensors):
-    """What was allocated on the current stream and is used on `stream` is kept until that use is over."""
+    """What the caller gave, allocated on another stream perhaps, is kept until its use on `stream` is over."""
     if stream is not None:
+        stream = _torch_stream(stream)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -210,7 +240,7 @@ def kda_forward_chunked(q, k, v, g, beta, initial_state=None, out=None, final_st
         _need(t, s, io, n)
     _need(initial_state, (B, H, dk, dv), torch.float32, "initial_state", allow_none=True)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=io, device=q.device)
+        out = _new(stream, torch.empty, (B, T, H, dv), dtype=io, device=q.device)
     _need(out, (B, T, H, dv), io, "out")
     _need(final_state, (B, H, dk, dv), torch.float32, "final_state", allow_none=True)
     _check(_lib.kda_forward_chunked(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -238,7 +268,7 @@ def kda_forward_chunked_varlen(q, k, v, g, beta, cu_seqlens, initial_state=None,
         _need(t, s, io, n)
     _need(initial_state, (N, H, dk, dv), torch.float32, "initial_state", allow_none=True)
     if out is None:
-        out = torch.empty((Tt, H, dv), dtype=io, device=q.device)
+        out = _new(stream, torch.empty, (Tt, H, dv), dtype=io, device=q.device)
     _need(out, (Tt, H, dv), io, "out")
     _need(final_state, (N, H, dk, dv), torch.float32, "final_state", allow_none=True)
     _check(_lib.kda_forward_chunked_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -274,14 +304,14 @@ def kda_backward_chunked(q, k, v, g, beta, d_out, initial_state=None, d_final_st
               "dbeta": (B, T, H)}
     for n, s in shapes.items():
         if gr.get(n) is None:
-            gr[n] = torch.empty(s, dtype=io, device=q.device)
+            gr[n] = _new(stream, torch.empty, s, dtype=io, device=q.device)
         _need(gr[n], s, io, n)
     if d_initial_state is None:
-        d_initial_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        d_initial_state = _new(stream, torch.empty, (B, H, dk, dv), dtype=torch.float32, device=q.device)
     _need(d_initial_state, (B, H, dk, dv), torch.float32, "d_initial_state")
     need = kda_backward_workspace_size(B, T, H, dk, dv, io)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _workspace(stream, need, q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.kda_backward_chunked(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(d_out), _ptr(d_final_state),
@@ -301,7 +331,7 @@ def kda_decode_step(q, k, v, g, beta, state, out=None, *, stream=None):
         _need(t, s, io, n)
     _need(state, (B, H, dk, dv), torch.float32, "state")
     if out is None:
-        out = torch.empty((B, H, dv), dtype=io, device=q.device)
+        out = _new(stream, torch.empty, (B, H, dv), dtype=io, device=q.device)
     _need(out, (B, H, dv), io, "out")
     _check(_lib.kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
                                 _ptr(out), B, H, dk, dv, _io_code(io), _stream(stream)),
@@ -342,11 +372,11 @@ def kda_layer_forward(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, g_raw, A_log,
     _need(initial_state, (B, H, dk, dv), f32, "initial_state", allow_none=True)
     _need(final_state, (B, H, dk, dv), f32, "final_state", allow_none=True)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=io, device=g_raw.device)
+        out = _new(stream, torch.empty, (B, T, H, dv), dtype=io, device=g_raw.device)
     _need(out, (B, T, H, dv), io, "out")
     need = kda_layer_workspace_size(B, T, H, dk, dv, io)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=g_raw.device)
+    if workspace is None:
+        workspace = _workspace(stream, need, g_raw.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.kda_layer_forward(
         _ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_q), _ptr(conv_k), _ptr(conv_v),
@@ -381,11 +411,11 @@ def kda_layer_forward_varlen(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, g_raw,
     _need(initial_state, (N, H, dk, dv), f32, "initial_state", allow_none=True)
     _need(final_state, (N, H, dk, dv), f32, "final_state", allow_none=True)
     if out is None:
-        out = torch.empty((Tt, H, dv), dtype=io, device=g_raw.device)
+        out = _new(stream, torch.empty, (Tt, H, dv), dtype=io, device=g_raw.device)
     _need(out, (Tt, H, dv), io, "out")
     need = kda_layer_workspace_size(1, Tt, H, dk, dv, io)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=g_raw.device)
+    if workspace is None:
+        workspace = _workspace(stream, need, g_raw.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.kda_layer_forward_varlen(
         _ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_q), _ptr(conv_k), _ptr(conv_v),
@@ -416,7 +446,7 @@ def kda_layer_decode_step(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, cache_q, 
     _need(dt_bias, (H * dk,), f32, "dt_bias", allow_none=True)
     _need(o_norm_w, (dv,), f32, "o_norm_w", allow_none=True)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=io, device=g_raw.device)
+        out = _new(stream, torch.empty, (B, H, dv), dtype=io, device=g_raw.device)
     _need(out, (B, H, dv), io, "out")
     _check(_lib.kda_layer_decode_step(
         _ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_q), _ptr(conv_k), _ptr(conv_v),
@@ -448,7 +478,7 @@ def kda_layer_forward_noalloc(q_raw, k_raw, v_raw, conv_q, conv_k, conv_v, g_raw
     _need(initial_state, (B, H, dk, dv), f32, "initial_state", allow_none=True)
     _need(final_state, (B, H, dk, dv), f32, "final_state", allow_none=True)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=io, device=g_raw.device)
+        out = _new(stream, torch.empty, (B, T, H, dv), dtype=io, device=g_raw.device)
     _need(out, (B, T, H, dv), io, "out")
     _check(_lib.kda_layer_forward_noalloc(
         _ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_q), _ptr(conv_k), _ptr(conv_v),
@@ -480,10 +510,6 @@ def _gdr_shapes(q, k, v, g, beta, cu_seqlens):
     gates = (*lead, Hv)
     _need_all(((q, sq, io, "q"), (k, sq, io, "k"), (v, (*gates, dv), io, "v"), (g, gates, io, "g"), (beta, gates, io, "beta")))
     return N, Tt, Hk, Hv, dk, dv, lead
-
-
-def _workspace(need, device):
-    return _empty(need, dtype=torch.uint8, device=device) if need > 0 else None
 
 
 def _ws_bytes(workspace):
@@ -533,11 +559,11 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
     if p0 and p1 and p0 != p1:
         raise ValueError(f"initial_state has {p0} pages, final_state {p1}")
     if out is None:
-        out = torch.empty_like(v)
+        out = _new(stream, torch.empty_like, v)
     else:
         _need_all(((out, v.shape, q.dtype, "out"),))
     if workspace is None:
-        workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype), q.device)
+        workspace = _workspace(stream, kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype), q.device)
     _check(_lib.kda_gdr_forward(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(initial_index), _ptr(out),
         _ptr(final_state), _ptr(final_index), max(p0, p1), _ptr(cu_seqlens), _ptr(workspace), _ws_bytes(workspace),
@@ -564,11 +590,11 @@ def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=Non
     gr = dict(grads or {})
     for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
         if gr.get(n) is None:
-            gr[n] = torch.empty_like(t)
+            gr[n] = _new(stream, torch.empty_like, t)
         else:
             _need_all(((gr[n], t.shape, q.dtype, n),))
     if workspace is None:
-        workspace = _workspace(kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype, backward=True), q.device)
+        workspace = _workspace(stream, kda_gdr_workspace_size(N, Tt, Hk, Hv, dk, dv, q.dtype, backward=True), q.device)
     _check(_lib.kda_gdr_backward(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out),
         _ptr(d_final_state), _ptr(gr["dq"]), _ptr(gr["dk"]), _ptr(gr["dv"]), _ptr(gr["dg"]), _ptr(gr["dbeta"]),
@@ -599,8 +625,6 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
     Hv, dv = sv[-2:]
     gates = (*lead, Hv)
     shape = (*gates, dv)
-    if out is None:
-        out = _empty(shape, dtype=io, device=q.device)
     if index is None:
         P, idx = N, None
     else:
@@ -608,7 +632,11 @@ def kda_gdr_decode(q, k, v, g, beta, state, index=None, out=None, *, stream=None
         _need_all(((index, (N,), torch.int32, "index"),))
         idx = index.data_ptr()
     _need_all(((q, sq, io, "q"), (k, sq, io, "k"), (v, shape, io, "v"), (g, gates, io, "g"), (beta, gates, io, "beta"),
-               (state, (P, Hv, dk, dv), torch.float32, "state"), (out, shape, io, "out")))
+               (state, (P, Hv, dk, dv), torch.float32, "state")))
+    if out is None:
+        out = _new(stream, _empty, shape, dtype=io, device=q.device)
+    else:
+        _need_all(((out, shape, io, "out"),))
     st = _lib.kda_gdr_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
                              idx, P, out.data_ptr(), N, T, Hk, Hv, dk, dv, _io_code(io), _stream(stream))
     if st:
@@ -644,7 +672,7 @@ def kda_pages_fork(cache, refs, parents, children=None, *, stream=None):
     L, P, nbytes = _cache(cache)
     n = _ids(parents, "parents")
     if children is None:
-        children = torch.empty_like(parents)
+        children = _new(stream, torch.empty_like, parents)
     _need_all(((refs, (P,), torch.int32, "refs"), (children, (n,), torch.int32, "children")))
     _check(_lib.kda_pages_fork(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(parents), _ptr(children), n, _stream(stream)),
            "kda_pages_fork")
@@ -693,11 +721,11 @@ def kda_pages_compact(cache, refs, table=None, live=None, *, workspace=None, str
         _need_all(((table, table.shape, torch.int32, "table"),))
         n = table.numel()
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=cache.device)
+        live = _new(stream, torch.empty, 1, dtype=torch.int32, device=cache.device)
     else:
         _need_all(((live, (1,), torch.int32, "live"),))
     if workspace is None:
-        workspace = _workspace(kda_pages_workspace_size(P), cache.device)
+        workspace = _workspace(stream, kda_pages_workspace_size(P), cache.device)
     _check(_lib.kda_pages_compact(_ptr(cache), nbytes, L, P, _ptr(refs), _ptr(table), n, _ptr(live), _ptr(workspace),
                                   _ws_bytes(workspace), _stream(stream)), "kda_pages_compact")
     _on(stream, live, workspace)

@@ -1131,3 +1131,42 @@ def test_bad_pages_of_few_long_sequences(kda):
     assert torch.equal(got, none)
     with pytest.raises(kda.KdaError):
         kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_a_call_on_a_given_stream_takes_no_block_in_use(kda, io, dk):
+    """Blocks that the current stream has freed and still writes are not what a call on another stream allocates."""
+    N, T, Hk, Hv = 2, 700, 1, 2
+    d = make(N * T, Hk, Hv, dk, dk, io, 120, N)
+    x = [t.view(N, T, *t.shape[1:]) for t in to(d, *NAMES, "dO")]
+    wide = x[0].repeat(1, 1, 2, 1)                       # the per-channel rule has as many key heads as value heads
+    y = (wide, wide, x[2], -wide.abs(), x[4])
+    s0, tok = d["s0"].cuda(), [t[:, 0].contiguous() for t in x[:5]]
+    cache, ids = torch.randn(2, 9, 64, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    refs = torch.tensor([1, 1, 1, 0, 0, 1, 0, 0, 1], dtype=torch.int32, device="cuda")
+    calls = {                                            # the function, and its arguments (made anew: some are written)
+        "forward": (kda.kda_gdr_forward, lambda: (*x[:5], None, s0)),
+        "backward": (kda.kda_gdr_backward, lambda: (*x, None, s0)),
+        "decode": (kda.kda_gdr_decode, lambda: (*tok, s0.clone())),
+        "fork": (kda.kda_pages_fork, lambda: (cache.clone(), refs.clone(), ids)),
+        "compact": (kda.kda_pages_compact, lambda: (cache.clone(), refs.clone())),
+        "chunked": (kda.kda_forward_chunked, lambda: (*y, s0)),
+        "chunked backward": (kda.kda_backward_chunked, lambda: (*y, x[5], s0)),
+    }
+    spaces = [kda.kda_backward_workspace_size(N, T, Hv, dk, dk, DT[io]), kda.kda_pages_workspace_size(9),
+              *(kda.kda_gdr_workspace_size(N, N * T, Hk, Hv, dk, dk, DT[io], backward=b) for b in (False, True))]
+    tensors = lambda r: [t for t in (r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else (r,))  # noqa: E731
+                         if t is not None]
+    s = torch.cuda.Stream()
+    for name, (call, args) in calls.items():
+        want, given = tensors(call(*args())), args()
+        torch.cuda.synchronize()
+        busy = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in [t.nbytes for t in want] + spaces for _ in range(2)]
+        torch.cuda._sleep(100_000_000)                   # tens of ms, behind which the blocks are written
+        for b in busy:
+            b.fill_(255)
+        del busy, b
+        got = tensors(call(*given, stream=s))
+        torch.cuda.synchronize()
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want)), name
+    kda.kda_check_device_error()
