@@ -285,13 +285,14 @@ static int early_chunks(int N, int T, int Hv)
     return (chunks - early) * walks >= 600 ? (int)early : 0;
 }
 
-// items; then 1 KB aligned: for the gradients S, U, dS, H, or the states between two walks; the sequences' order
+// items; then 1 KB aligned: for the gradients S, U, dS, H, or the states between two walks and their marks; the
+// sequences' order
 size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
 {
     (void)Hk;
     const size_t items = (size_t)gdr_slots(N, T) * Hv;
     // whether they are used or not, so that a workspace of the most sequences and tokens does for fewer
-    const size_t carry = backward ? 0 : (size_t)std::min<long long>((long long)N * Hv, SMS) * D * D * 4;
+    const size_t carry = backward ? 0 : (size_t)std::min<long long>((long long)N * Hv, SMS) * (D * D + 1) * 4;
     return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + carry + 4 * (size_t)N;
 }
 
@@ -315,6 +316,8 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
     } else if (early_chunks(a.N, a.T, a.Hv)) {
         p.carry = (float *)at;
         at += (size_t)a.N * a.Hv * D * D * 4;
+        p.carried = (int *)at;
+        at += (size_t)a.N * a.Hv * 4;
     }
     if (a.T > 0 && a.cu && a.N > 1) p.order = (int *)at;
     p.wait_ns = hk.wait_ns;

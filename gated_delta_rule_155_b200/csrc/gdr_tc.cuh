@@ -27,6 +27,7 @@ struct TcP {
     uint8_t *items;
     int *order;              // sequences by length, longest first (null: as they are)
     float *carry;            // the states between two walks of the forward pass
+    int *carried;            // whether the first of them left one: [N, Hv] (null: no two walks)
     uint8_t *S, *U, *dS, *H; // kept for the gradients, operand tiles of 2, 1, 2 and 1 TILE bytes an item
     int head0, heads;        // the value heads of a launch of prep and forward walk
     int chunk0, chunk1;      // and its chunks of every sequence

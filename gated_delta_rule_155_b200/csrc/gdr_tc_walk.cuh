@@ -43,7 +43,10 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
     const int hv = p.head0 + (int)(block % p.heads), hk = hv / (a.Hv / a.Hk);
     const int n = p.order ? p.order[block / p.heads] : (int)(block / p.heads);
     SeqSpan span = span_of(a.cu, n, a.N, a.T);
-    const int all = (span.len + CH - 1) / CH, first = min(p.chunk0, all), nchunks = min(p.chunk1, all) - first;
+    // a second walk has nothing to go on where the first has given up: no chunks, and no state to keep
+    auto carried = [&]() -> int & { return p.carried[(size_t)n * a.Hv + hv]; };
+    auto begun = [&]() { return p.chunk0 == 0 || carried(); };
+    const int all = (span.len + CH - 1) / CH, first = min(p.chunk0, all), nchunks = begun() ? min(p.chunk1, all) - first : 0;
     const size_t item0 = (size_t)slot_base(span.row0, n) + first;
     span.row0 += first * CH;
     span.len -= first * CH;
@@ -88,7 +91,7 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             for (int ch = 0; ch < nchunks && !*abort_flag; ++ch) {
                 const int st = ch % STAGES;
                 if (ch >= STAGES && !wait(&empty[st], ch / STAGES - 1)) break;
-                if (ch == p.skip_load_chunk) continue;   // injected failure: the wait for it runs out
+                if (first + ch == p.skip_load_chunk) continue;   // injected failure: the wait for it runs out
                 uint8_t *s = sm + st * ST_BYTES;
                 mbar_arrive_expect_tx(&full[st], 3 * TILE + IT_WALK);
                 const int row = span.row0 + ch * CH;
@@ -102,7 +105,7 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             }
             // after an abort the loads of the last stages may still be on their way
             for (int seen = issued > STAGES ? issued - STAGES : 0; seen < issued && *abort_flag; ++seen)
-                if (seen != p.skip_load_chunk)
+                if (first + seen != p.skip_load_chunk)
                     mbar_wait_timed(&full[seen % STAGES], (uint32_t)((seen / STAGES) & 1), DRAIN_NS);
         }
     } else if (warp == 17) {
@@ -319,7 +322,8 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
         if (!KEEP && a.sT) {
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             const int page = page_of(a.sT_index, n, a.pages, a.err);
-            bool keep = page >= 0 && ok;
+            named_bar_sync(1, 512);                  // all warps or none: a state is kept whole
+            bool keep = page >= 0 && ok && begun() && !*abort_flag;
             if (page >= 0 && (a.sT_index || (p.start_index && a.sT == p.start))) {
                 bool clash = false;       // as page_is_free, a warp at a time
                 for (int j = lane; j < a.N; j += 32) {
@@ -331,6 +335,7 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                     raise_error(a.err, ERR_PAGE_INDEX);
                 }
             }
+            if (p.carried && p.chunk0 == 0 && tid == 0) carried() = keep;
             if (keep) {
                 float *dst = a.sT + (((size_t)page * a.Hv + hv) * D + r0) * D + dv;
                 uint32_t x[32];

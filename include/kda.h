@@ -346,6 +346,7 @@ kda_status_t kda_gdr_workspace_size(int N, int T_total, int Hk, int Hv, int dk, 
  * the same final page the first keeps its state there, and a final page that another sequence
  * starts from (in the same buffer) is not written.  Each sets the device error word
  * (KDA_ERR_INDEX from kda_check_device_error).  A sequence of length 0 passes its state through.
+ * A sequence and head whose bounded wait runs out (KDA_ERR_TIMEOUT) leaves its final state as it was.
  */
 kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const void *g, const void *beta,
                              const float *initial_state, const int *initial_index, void *out, float *final_state,

@@ -1170,3 +1170,45 @@ def test_a_call_on_a_given_stream_takes_no_block_in_use(kda, io, dk):
         torch.cuda.synchronize()
         assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want)), name
     kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("N,T,Hv,chunk", [
+    (1, 8192, 140, 50), (1, 8192, 140, 0),     # cut at chunk 119: the first part gives up
+    (1, 8192, 140, 125),                       # the second does
+    (2, 420, 96, 3),                           # cut at a head
+    (2, 900, 8, 5),                            # in one part
+])
+def test_a_walk_that_gives_up_keeps_no_state(kda, N, T, Hv, chunk):
+    """A forward pass whose wait runs out leaves the final pages as they were, however it is cut, and says so; the
+    same call without the failure is right afterwards."""
+    torch.manual_seed(121)
+    unit = torch.nn.functional.normalize
+    x = [unit(torch.randn(N, T, 2, 128, device="cuda"), dim=-1).bfloat16() for _ in range(2)]
+    x += [torch.randn(N, T, Hv, 128, device="cuda").bfloat16(), -0.1 * torch.rand(N, T, Hv, device="cuda"), torch.rand(N, T, Hv, device="cuda")]
+    x = [t.bfloat16() for t in x]
+    first = torch.randn(2 * N + 1, Hv, 128, 128, device="cuda")
+    ids = torch.arange(2 * N, -1, -1, dtype=torch.int32, device="cuda")
+    start, end = ids[:N].clone(), ids[N:2 * N].clone()
+    ws = torch.empty(kda.kda_gdr_workspace_size(N, N * T, 2, Hv, 128, 128, torch.bfloat16), dtype=torch.uint8, device="cuda")
+
+    def call(in_place):
+        p = first.clone()
+        ws.fill_(1)                            # what a part that was not computed would be taken for
+        out, _ = kda.kda_gdr_forward(*x, None, p, None, p, initial_index=start, final_index=start if in_place else end, workspace=ws)
+        return out, p
+    want = [call(b) for b in (True, False)]
+    kda.kda_check_device_error()
+    for in_place, (out, pages) in zip((True, False), want):
+        kda.kda_set_wait_test_hooks(1_000_000, chunk)
+        try:
+            _, got = call(in_place)
+            with pytest.raises(kda.KdaError) as e:
+                kda.kda_check_device_error()
+            assert e.value.status == 5
+        finally:
+            kda.kda_set_wait_test_hooks(0, -1)
+        assert torch.equal(got, first)
+        again = call(in_place)
+        kda.kda_check_device_error()
+        assert torch.equal(again[0], out) and torch.equal(again[1], pages)
+        assert not torch.equal(pages, first)
