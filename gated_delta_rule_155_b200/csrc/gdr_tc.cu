@@ -85,10 +85,12 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         mbar_init(&bars[2], 1);
         *abort_flag = 0;
         fence_mbar_init();
-        mbar_arrive_expect_tx(&bars[0], 2 * TILE);
-        for (int cb = 0; cb < 2; ++cb) {
-            tma_load_4d(sm + PR_KQ + cb * TILE, &tm_k, cb * 64, hk, row0, 0, &bars[0]);
-            tma_load_4d(sm + PR_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row0, 0, &bars[0]);
+        if (c != p.skip_prep_chunk) {                  // else an injected failure: the wait for them runs out
+            mbar_arrive_expect_tx(&bars[0], 2 * TILE);
+            for (int cb = 0; cb < 2; ++cb) {
+                tma_load_4d(sm + PR_KQ + cb * TILE, &tm_k, cb * 64, hk, row0, 0, &bars[0]);
+                tma_load_4d(sm + PR_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row0, 0, &bars[0]);
+            }
         }
     }
     if (warp == 0) {
@@ -234,7 +236,8 @@ gdr_prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             fence_proxy_async();
         }
     } else if (tid == 0) {
-        mbar_wait_timed(&bars[0], 0, DRAIN_NS);   // the tiles, if they are still on their way
+        gates[GA_GAM + CH - 1] = -1.0f;           // no decay is negative: the walks stop at this chunk
+        if (c != p.skip_prep_chunk) mbar_wait_timed(&bars[0], 0, DRAIN_NS);   // the tiles, if they are still on their way
         mma_commit(&bars[1]);
         mbar_wait_timed(&bars[1], 0, DRAIN_NS);
     }
@@ -321,7 +324,8 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
     }
     if (a.T > 0 && a.cu && a.N > 1) p.order = (int *)at;
     p.wait_ns = hk.wait_ns;
-    p.skip_load_chunk = hk.skip_load_chunk;
+    p.skip_load_chunk = std::max(hk.skip_load_chunk, -1);
+    p.skip_prep_chunk = hk.skip_load_chunk <= -2 ? -2 - hk.skip_load_chunk : -1;
 }
 
 cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, CUtensorMap &mv, cudaStream_t s)

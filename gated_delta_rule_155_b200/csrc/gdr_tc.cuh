@@ -35,7 +35,7 @@ struct TcP {
     const int *start_index;
     bool beside;             // prep: beside the walk before it in the stream
     unsigned long long wait_ns;
-    int skip_load_chunk;
+    int skip_load_chunk, skip_prep_chunk;   // injected failures: of the walks, of prep (-1: none)
 };
 
 KDA_DEVICE void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)

@@ -224,6 +224,11 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (!(ok = wait_full(i))) break;
             {                                        // dS decayed, in the shadow of the product
                 const float gC = gates[GA_GAM + CH - 1];
+                if (gC < 0.0f) {                     // prep has given up on this chunk: so does the block
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
                 float *x = (float *)S;
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], gC, gC);

@@ -740,7 +740,8 @@ def kda_check_device_error(stream=None):
 
 def kda_set_wait_test_hooks(wait_limit_ns=0, skip_load_chunk=-1):
     """Limit of the tensor-core kernels' bounded waits (0: the default 2 s) and an injected
-    failure (the tile load of chunk `skip_load_chunk` is never issued; -1: off).  Process-wide."""
+    failure (the tile load of chunk `skip_load_chunk` is never issued; -1: off; c <= -2: that of chunk -2 - c
+    in the launch before the walks of the head-gated rule).  Process-wide."""
     _check(_lib.kda_set_wait_test_hooks(int(wait_limit_ns), int(skip_load_chunk)), "kda_set_wait_test_hooks")
 
 

@@ -437,7 +437,9 @@ kda_status_t kda_pages_compact(void *cache, size_t page_bytes, int layers, int p
  *                    default of 2 s
  *   skip_load_chunk  >= 0: in every later launch, the tile load of that chunk index is
  *                    never issued, so the wait for it runs out after the limit (the
- *                    kernel's outputs from that chunk on are then unspecified); -1: off
+ *                    kernel's outputs from that chunk on are then unspecified); -1: off; c <= -2:
+ *                    that of chunk -2 - c, in the launch before the walks of kda_gdr_forward and
+ *                    kda_gdr_backward alone
  * The settings are process-wide and read at each launch of those kernels; change them only
  * while no call is being made from another host thread.  Always returns KDA_OK.
  */

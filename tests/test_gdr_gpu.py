@@ -1177,6 +1177,7 @@ def test_a_call_on_a_given_stream_takes_no_block_in_use(kda, io, dk):
     (1, 8192, 140, 125),                       # the second does
     (2, 420, 96, 3),                           # cut at a head
     (2, 900, 8, 5),                            # in one part
+    (1, 8192, 140, -2 - 50), (1, 8192, 140, -2 - 125), (2, 420, 96, -2 - 3), (2, 900, 8, -2 - 5),   # what is before the walk
 ])
 def test_a_walk_that_gives_up_keeps_no_state(kda, N, T, Hv, chunk):
     """A forward pass whose wait runs out leaves the final pages as they were, however it is cut, and says so; the
@@ -1212,3 +1213,26 @@ def test_a_walk_that_gives_up_keeps_no_state(kda, N, T, Hv, chunk):
         kda.kda_check_device_error()
         assert torch.equal(again[0], out) and torch.equal(again[1], pages)
         assert not torch.equal(pages, first)
+
+
+@pytest.mark.parametrize("chunk", [0, 2, 9])
+def test_a_backward_call_whose_first_launch_gives_up_is_reported(kda, chunk):
+    """The tiles of a chunk never come in the launch before the walks: both walks stop there, the error is reported
+    once, and the next call is right."""
+    d = make(2 * 640, 1, 2, 128, 128, "bf16", 122, 2)
+    x = [t.view(2, 640, *t.shape[1:]) for t in to(d, *NAMES, "dO")]
+    want = kda.kda_gdr_backward(*x, None, d["s0"].cuda(), d["dS"].cuda())
+    first = torch.full((2, 2, 128, 128), 7.0, device="cuda")
+    kda.kda_set_wait_test_hooks(1_000_000, -2 - chunk)
+    try:
+        kda.kda_gdr_backward(*x, None, d["s0"].cuda(), d["dS"].cuda(), d_initial_state=first)
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_check_device_error()
+        assert e.value.status == 5
+    finally:
+        kda.kda_set_wait_test_hooks(0, -1)
+    assert bool((first == 7.0).all())
+    got = kda.kda_gdr_backward(*x, None, d["s0"].cuda(), d["dS"].cuda())
+    kda.kda_check_device_error()
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(got[n], want[n]), n
