@@ -6,7 +6,8 @@ Each ``csrc/*.cu`` is compiled separately (in parallel) with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` and linked into
 ``gated_delta_rule_155_b200/libkda.so`` (CUDA runtime linked statically).
 Objects go to ``_build/`` at the repository root.  ``csrc/calls.cpp``, the binding's short
-calls, is compiled with g++ against torch's headers into the extension module ``_calls.so``.
+calls, is compiled with g++ against torch's headers into the extension module ``_calls.so``; where that
+fails, the library is built all the same, with a warning.
 A rebuild happens only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -83,7 +85,15 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, jobs: int = 0, verbose: bool = False, extra=()) -> str:
-    build_calls(force, verbose)
+    lib = build_library(force, jobs, verbose, extra)
+    try:
+        build_calls(force, verbose)
+    except (RuntimeError, OSError, ImportError) as e:     # marshalling only: the library does without
+        warnings.warn(f"_calls.so was not built, short calls will be marshalled in Python: {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def build_library(force: bool = False, jobs: int = 0, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)

@@ -7,7 +7,8 @@ contiguity, passes raw device pointers and the current CUDA stream, and raises
 ready there, and what it allocates comes out of that stream's memory; the caller orders the
 streams before it reads the results on another.  The calls whose kernels take a few microseconds go
 through ``_calls.so`` (``csrc/calls.cpp``), which does the same for well-formed arguments in
-C++; every other argument comes back here to be named in an error.  All computation happens in the library's
+C++; every other argument comes back here to be named in an error, and all of them do, with a warning at
+import, where it was not built.  All computation happens in the library's
 CUDA kernels.  There is no fallback: if ``libkda.so`` is missing or fails to load,
 importing this module raises.
 """
@@ -16,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 
 import torch
 
@@ -93,11 +95,20 @@ def _load():
 _lib = _load()
 
 
+class _NoCalls:
+    """In place of the short calls where they were not built: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
 def _load_calls():
     try:
         from gated_delta_rule_155_b200 import _calls
     except ImportError as e:
-        raise ImportError(f"_calls.so does not load ({e}); build it with `python -m gated_delta_rule_155_b200.build`") from e
+        warnings.warn(f"_calls.so does not load ({e}): short calls are marshalled in Python, 10 to 20 us each; build it with "
+                      "`python -m gated_delta_rule_155_b200.build`", RuntimeWarning, stacklevel=3)
+        return _NoCalls()
     names = ("kda_gdr_decode", "kda_gdr_workspace_size", "kda_gdr_forward", "kda_gdr_backward", "kda_pages_fork",
              "kda_pages_free", "kda_pages_workspace_size", "kda_pages_compact")
     _calls.init(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names))
@@ -105,7 +116,8 @@ def _load_calls():
 
 
 # The calls whose kernels take a few microseconds, in C++: None where an argument is not well-formed (the
-# Python function then checks them one by one and raises), a status where the library refuses.
+# Python function then checks them one by one and raises), a status where the library refuses.  Only marshalling:
+# without them the Python functions make the same calls of the library.
 _calls = _load_calls()
 
 EXPORTED_SYMBOLS = ("kda_status_string", "kda_abi_version", "kda_forward_chunked",

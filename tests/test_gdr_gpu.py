@@ -1236,3 +1236,27 @@ def test_a_backward_call_whose_first_launch_gives_up_is_reported(kda, chunk):
     kda.kda_check_device_error()
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+def test_marshalling_in_python_gives_the_same_calls(kda, monkeypatch, io, dk):
+    d = make(150, 1, 3, dk, dk, io, 123, 3)
+    x, do, cu = to(d, *NAMES), d["v"].cuda().flip(0), torch.tensor([0, 80, 80, 150], dtype=torch.int32, device="cuda")
+    tok = [t[:3].contiguous() for t in x]
+    ids, refs = torch.tensor([0, -1], dtype=torch.int32, device="cuda"), torch.tensor([1, 0, 2, 0, 1], dtype=torch.int32)
+
+    def run():
+        s0, r, cache = d["s0"].cuda(), refs.cuda(), torch.arange(80.0, device="cuda").view(1, 5, 16)
+        sT = torch.empty_like(s0)
+        out, _ = kda.kda_gdr_forward(*x, cu, s0, final_state=sT)
+        gr = kda.kda_gdr_backward(*x, do, cu, s0)
+        step = kda.kda_gdr_decode(*tok, s0)
+        kids = kda.kda_pages_fork(cache, r, ids)
+        kda.kda_pages_free(r, ids)
+        live = kda.kda_pages_compact(cache, r)
+        kda.kda_check_device_error()
+        return [out, sT, *(gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta")), step, s0, kids, r, live, cache]
+    assert not isinstance(kda._calls, kda._NoCalls)              # built here
+    want = run()
+    monkeypatch.setattr(kda, "_calls", kda._NoCalls())
+    assert all(torch.equal(a, b) for a, b in zip(run(), want))

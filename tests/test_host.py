@@ -6,6 +6,7 @@ import os
 import subprocess
 import sys
 
+import pytest
 import torch
 
 from gated_delta_rule_155_b200 import inputs
@@ -89,3 +90,46 @@ def test_reference_arm_prints_one_json_line():
     assert d["higher_is_better"] is True and d["dtype"] == "f64"
     assert d["cpu_baseline"]["kind"] == "oracle" and d["cpu_baseline"]["cores"] >= 1
     assert d["e2e"]["h2d_bytes_per_step"] == 0 and d["e2e"]["value"] == d["value"]
+
+
+def _package_without_short_calls(path):
+    """A copy of the binding beside the built library, without the extension module."""
+    from gated_delta_rule_155_b200 import build
+
+    build.build()
+    pkg = path / "gated_delta_rule_155_b200"
+    pkg.mkdir()
+    for name in ("__init__.py", "kda.py", "build.py"):
+        (pkg / name).write_bytes(open(os.path.join(build.PKG, name), "rb").read())
+    os.symlink(build.LIB, pkg / "libkda.so")
+    return path
+
+
+def test_the_binding_loads_without_the_short_calls(tmp_path):
+    """The library and every entry point are there; what is missing is named in a warning."""
+    code = ("import warnings, torch\n"
+            "with warnings.catch_warnings(record=True) as w:\n"
+            "    warnings.simplefilter('always')\n"
+            "    from gated_delta_rule_155_b200 import kda\n"
+            "assert any('_calls' in str(x.message) for x in w), [str(x.message) for x in w]\n"
+            "assert all(hasattr(kda.library(), n) for n in kda.EXPORTED_SYMBOLS)\n"
+            "q, g, s = torch.zeros(1, 2, 64), torch.zeros(1, 2), torch.zeros(1, 2, 64, 64)\n"
+            "for f, a in ((kda.kda_gdr_decode, (q, q, q, g, g, s)), (kda.kda_gdr_forward, (q, q, q, g, g, g[0].int())),\n"
+            "             (kda.kda_pages_free, (g[0].int(), g[0].int()))):\n"
+            "    try:\n"
+            "        f(*a)\n"
+            "    except (ValueError, RuntimeError):\n"
+            "        continue\n"
+            "    raise SystemExit('host tensors were taken')\n")
+    subprocess.run([sys.executable, "-c", code], cwd=_package_without_short_calls(tmp_path), check=True)
+
+
+def test_the_library_is_built_without_a_host_compiler(monkeypatch, tmp_path):
+    from gated_delta_rule_155_b200 import build
+
+    build.build()
+    monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"), raising=False)
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        assert build.build() == build.LIB
