@@ -6,8 +6,8 @@ Each ``csrc/*.cu`` is compiled separately (in parallel) with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` and linked into
 ``gated_delta_rule_155_b200/libkda.so`` (CUDA runtime linked statically).
 Objects go to ``_build/`` at the repository root.  ``csrc/calls.cpp``, the binding's short
-calls, is compiled with g++ against torch's headers into the extension module ``_calls.so``; where that
-fails, the library is built all the same, with a warning.
+calls, is compiled with g++ against torch's headers into an extension module whose file name has
+the versions of torch and Python; where that fails, the library is built all the same, with a warning.
 A rebuild happens only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -18,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import warnings
 from concurrent.futures import ThreadPoolExecutor
 
@@ -27,7 +28,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
-CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -61,18 +61,30 @@ def _newer(lib, deps) -> bool:
     return os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps)
 
 
-def build_calls(force: bool = False, verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "calls.cpp")
-    if not force and _newer(CALLS, [src, os.path.join(INCLUDE, "kda.h")]):
-        return CALLS
-    import sysconfig
+def _abi() -> int:
+    import torch
 
+    return int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def calls_path() -> str:
+    """Where the short calls' module for this torch and this Python is.  It reads tensors through torch's C++ headers, so
+    one that was built against others is another file, which is neither current nor loaded."""
+    import torch
+
+    return os.path.join(PKG, f"_calls.torch-{torch.__version__}-cxx{_abi()}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    src, calls = os.path.join(CSRC, "calls.cpp"), calls_path()
+    if not force and _newer(calls, [src, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]):
+        return calls
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = calls + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(root, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={_abi()}", "-I", os.path.join(root, "include"),
            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
@@ -80,8 +92,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, calls)
+    return calls
 
 
 def build(force: bool = False, jobs: int = 0, verbose: bool = False, extra=()) -> str:
@@ -89,7 +101,7 @@ def build(force: bool = False, jobs: int = 0, verbose: bool = False, extra=()) -
     try:
         build_calls(force, verbose)
     except (RuntimeError, OSError, ImportError) as e:     # marshalling only: the library does without
-        warnings.warn(f"_calls.so was not built, short calls will be marshalled in Python: {e}", RuntimeWarning, stacklevel=2)
+        warnings.warn(f"the _calls extension was not built, short calls will be marshalled in Python: {e}", RuntimeWarning, stacklevel=2)
     return lib
 
 

@@ -6,7 +6,7 @@ contiguity, passes raw device pointers and the current CUDA stream, and raises
 :class:`KdaError` on a non-OK status.  With ``stream=`` a call runs on that stream, its inputs must be
 ready there, and what it allocates comes out of that stream's memory; the caller orders the
 streams before it reads the results on another.  The calls whose kernels take a few microseconds go
-through ``_calls.so`` (``csrc/calls.cpp``), which does the same for well-formed arguments in
+through the ``_calls`` extension (``csrc/calls.cpp``), which does the same for well-formed arguments in
 C++; every other argument comes back here to be named in an error, and all of them do, with a warning at
 import, where it was not built.  All computation happens in the library's
 CUDA kernels.  There is no fallback: if ``libkda.so`` is missing or fails to load,
@@ -16,10 +16,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import warnings
 
 import torch
+
+from gated_delta_rule_155_b200 import build
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -103,10 +106,15 @@ class _NoCalls:
 
 
 def _load_calls():
+    path = build.calls_path()
     try:
-        from gated_delta_rule_155_b200 import _calls
+        if not os.path.exists(path):
+            raise ImportError(f"{os.path.basename(path)} not found")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._calls", path)
+        _calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_calls)
     except ImportError as e:
-        warnings.warn(f"_calls.so does not load ({e}): short calls are marshalled in Python, 10 to 20 us each; build it with "
+        warnings.warn(f"the _calls extension does not load ({e}): short calls are marshalled in Python, 10 to 20 us each; build it with "
                       "`python -m gated_delta_rule_155_b200.build`", RuntimeWarning, stacklevel=3)
         return _NoCalls()
     names = ("kda_gdr_decode", "kda_gdr_workspace_size", "kda_gdr_forward", "kda_gdr_backward", "kda_pages_fork",

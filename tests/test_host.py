@@ -130,6 +130,24 @@ def test_the_library_is_built_without_a_host_compiler(monkeypatch, tmp_path):
     build.build()
     monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
     monkeypatch.setattr(build, "PKG", str(tmp_path))
-    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"), raising=False)
     with pytest.warns(RuntimeWarning, match="_calls"):
         assert build.build() == build.LIB
+
+
+def test_short_calls_built_for_another_torch_are_not_loaded(monkeypatch, tmp_path):
+    """Neither current nor loaded, however new the file is: it reads tensors as the other torch lays them out."""
+    from gated_delta_rule_155_b200 import build
+
+    here = build.build_calls()
+    monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    assert build.build_calls() == here                             # nothing to do
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(OSError):
+        build.build_calls()                                        # to be built again
+    monkeypatch.undo()
+    root = _package_without_short_calls(tmp_path)
+    for name in ("_calls.so", os.path.basename(here).replace(torch.__version__, "0.0.1")):
+        (root / "gated_delta_rule_155_b200" / name).write_bytes(open(here, "rb").read())
+    code = ("import warnings\nwarnings.simplefilter('ignore')\nfrom gated_delta_rule_155_b200 import kda\n"
+            "assert isinstance(kda._calls, kda._NoCalls)\n")
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
