@@ -31,12 +31,10 @@ KDA_DEVICE void load_vec(const float *p, float (&x)[R])
 template <int R>
 KDA_DEVICE void load_vec(const __nv_bfloat16 *p, float (&x)[R])
 {
+    static_assert(R % 8 == 0, "16-byte loads");
     uint32_t w[R / 2];
-    if constexpr (R >= 8)
 #pragma unroll
-        for (int e = 0; e < R / 2; e += 4) *(uint4 *)(w + e) = *(const uint4 *)(p + 2 * e);
-    else
-        *(uint2 *)w = *(const uint2 *)p;
+    for (int e = 0; e < R / 2; e += 4) *(uint4 *)(w + e) = *(const uint4 *)(p + 2 * e);
 #pragma unroll
     for (int e = 0; e < R / 2; ++e) {
         x[2 * e] = __uint_as_float(w[e] << 16);
