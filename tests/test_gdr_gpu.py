@@ -1260,3 +1260,64 @@ def test_marshalling_in_python_gives_the_same_calls(kda, monkeypatch, io, dk):
     want = run()
     monkeypatch.setattr(kda, "_calls", kda._NoCalls())
     assert all(torch.equal(a, b) for a, b in zip(run(), want))
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_copies_and_other_streams(kda, io, dk, captured):
+    """Kernels that are brought up early wait for what is before them that is no kernel of their stream: a copy from
+    the host, a fill, and another stream's work behind an event."""
+    N, T, Hk, Hv, R = 3, 70, 2, 4, 3
+    d = make(R * N * T, Hk, Hv, dk, dk, io, 124, N)
+    src = [t.view(R, N, T, *t.shape[1:]) for t in (d[n].pin_memory() for n in NAMES)]
+    x, first = [t[0].cuda() for t in src], d["s0"].cuda()
+    state, refs, ids = first.clone(), torch.zeros(N, dtype=torch.int32, device="cuda"), torch.arange(N, dtype=torch.int32, device="cuda")
+    outs, side = [torch.empty(R, *src[2].shape[1:], dtype=DT[io], device="cuda") for _ in range(2)], torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        state.copy_(first)
+        for r in range(R):
+            for a, b in zip(x, src):                       # copies from the host, then a call
+                a.copy_(b[r], non_blocking=True)
+            kda.kda_gdr_forward(*x, None, state, outs[0][r], state)
+            side.wait_stream(main)
+            with torch.cuda.stream(side):                  # inputs that another stream makes, late
+                torch.cuda._sleep(200_000)
+                for a in x[:3]:
+                    a.mul_(0.5)
+            main.wait_stream(side)
+            kda.kda_gdr_decode(*x, state, None, outs[1][r])
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                refs.zero_()
+            main.wait_stream(side)
+            kda.kda_pages_fork(state[None], refs, torch.full_like(ids, -1) if r == R - 2 else ids[:0])
+
+    def plain():
+        s, got = f64(d["s0"]), [[], []]
+        for r in range(R):
+            a = [f64(t[r]) for t in src]
+            flat = [t.reshape(N * T, *t.shape[2:]) for t in a]
+            o, s = gdr.forward(*flat, cu_of([T] * N), s)
+            got[0].append(o.reshape(a[2].shape))
+            a = [0.5 * t for t in a[:3]] + a[3:]
+            o, s = gdr.decode(*a, s)
+            got[1].append(o)
+            if r == R - 2:
+                s = np.zeros_like(s)
+        return np.stack(got[0]), np.stack(got[1]), s
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(2):
+            graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    kda.kda_check_device_error()
+    ro, rd, rs = plain()
+    near(outs[0], ro, io, io == "f32", "forward")
+    near(outs[1], rd, io, io == "f32", "decode")
+    near(state, rs, io, io == "f32", "states", stored=False)
