@@ -338,6 +338,7 @@ kda_status_t kda_layer_decode_step(const void *q_raw, const void *k_raw, const v
 kda_status_t kda_set_wait_test_hooks(unsigned long long wait_limit_ns, int skip_load_chunk)
 {
     kda::set_wait_hooks(wait_limit_ns, skip_load_chunk);
+    kda::set_gdr_prep_hook(skip_load_chunk <= -2 ? -2 - skip_load_chunk : -1);
     return KDA_OK;
 }
 

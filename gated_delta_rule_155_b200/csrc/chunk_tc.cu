@@ -1056,7 +1056,7 @@ WaitHooks wait_hooks() { return WaitHooks{g_wait_ns.load(), g_skip_load_chunk.lo
 void set_wait_hooks(unsigned long long wait_ns, int skip_load_chunk)
 {
     g_wait_ns.store(wait_ns ? wait_ns : kDefaultWaitNs);
-    g_skip_load_chunk.store(skip_load_chunk);
+    g_skip_load_chunk.store(skip_load_chunk < 0 ? -1 : skip_load_chunk);
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t s)

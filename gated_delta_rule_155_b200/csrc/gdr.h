@@ -39,6 +39,8 @@ cudaError_t launch_gdr_backward_simt(const GdrArgs &a, cudaStream_t s);
 // tcgen05 kernels: bf16, dk = dv = 128.
 bool gdr_tc_shape(int dk, int dv, IoType io);
 bool gdr_tc_available();
+// The chunk whose tiles prep never loads, for tests (-1: none).  Process-wide, as WaitHooks.
+void set_gdr_prep_hook(int skip_chunk);
 size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward);
 cudaError_t launch_gdr_forward_tc(const GdrArgs &a, cudaStream_t s);
 cudaError_t launch_gdr_backward_tc(const GdrArgs &a, cudaStream_t s);

@@ -8,6 +8,7 @@
 //   tokens of 96 heads), 75 us for 4224; shared memory bounds it (its data pipe is busy 78 % of the time).
 // walk, a block per sequence and value head: gdr_tc_walk.cuh.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "gdr_tc_walk.cuh"
@@ -299,6 +300,9 @@ size_t gdr_tc_workspace(int N, int T, int Hk, int Hv, bool backward)
     return items * (IT_BYTES + (backward ? 6 * TILE : 0)) + carry + 4 * (size_t)N;
 }
 
+static std::atomic<int> g_skip_prep_chunk{-1};
+void set_gdr_prep_hook(int skip_chunk) { g_skip_prep_chunk.store(skip_chunk); }
+
 void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
 {
     const WaitHooks hk = wait_hooks();
@@ -324,8 +328,8 @@ void gdr_tc_plan(const GdrArgs &a, bool backward, TcP &p)
     }
     if (a.T > 0 && a.cu && a.N > 1) p.order = (int *)at;
     p.wait_ns = hk.wait_ns;
-    p.skip_load_chunk = std::max(hk.skip_load_chunk, -1);
-    p.skip_prep_chunk = hk.skip_load_chunk <= -2 ? -2 - hk.skip_load_chunk : -1;
+    p.skip_load_chunk = hk.skip_load_chunk;
+    p.skip_prep_chunk = g_skip_prep_chunk.load();
 }
 
 cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, CUtensorMap &mv, cudaStream_t s)

@@ -54,6 +54,9 @@ KDA_DEVICE void mbar_arrive(uint64_t *bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// named_bar_sync for warps that need not wait
+KDA_DEVICE void named_bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
 // x -> bf16 hi and lo, two values a word
 KDA_DEVICE void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
 {

@@ -87,13 +87,19 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                     tma_load_4d(s + ST_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row, 0, &full[st]);
                     tma_load_4d(s + ST_V + cb * (TILE / 2), &tm_do, cb * 64, hv, row, 0, &full[st]);
                 }
-                bulk_load(s + ST_MM, p.items + ((item0 + ch) * a.Hv + hv) * IT_BYTES, IT_WALK, &full[st]);
+                const uint8_t *item = p.items + ((item0 + ch) * a.Hv + hv) * IT_BYTES;
+                bulk_load(s + ST_MM, item, IT_WALK, &full[st]);
                 issued = i + 1;
+                // prep has given up on this chunk: so does the block (found here, where nothing waits for the answer: as a
+                // branch of the chain's or the MMAs' warps it took 1 to 2 % of a walk)
+                if (((const float *)(item + IT_GATES))[GA_GAM + CH - 1] < 0.0f) *abort_flag = 1;
             }
             for (int seen = issued > STAGES ? issued - STAGES : 0; seen < issued && *abort_flag; ++seen)
                 if (seen != p.skip_load_chunk)
                     mbar_wait_timed(&full[seen % STAGES], (uint32_t)((seen / STAGES) & 1), DRAIN_NS);
         }
+        __syncwarp();
+        if (a.ds0) named_bar_arrive(1, 544);             // every chunk's mark has been looked at
     } else if (warp == 17) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t id_y = idesc_bf16(128, 64, false, false), id_h = idesc_bf16(128, 64, false, true),
@@ -224,11 +230,6 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (!(ok = wait_full(i))) break;
             {                                        // dS decayed, in the shadow of the product
                 const float gC = gates[GA_GAM + CH - 1];
-                if (gC < 0.0f) {                     // prep has given up on this chunk: so does the block
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
                 float *x = (float *)S;
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], gC, gC);
@@ -304,7 +305,8 @@ KDA_DEVICE void walk_reverse(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
         if (ok && nchunks > 0) arrive(b_s);          // the last H's tile is written
         if (a.ds0) {
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
-            if (ok) {
+            named_bar_sync(1, 544);                  // all warps or none
+            if (ok && !*abort_flag) {
                 uint32_t x[32];
                 tmem_ld32(at + TM_S + r0, x);
                 tmem_wait_ld();

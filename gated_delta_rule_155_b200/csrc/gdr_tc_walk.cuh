@@ -100,14 +100,20 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
                     tma_load_4d(s + ST_KQ + cb * TILE + TILE / 2, &tm_q, cb * 64, hk, row, 0, &full[st]);
                     tma_load_4d(s + ST_V + cb * (TILE / 2), &tm_v, cb * 64, hv, row, 0, &full[st]);
                 }
-                bulk_load(s + ST_MM, p.items + ((item0 + ch) * a.Hv + hv) * IT_BYTES, IT_WALK, &full[st]);
+                const uint8_t *item = p.items + ((item0 + ch) * a.Hv + hv) * IT_BYTES;
+                bulk_load(s + ST_MM, item, IT_WALK, &full[st]);
                 issued = ch + 1;
+                // prep has given up on this chunk: so does the block (found here, where nothing waits for the answer: as a
+                // branch of the chain's or the MMAs' warps it took 1 to 2 % of a walk)
+                if (((const float *)(item + IT_GATES))[GA_GAM + CH - 1] < 0.0f) *abort_flag = 1;
             }
             // after an abort the loads of the last stages may still be on their way
             for (int seen = issued > STAGES ? issued - STAGES : 0; seen < issued && *abort_flag; ++seen)
                 if (first + seen != p.skip_load_chunk)
                     mbar_wait_timed(&full[seen % STAGES], (uint32_t)((seen / STAGES) & 1), DRAIN_NS);
         }
+        __syncwarp();
+        if (!KEEP && a.sT) named_bar_arrive(1, 544);     // every chunk's mark has been looked at
     } else if (warp == 17) {
         // ------------------------------------------------------------ MMAs
         constexpr int NX = KEEP ? 64 : 128;      // X (and Q S), U (and P U)
@@ -229,11 +235,6 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
             if (!(ok = wait_full(ch))) break;
             {                                        // the state decayed, in the shadow of the product
                 const float gC = gates[GA_GAM + CH - 1];
-                if (gC < 0.0f) {                     // prep has given up on this chunk: so does the block
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
                 float *x = (float *)S;
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], gC, gC);
@@ -327,7 +328,7 @@ KDA_DEVICE void walk_forward(const CUtensorMap &tm_q, const CUtensorMap &tm_k, c
         if (!KEEP && a.sT) {
             if (nchunks > 0 && ok && (ok = wait_all(m_s, nchunks - 1))) tc_fence_after();
             const int page = page_of(a.sT_index, n, a.pages, a.err);
-            named_bar_sync(1, 512);                  // all warps or none: a state is kept whole
+            named_bar_sync(1, 544);                  // all warps or none: a state is kept whole
             bool keep = page >= 0 && ok && begun() && !*abort_flag;
             if (page >= 0 && (a.sT_index || (p.start_index && a.sT == p.start))) {
                 bool clash = false;       // as page_is_free, a warp at a time

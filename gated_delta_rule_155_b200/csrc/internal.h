@@ -108,8 +108,7 @@ bool device_is_sm100();
 bool tensor_maps_available();
 
 // Limit of every bounded mbarrier wait in the tensor-core kernels, and an injected failure
-// (the tile load of chunk `skip_load_chunk` is never issued; -1: none; c <= -2: that of chunk -2 - c in the
-// head-gated rule's prep).  Process-wide, read at
+// (the tile load of chunk `skip_load_chunk` is never issued; -1: none).  Process-wide, read at
 // each launch; set through kda_set_wait_test_hooks.
 struct WaitHooks {
     unsigned long long wait_ns;
