@@ -8,10 +8,11 @@
 // bytes, lane l the dk / 8 consecutive rows from (l / 4) dk / 8 on, so its k and q are vector loads; all
 // the state's loads go out before anything is waited for (8 KB a warp, 128 KB an SM), and the column sums
 // are shuffles.  A block is four warps (64 columns).  Bound by HBM: 250 sequences of 32 heads (1.05 GB)
-// in 162 us, 6.5 TB/s; five drafted tokens of 37 sequences (158 MB) 39 us.  Measured beside it: a block
-// per head with sums over its warps in shared memory, three barriers a token: 276 and 82 us; eight columns
-// a warp (32-byte pieces of rows): 211 and 63 us; three blocks an SM instead of four: 171 and 47 us; the
-// next token's vectors loaded ahead into registers: 170 and 49 us.
+// in 164 us, 6.4 TB/s; five drafted tokens of 37 sequences (158 MB) 43.5 us.
+// When it was chosen, against its own 162 and 39 us in the same measurement: a block per head with sums over
+// its warps in shared memory, three barriers a token: 276 and 82 us; eight columns a warp (32-byte pieces of
+// rows): 211 and 63 us; three blocks an SM instead of four: 171 and 47 us; the next token's vectors loaded
+// ahead into registers: 170 and 49 us.
 #include "gdr.cuh"
 
 namespace kda {

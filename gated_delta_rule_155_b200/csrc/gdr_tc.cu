@@ -2,8 +2,9 @@
 // dk = dv = 128): the forward pass.  The formulas are those of gdr_simt.cu.
 //
 // prep, a block per chunk and value head: [K; Q] K^T in one M = 128 MMA (exact bf16 operands, fp32
-//   sums), the decays, M = (I + A)^-1 and P M in fp32 on CUDA cores; M and P M go to the workspace as
-//   one 128 x 64 operand [M; P M], split into bf16 hi + lo, in the 128-byte swizzle of the MMA's
+//   sums), the decays in fp32, M = (I + A)^-1 by substitution in blocks of 16 (fp32) and split tf32 products of
+//   the blocks (2^-21), P M on tcgen05 from bf16 hi + lo pairs (lo x lo left out: 2^-16); M and P M go to the
+//   workspace as one 128 x 64 operand [M; P M], split into bf16 hi + lo, in the 128-byte swizzle of the MMA's
 //   operand tiles, so the walk brings it in with one bulk copy.  765 us for 49152 chunks and heads (4 x 8192
 //   tokens of 96 heads), 75 us for 4224; shared memory bounds it (its data pipe is busy 78 % of the time).
 // walk, a block per sequence and value head: gdr_tc_walk.cuh.
@@ -23,7 +24,7 @@ using namespace gdr;
 // place; later M's hi, lo) in their place.  36 KB and 128 threads, so that six blocks share an SM: a block is a
 // chain of short steps with a barrier behind each, and what one leaves idle the others use.
 constexpr int LM = 68, PR_T = 128;
-constexpr int SMS = 148;
+constexpr int SMS = 148;                   // of a B200; the plans of launches depend on it, no result does
 constexpr int PR_KQ = 0, PR_P = 0, PR_A = TILE, PR_MHL = PR_A, PR_G = 33 * 1024 + 512;
 constexpr int PR_BYTES = PR_G + 4 * 256 + 64 + 1024;
 static_assert(PR_A + 64 * LM * 4 <= PR_G && PR_MHL + TILE <= PR_G && 2 * TILE <= PR_G && PR_BYTES + 1024 <= 228 * 1024 / 6, "regions");
@@ -276,10 +277,10 @@ bool gdr_tc_available() { return device_is_sm100() && tensor_maps_available(); }
 
 // Walks that leave SMs idle: how many chunks of every sequence (of the mean length) to walk before the others are
 // prepared, which then runs beside them on the idle SMs; that takes about as long as those walks if prep costs
-// 1 / 205 of a walk's step a chunk and head on all SMs (15.6 ns, 3.2 us).  2 x 4096 tokens of 32 heads 238 us (267
-// in one prep and one walk), 32768 of 32 heads 1583 (1764), 4096 of 16 heads 208 (214); fewer than 600 chunks and
-// heads to prepare beside are not worth two launches more (512 tokens of 64 heads, 320: 46 us against 43; 1024 of 32
-// heads, 416: 67 against 66).  The states in between are fp32, so the parts give the bits of the whole.  0: all
+// 1 / 205 of a walk's step a chunk and head on all SMs (15.6 ns, 3.2 us).  2 x 4096 tokens of 32 heads 233 us (263
+// in one prep and one walk), 32768 of 32 heads 1587 (1773), 4096 of 16 heads 210 (216); fewer than 600 chunks and
+// heads to prepare beside are not worth two launches more (512 tokens of 64 heads, 320: 51 us against 44; 1024 of 32
+// heads, 416: 71 against 67).  The states in between are fp32, so the parts give the bits of the whole.  0: all
 // chunks in one prep and one walk.
 static int early_chunks(int N, int T, int Hv)
 {
@@ -352,9 +353,9 @@ cudaError_t launch_gdr_prep_tc(const TcP &p, CUtensorMap &mq, CUtensorMap &mk, C
 // Sequences of one length whose walks fill the SMs more than once but not evenly: the value heads that walk first,
 // few enough to leave SMs idle, so many that the others' walks fill the SMs evenly.  The others' prep runs beside them
 // on the idle SMs (not before, and not on the idle SMs of the last round, when nothing is left to do).  4 x 8192
-// tokens of 96 heads 1833 us (1955 in one prep and one walk), 2 x 4096 of 96 heads 459 (603), 2 x 512 of 96 heads 79
-// (93); where the idle SMs have fewer than 400 chunks' time, two launches more cost what it gives (2 x 128 of 96
-// heads 36.5 against 35.9).  Packed sequences: their lengths are on the device only; launches that decide there which
+// tokens of 96 heads 2000 us (2090 in one prep and one walk), 2 x 4096 of 96 heads 500 (577), 2 x 512 of 96 heads 79
+// (88); where the idle SMs have fewer than 400 chunks' time, two launches more cost what it gives (2 x 128 of 96
+// heads 34.5 against 33.6).  Packed sequences: their lengths are on the device only; launches that decide there which
 // of them has work gave 4 x 8192 packed tokens of 96 heads 1 % and cost lengths that differ 5 %.  0: all heads in
 // one prep and one walk, as in the backward pass, whose longer reverse and shorter forward walks fill the SMs better
 // (2 x 4096 tokens of 48 heads 775 us, 813 in two parts).

@@ -568,7 +568,8 @@ def kda_gdr_forward(q, k, v, g, beta, cu_seqlens=None, initial_state=None, out=N
     without it; value head h uses key head h // (Hv // Hk).  States are fp32 [N, Hv, dk, dv], or pages
     [P, Hv, dk, dv] with an int32 index [N] (initial: -1 starts from zeros; final: -1 is not kept; the
     two buffers have the same number of pages).  ``workspace`` (a uint8 CUDA tensor of
-    kda_gdr_workspace_size bytes) is allocated with torch when not given.  Returns (out, final_state)."""
+    kda_gdr_workspace_size bytes) is allocated with torch when not given.  Rows of no sequence are not written: in an
+    ``out`` that is allocated here they hold anything.  Returns (out, final_state)."""
     if stream is None and workspace is None:
         r = _calls.gdr_forward(q, k, v, g, beta, cu_seqlens, initial_state, out, final_state, initial_index, final_index)
         if r is not None:
@@ -596,7 +597,8 @@ def kda_gdr_backward(q, k, v, g, beta, d_out, cu_seqlens=None, initial_state=Non
                      grads=None, d_initial_state=None, workspace=None, stream=None):
     """Gradients of kda_gdr_forward (dense states).  Returns a dict dq, dk, dv, dg, dbeta (io dtype,
     shaped as the inputs) and d_initial_state (fp32, None unless a buffer is passed).  ``grads`` may
-    hold preallocated outputs; ``workspace`` is allocated with torch when not given."""
+    hold preallocated outputs; ``workspace`` is allocated with torch when not given.  Rows of no sequence are not
+    written: where T_total has some behind the last sequence, give gradients that hold zeros there."""
     if grads is None and stream is None and workspace is None:
         r = _calls.gdr_backward(q, k, v, g, beta, d_out, cu_seqlens, initial_state, d_final_state, d_initial_state)
         if r is not None:

@@ -313,7 +313,9 @@ kda_status_t kda_layer_decode_step(const void *q_raw, const void *k_raw, const v
  * dk = dv = 128 runs on tcgen05 kernels (KDA_ERR_UNSUPPORTED where they cannot run); its
  * products read the state, its corrections and their gradients as bf16 hi + lo pairs with
  * fp32 sums, so states and out carry about 2^-16 relative error before out's own rounding.
- * The other shapes run exact fp32 CUDA-core kernels.  A g below -128 (-inf among them) acts as
+ * The other shapes run to fp32 accuracy: products as split tf32 on the tensor cores (a factor within
+ * 2^-23, the product of the low parts, at most 2^-24, left out; within 2^-21 in the chunk's inverse),
+ * summed in fp32.  A g below -128 (-inf among them) acts as
  * a full reset, which exp(g) = 0 is; NaN inputs reach their own head's values and no other's.
  * A buffer that is written shares no memory with another argument unless it says so here (the
  * same pointer is refused: KDA_ERR_INVALID_ARG).
@@ -362,6 +364,7 @@ kda_status_t kda_gdr_forward(const void *q, const void *k, const void *v, const 
  *   d_q, d_k        [T_total, Hk, dk] io dtype (written; summed over the value heads of the group)
  *   d_v             [T_total, Hv, dv] io dtype (written)     d_g, d_beta  [T_total, Hv] io dtype (written)
  *   d_initial_state [N, Hv, dk, dv] fp32 (written) or NULL; may be d_final_state
+ * Rows of no sequence (behind the last, where T_total is larger than its end) are left as they were.
  *   workspace       kda_gdr_workspace_size(.., 1) bytes, 256-byte aligned
  * No atomics: the same inputs give the same bits.
  */
