@@ -79,6 +79,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     src, calls = os.path.join(CSRC, "calls.cpp"), calls_path()
     if not force and _newer(calls, [src, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]):
         return calls
+    if os.path.exists(calls):
+        os.remove(calls)          # it does not fit these sources: where the build fails, none is better than it
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))

@@ -132,6 +132,12 @@ def test_the_library_is_built_without_a_host_compiler(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "PKG", str(tmp_path))
     with pytest.warns(RuntimeWarning, match="_calls"):
         assert build.build() == build.LIB
+    old = build.calls_path()                                       # one of older sources is not left to be loaded
+    open(old, "w").close()
+    os.utime(old, (0, 0))
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        assert build.build() == build.LIB
+    assert not os.path.exists(old)
 
 
 def test_short_calls_built_for_another_torch_are_not_loaded(monkeypatch, tmp_path):
