@@ -1321,3 +1321,43 @@ def test_calls_behind_copies_and_other_streams(kda, io, dk, captured):
     near(outs[0], ro, io, io == "f32", "forward")
     near(outs[1], rd, io, io == "f32", "decode")
     near(state, rs, io, io == "f32", "states", stored=False)
+
+
+@pytest.mark.parametrize("io,dk", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("forked", [False, True])
+def test_captured_calls_on_a_given_stream(kda, io, dk, forked):
+    """stream= while it is captured, as the current stream or forked from it: what the calls allocate is the graph's."""
+    N, T, Hk, Hv = 2, 130, 1, 2
+    d = make(N * T, Hk, Hv, dk, dk, io, 125, N)
+    x, s0 = [t.view(N, T, *t.shape[1:]) for t in to(d, *NAMES, "dO")], d["s0"].cuda()
+    out, kept = [torch.zeros_like(x[2]) for _ in range(2)], torch.zeros_like(x[0])
+    refs, ids = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    cache, kids = torch.ones(1, 3, 8, device="cuda"), torch.full_like(ids, 9)
+    graph, main, side = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        s = side if forked else main
+        s.wait_stream(main)
+        a, _ = kda.kda_gdr_forward(*x[:5], None, s0, stream=s)
+        gr = kda.kda_gdr_backward(*x, None, s0, stream=s)
+        k = kda.kda_pages_fork(cache, refs, ids, stream=s)
+        main.wait_stream(s)
+        out[0].copy_(a)
+        kept.copy_(gr["dq"])
+        kids.copy_(k)
+        del a, gr, k                                       # read on one stream, made on the other
+        junk = [torch.full_like(x[2], 7.0) for _ in range(8)]
+        s.wait_stream(main)
+        b, _ = kda.kda_gdr_forward(*x[:5], None, s0, stream=s)
+        main.wait_stream(s)
+        out[1].copy_(b)
+    want = kda.kda_gdr_forward(*x[:5], None, s0)[0]
+    dq = kda.kda_gdr_backward(*x, None, s0)["dq"]
+    for _ in range(2):
+        for t in (*out, kept, refs):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want) and torch.equal(out[1], want) and torch.equal(kept, dq)
+        assert kids.tolist() == [0, 1] and bool((junk[0] == 7.0).all())
+    kda.kda_check_device_error()
